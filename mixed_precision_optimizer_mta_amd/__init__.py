@@ -1,6 +1,8 @@
 """Fused mixed-precision gradient clip + multi-tensor AdamW for MI355X.
 
-The work runs in libmta.so (HIP, gfx950) behind the C ABI of include/mta.h.
+The work runs in libmta.so (HIP, gfx950) behind the C ABI of include/mta.h
+(the optimizer step) and include/mta_ops.h (what makes its gradients: 8-bit
+activation checkpoints with their backward, and a clipped policy loss).
 ``_binding`` mirrors that ABI name for name; ``MtaList`` marshals PyTorch
 tensors and the current HIP stream into it.  Nothing here computes any part
 of the step, and nothing falls back to another implementation: if
@@ -19,3 +21,10 @@ from ._binding import (  # noqa: F401
 from .torch_list import (AmpState, GradClipper, MtaList,  # noqa: F401
                          clip_norm_joint)
 from .optim import MtaOptimizer  # noqa: F401
+from ._binding import OPS_EXPORTS, mta_ops_version  # noqa: F401
+from .checkpoint import (Checkpoint8, checkpointed_act,  # noqa: F401
+                         checkpointed_linear, ckpt_act, ckpt_act_backward,
+                         ckpt_pack, ckpt_unpack, ckpt_wgrad)
+from .policy import (PolicyLoss, policy_loss,  # noqa: F401
+                     policy_loss_backward, policy_loss_forward,
+                     policy_loss_grad)

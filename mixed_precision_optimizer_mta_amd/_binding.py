@@ -1,4 +1,5 @@
-"""ctypes binding of libmta.so: the C ABI of include/mta.h, same names.
+"""ctypes binding of libmta.so: the C ABI of include/mta.h and
+include/mta_ops.h, same names.
 
 Argument marshalling only: every step of the optimizer runs in the HIP
 library.  If the library is not built, loading fails loudly; there is no
@@ -23,8 +24,14 @@ STATUS_NAMES = {0: "MTA_OK", -1: "MTA_EINVAL", -2: "MTA_EALIGN",
                 -3: "MTA_EDTYPE", -4: "MTA_ENOMEM", -5: "MTA_EHIP",
                 -6: "MTA_ESTATE"}
 
+MTA_ACT_NONE = 0
+ACTIVATIONS = {"relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+MTA_CKPT_BLOCK = 32
+
 # MTA_ABI_VERSION of include/mta.h that these structs mirror
 ABI_VERSION = 5
+# MTA_OPS_VERSION of include/mta_ops.h
+OPS_VERSION = 1
 
 # every symbol include/mta.h declares
 EXPORTS = ("mta_list_create", "mta_list_destroy", "mta_scale",
@@ -36,6 +43,12 @@ EXPORTS = ("mta_list_create", "mta_list_destroy", "mta_scale",
            "mta_clip_norm_joint", "mta_amp_clip_norm_joint",
            "mta_list_set_no_decay", "mta_scale_device",
            "mta_clip_norm_noalloc")
+
+# every symbol include/mta_ops.h declares
+OPS_EXPORTS = ("mta_ckpt_pack", "mta_ckpt_unpack", "mta_ckpt_act_backward",
+               "mta_ckpt_wgrad", "mta_ckpt_wgrad_workspace",
+               "mta_policy_loss", "mta_policy_loss_backward",
+               "mta_policy_loss_workspace", "mta_ops_version")
 
 
 class mta_tensor(ctypes.Structure):
@@ -75,6 +88,42 @@ class mta_list_info_t(ctypes.Structure):
                 ("state_buffers", ctypes.c_int32),
                 ("weight_copy_type", ctypes.c_int32),
                 ("norm_kept_tiles", ctypes.c_int32)]
+
+
+class mta_ckpt_tensor(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("y", ctypes.c_void_p),
+                ("q", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64),
+                ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64)]
+
+
+class mta_ckpt_wgrad_args(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p),
+                ("dy", ctypes.c_void_p), ("dw", ctypes.c_void_p),
+                ("db", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_int64),
+                ("tokens", ctypes.c_int64), ("fin", ctypes.c_int64),
+                ("fout", ctypes.c_int64), ("lddy", ctypes.c_int64),
+                ("lddw", ctypes.c_int64), ("type", ctypes.c_int32),
+                ("gtype", ctypes.c_int32), ("accumulate", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
+
+
+class mta_policy_args(ctypes.Structure):
+    _fields_ = [("logits", ctypes.c_void_p), ("actions", ctypes.c_void_p),
+                ("old_logp", ctypes.c_void_p),
+                ("advantages", ctypes.c_void_p),
+                ("weights", ctypes.c_void_p), ("ref_logp", ctypes.c_void_p),
+                ("d_grad_scale", ctypes.c_void_p),
+                ("dlogits", ctypes.c_void_p), ("saved", ctypes.c_void_p),
+                ("logp", ctypes.c_void_p), ("stats", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_int64),
+                ("rows", ctypes.c_int64), ("vocab", ctypes.c_int64),
+                ("ld", ctypes.c_int64), ("ldd", ctypes.c_int64),
+                ("clip_low", ctypes.c_double), ("clip_high", ctypes.c_double),
+                ("kl_coef", ctypes.c_double), ("type", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 class MtaError(RuntimeError):
@@ -137,13 +186,29 @@ def lib():
         L.mta_last_error.argtypes = []
         L.mta_last_error.restype = ctypes.c_char_p
         L.mta_abi_version.argtypes = []
-        for name in EXPORTS:
+        tensors = ctypes.POINTER(mta_ckpt_tensor)
+        L.mta_ckpt_pack.argtypes = [tensors, i64, c_int, c_int, vp]
+        L.mta_ckpt_unpack.argtypes = [tensors, i64, c_int, vp]
+        L.mta_ckpt_act_backward.argtypes = [tensors, i64, c_int, c_int, vp]
+        L.mta_ckpt_wgrad.argtypes = [ctypes.POINTER(mta_ckpt_wgrad_args), vp]
+        L.mta_ckpt_wgrad_workspace.argtypes = [i64, i64, i64, c_int,
+                                               ctypes.c_int32,
+                                               ctypes.POINTER(i64)]
+        for fn in (L.mta_policy_loss, L.mta_policy_loss_backward):
+            fn.argtypes = [ctypes.POINTER(mta_policy_args), vp]
+        L.mta_policy_loss_workspace.argtypes = [i64, ctypes.POINTER(i64)]
+        L.mta_ops_version.argtypes = []
+        for name in EXPORTS + OPS_EXPORTS:
             if name != "mta_last_error":
                 getattr(L, name).restype = ctypes.c_int
         if L.mta_abi_version() != ABI_VERSION:
             raise RuntimeError(
                 f"{LIB_PATH} has ABI {L.mta_abi_version()}, this binding "
                 f"speaks {ABI_VERSION}: rebuild the library")
+        if L.mta_ops_version() != OPS_VERSION:
+            raise RuntimeError(
+                f"{LIB_PATH} has operators version {L.mta_ops_version()}, "
+                f"this binding speaks {OPS_VERSION}: rebuild the library")
         _lib = L
     return _lib
 
@@ -340,3 +405,63 @@ def mta_amp_step(handle, opt, d_amp, d_coef, stream=0):
     o = _opt(opt)
     _check(lib().mta_amp_step(handle, ctypes.byref(o), d_amp, d_coef, stream),
            "mta_amp_step")
+
+
+def _ckpt_table(tensors):
+    arr = (mta_ckpt_tensor * max(1, len(tensors)))()
+    for i, t in enumerate(tensors):
+        arr[i] = t
+    return arr
+
+
+def mta_ckpt_pack(tensors, type, act, stream=0):
+    """tensors: sequence of (x, y, q, scale, rows, cols, ldx, ldy), pointers
+    as ints (y None without an activation)."""
+    _check(lib().mta_ckpt_pack(_ckpt_table(tensors), len(tensors), type, act,
+                               stream), "mta_ckpt_pack")
+
+
+def mta_ckpt_unpack(tensors, type, stream=0):
+    _check(lib().mta_ckpt_unpack(_ckpt_table(tensors), len(tensors), type,
+                                 stream), "mta_ckpt_unpack")
+
+
+def mta_ckpt_act_backward(tensors, type, act, stream=0):
+    _check(lib().mta_ckpt_act_backward(_ckpt_table(tensors), len(tensors),
+                                       type, act, stream),
+           "mta_ckpt_act_backward")
+
+
+def mta_ckpt_wgrad_workspace(tokens, fin, fout, type, cus=0):
+    out = ctypes.c_int64()
+    _check(lib().mta_ckpt_wgrad_workspace(tokens, fin, fout, type, cus,
+                                          ctypes.byref(out)),
+           "mta_ckpt_wgrad_workspace")
+    return out.value
+
+
+def mta_ckpt_wgrad(args, stream=0):
+    """args: an mta_ckpt_wgrad_args."""
+    _check(lib().mta_ckpt_wgrad(ctypes.byref(args), stream), "mta_ckpt_wgrad")
+
+
+def mta_policy_loss_workspace(rows):
+    out = ctypes.c_int64()
+    _check(lib().mta_policy_loss_workspace(rows, ctypes.byref(out)),
+           "mta_policy_loss_workspace")
+    return out.value
+
+
+def mta_policy_loss(args, stream=0):
+    """args: an mta_policy_args."""
+    _check(lib().mta_policy_loss(ctypes.byref(args), stream),
+           "mta_policy_loss")
+
+
+def mta_policy_loss_backward(args, stream=0):
+    _check(lib().mta_policy_loss_backward(ctypes.byref(args), stream),
+           "mta_policy_loss_backward")
+
+
+def mta_ops_version():
+    return lib().mta_ops_version()

@@ -12,17 +12,20 @@ Flags that carry meaning:
 """
 import os
 import subprocess
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libmta.so")
-SOURCES = [os.path.join(CSRC, "mta_kernels.hip"),
-           os.path.join(CSRC, "mta_host.cpp")]
+SOURCES = [os.path.join(CSRC, name) for name in
+           ("mta_kernels.hip", "mta_host.cpp", "ckpt_kernels.hip",
+            "wgrad_kernels.hip", "policy_kernels.hip", "ops_host.cpp")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
-FLAGS = ["-O3", "-std=c++17", "-fPIC", "-shared", f"--offload-arch={ARCH}",
+FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}",
          "-ffp-contract=off", "-fhip-fp32-correctly-rounded-divide-sqrt",
          "-fno-gpu-flush-denormals-to-zero",
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
@@ -34,9 +37,7 @@ def build(verbose=False):
     return _compile(LIB, SOURCES, verbose)
 
 
-def _compile(lib, sources, verbose):
-    tmp = lib + ".tmp"
-    cmd = [HIPCC, *FLAGS, "-o", tmp, *sources]
+def _run(cmd, verbose):
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -46,6 +47,19 @@ def _compile(lib, sources, verbose):
         raise RuntimeError(f"hipcc failed ({r.returncode}):\n{err}")
     if verbose and err.strip():
         print(err)
+
+
+def _compile(lib, sources, verbose):
+    """One object a source, compiled side by side, then linked."""
+    tmp = lib + ".tmp"
+    with tempfile.TemporaryDirectory() as d:
+        objs = [os.path.join(d, os.path.basename(s) + ".o") for s in sources]
+        with ThreadPoolExecutor(len(sources)) as pool:
+            list(pool.map(lambda so: _run([HIPCC, *FLAGS, "-c", "-o", so[1],
+                                           so[0]], verbose),
+                          zip(sources, objs)))
+        _run([HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", "-o", tmp,
+              *objs], verbose)
     os.replace(tmp, lib)
     return lib
 

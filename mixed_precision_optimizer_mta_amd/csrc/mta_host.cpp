@@ -714,6 +714,14 @@ int plan_list(const mta_tensor *tensors, int64_t count, int gtype, int mkind,
 
 }  // namespace
 
+int mta::report(int code, const char *msg) {
+  return code == MTA_OK ? ok() : fail(code, "%s", msg);
+}
+
+int mta::report_launch(hipError_t e, hipStream_t stream, const char *what) {
+  return after_launch(e, stream, what);
+}
+
 extern "C" {
 
 int mta_abi_version(void) { return MTA_ABI_VERSION; }

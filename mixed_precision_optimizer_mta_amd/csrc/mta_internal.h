@@ -155,6 +155,13 @@ hipError_t launch_amp_update(mta_amp_state *state, double growth,
                              double backoff, int32_t interval,
                              hipStream_t stream);
 
+// The calling thread's last error (mta_last_error), for the library's other
+// host files: records `msg` and returns `code`; with code MTA_OK clears it.
+int report(int code, const char *msg);
+// After a call's launches: their status reported under the call's name, and
+// with MTA_DEBUG_SYNC the wait for them.
+int report_launch(hipError_t e, hipStream_t stream, const char *what);
+
 // The allocation-free norm's scratch: a file-scope device array in
 // mta_kernels.hip of this many bytes (its ticket region, its partial
 // slots, then its gradient tile table).

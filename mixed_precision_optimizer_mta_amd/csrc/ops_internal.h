@@ -1,0 +1,92 @@
+// ops_internal.h -- types shared by the host side and the gfx950 kernels of
+// the operators of include/mta_ops.h.  Not part of the public C ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/mta_ops.h"
+#include "mta_internal.h"
+
+namespace mta {
+
+// ---- 8-bit checkpoints --------------------------------------------------
+
+constexpr int kCkptThreads = 256;
+constexpr int kCkptUnit = 8;    // elements a lane handles at a time
+constexpr int kCkptUnroll = 4;  // units a lane has in flight
+constexpr int kCkptChunk = kCkptThreads * kCkptUnroll;  // units a workgroup
+                                                        // handles at a time
+constexpr int kCkptTensors = 32;  // tensors in one launch (they travel in the
+                                  // kernel's arguments, 4 KiB at most)
+
+// One tensor of a launch.  Its work is `units` runs of 8 columns, row by row
+// and `row_units` to a row (a multiple of 4, so that the four lanes of a
+// scale's block never part).  A tensor whose rows follow each other without
+// gaps and are whole blocks long is one row (flat).
+struct CkptItem {
+  const void *x;
+  void *y;
+  uint8_t *q;
+  uint8_t *scale;
+  int64_t ldx, ldy;
+  uint64_t units;
+  uint32_t cols;
+  uint32_t row_units;  // 0: flat
+};
+
+struct CkptList {
+  CkptItem item[kCkptTensors];
+  uint32_t first[kCkptTensors + 1];  // first workgroup of each tensor; the
+                                     // last entry is the grid
+  uint32_t count;
+};
+static_assert(sizeof(CkptList) <= 4000, "kernel argument space");
+
+enum CkptMode { kCkptPack = 0, kCkptUnpack = 1, kCkptBackward = 2 };
+
+hipError_t launch_ckpt(int mode, int type, int act, const CkptList &list,
+                       hipStream_t stream);
+
+// ---- weight gradient from a checkpoint ----------------------------------
+
+struct WgradShape {
+  int tile_o, tile_i;  // output tile of a workgroup
+  int step;            // tokens of one pass through LDS
+  int terms;           // bfloat16 values a dy is taken as the sum of
+  int64_t tiles;       // output tiles
+  int splits;          // parts the tokens are cut into
+  int64_t per_split;   // tokens of a part, a multiple of `step`
+};
+
+WgradShape wgrad_shape(int64_t tokens, int64_t fin, int64_t fout, int type,
+                       int cus);
+
+struct WgradArgs {
+  const uint8_t *q, *scale;
+  const void *dy;
+  void *dw, *db;
+  float *part;     // [splits][fout * fin] when splits > 1
+  float *part_db;  // [splits][fout] when splits > 1
+  int64_t tokens, fin, fout, lddy, lddw;
+  int64_t ldq;
+  int type, gtype, accumulate;
+};
+
+hipError_t launch_wgrad(const WgradArgs &args, const WgradShape &shape,
+                        hipStream_t stream);
+
+// ---- policy loss --------------------------------------------------------
+
+static_assert(sizeof(mta_policy_row) == 16, "saved row layout");
+
+// Workgroups of a policy loss launch leave one set of partial sums each.
+constexpr int kPolicyGrid = 2048;
+constexpr int kPolicySums = 3;
+
+hipError_t launch_policy(const mta_policy_args &args, hipStream_t stream);
+hipError_t launch_policy_backward(const mta_policy_args &args,
+                                  hipStream_t stream);
+
+}  // namespace mta

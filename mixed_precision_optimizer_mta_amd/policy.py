@@ -1,0 +1,155 @@
+"""The clipped policy loss with a KL term, from the logits, over PyTorch
+tensors: mta_policy_loss and mta_policy_loss_backward of include/mta_ops.h.
+
+``policy_loss_grad`` is the loss and its gradient in one pass over the logits,
+the gradient multiplied by a factor in device memory: the ``loss_scale`` of a
+loss-scaled MtaOptimizer, so that a float16 gradient is scaled before it is
+rounded and the optimizer's step divides the scale out again.
+``policy_loss_forward`` and ``policy_loss_backward`` are the two halves, and
+``policy_loss`` is both as an autograd function.
+"""
+from collections import namedtuple
+
+import torch
+
+from . import _binding as B
+from .checkpoint import _as_rows, _check_type, _on, _same_device
+from .torch_list import _G
+
+#: stats: float32 [3] on the device, (loss, sum w kl, sum of the weights of
+#: clipped rows); logp: float32, one a row; saved: for policy_loss_backward;
+#: dlogits: the gradient, or None
+PolicyLoss = namedtuple("PolicyLoss", "stats logp saved dlogits")
+
+
+def _vector(t, dtype, n, dev, what):
+    if t is None:
+        return None
+    if t.dtype != dtype or t.numel() != n or t.device != dev or \
+            not t.is_contiguous():
+        raise ValueError(f"{what} is a contiguous {dtype} tensor of {n} "
+                         "values on the logits' device")
+    return t.data_ptr()
+
+
+def _scalar(t, dev):
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.numel() != 1 or t.device != dev:
+        raise ValueError("grad_scale is a one-element float32 tensor on the "
+                         "logits' device")
+    return t.data_ptr()
+
+
+def _run(logits, actions, old_logp, advantages, weights, ref_logp, clip_low,
+         clip_high, kl_coef, grad, save, grad_scale, out):
+    _check_type(logits, "logits")
+    rows, vocab, ld = _as_rows(logits, "logits")
+    if vocab < 1:
+        raise ValueError("logits needs a last dimension of at least 1")
+    dev = logits.device
+    f32 = torch.float32
+    dlogits, ldd = None, vocab
+    if grad:
+        if out is None:
+            dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+        else:
+            if out.shape != logits.shape or out.dtype != logits.dtype:
+                raise ValueError("out has the logits' shape and dtype")
+            _same_device(dev, out)
+            dlogits, ldd = out, _as_rows(out, "out")[2]
+    # one allocation: partial sums, what is saved, logp, stats
+    need = B.mta_policy_loss_workspace(rows)
+    kept = 16 * rows if save else 0
+    buf = torch.empty(need + kept + 4 * rows + 16, dtype=torch.uint8,
+                      device=dev)
+    base = buf.data_ptr()
+    logp = buf[need + kept:need + kept + 4 * rows].view(f32)
+    stats = buf[need + kept + 4 * rows:][:12].view(f32)
+    args = B.mta_policy_args(
+        logits.data_ptr(), _vector(actions, torch.int64, rows, dev, "actions"),
+        _vector(old_logp, f32, rows, dev, "old_logp"),
+        _vector(advantages, f32, rows, dev, "advantages"),
+        _vector(weights, f32, rows, dev, "weights"),
+        _vector(ref_logp, f32, rows, dev, "ref_logp"),
+        _scalar(grad_scale, dev),
+        None if dlogits is None else dlogits.data_ptr(),
+        base + need if save else None, base + need + kept,
+        base + need + kept + 4 * rows, base, need, rows, vocab, ld, ldd,
+        clip_low, clip_high, kl_coef, _G[logits.dtype], 0)
+    with _on(dev) as stream:
+        B.mta_policy_loss(args, stream)
+    saved = buf[need:need + kept] if save else None
+    return PolicyLoss(stats, logp.view(logits.shape[:-1]), saved, dlogits)
+
+
+def policy_loss_grad(logits, actions, old_logp, advantages, weights=None,
+                     ref_logp=None, clip_low=0.2, clip_high=0.2, kl_coef=0.0,
+                     grad_scale=None, out=None):
+    """The loss over the rows of logits [..., vocab] and its gradient in one
+    pass: a PolicyLoss whose dlogits is *grad_scale times the gradient, in the
+    logits' dtype, in `out` (which may be the logits themselves) or a new
+    tensor.
+
+    actions: int64, one a row; old_logp, advantages: float32, one a row;
+    weights: float32 (default 1 / rows each; a row of weight 0 is not read and
+    has gradient 0); ref_logp: float32, needed for kl_coef > 0."""
+    return _run(logits, actions, old_logp, advantages, weights, ref_logp,
+                clip_low, clip_high, kl_coef, True, False, grad_scale, out)
+
+
+def policy_loss_forward(logits, actions, old_logp, advantages, weights=None,
+                        ref_logp=None, clip_low=0.2, clip_high=0.2,
+                        kl_coef=0.0):
+    """The loss alone; ``saved`` serves policy_loss_backward."""
+    return _run(logits, actions, old_logp, advantages, weights, ref_logp,
+                clip_low, clip_high, kl_coef, False, True, None, None)
+
+
+def policy_loss_backward(logits, actions, saved, grad_scale=None, out=None):
+    """*grad_scale times the loss's gradient with respect to the logits, from
+    what policy_loss_forward saved for the same logits and actions."""
+    _check_type(logits, "logits")
+    rows, vocab, ld = _as_rows(logits, "logits")
+    dev = logits.device
+    if saved.numel() != 16 * rows or saved.device != dev:
+        raise ValueError("saved is that of a forward over the same rows")
+    if out is None:
+        out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+    elif out.shape != logits.shape or out.dtype != logits.dtype:
+        raise ValueError("out has the logits' shape and dtype")
+    _same_device(dev, out)
+    args = B.mta_policy_args(
+        logits=logits.data_ptr(),
+        actions=_vector(actions, torch.int64, rows, dev, "actions"),
+        d_grad_scale=_scalar(grad_scale, dev), dlogits=out.data_ptr(),
+        saved=saved.data_ptr(), rows=rows, vocab=vocab, ld=ld,
+        ldd=_as_rows(out, "out")[2], type=_G[logits.dtype])
+    with _on(dev) as stream:
+        B.mta_policy_loss_backward(args, stream)
+    return out
+
+
+class _Policy(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, actions, *args):
+        r = policy_loss_forward(logits, actions, *args)
+        ctx.save_for_backward(logits, actions, r.saved)
+        ctx.mark_non_differentiable(r.logp)
+        return r.stats[0], r.logp
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dloss, _):
+        logits, actions, saved = ctx.saved_tensors
+        d = policy_loss_backward(logits, actions, saved,
+                                 grad_scale=dloss.float().reshape(1))
+        return (d,) + (None,) * 8
+
+
+def policy_loss(logits, actions, old_logp, advantages, weights=None,
+                ref_logp=None, clip_low=0.2, clip_high=0.2, kl_coef=0.0):
+    """(loss, logp) with the loss differentiable with respect to the logits;
+    the gradient of a scaled loss is scaled before it is rounded."""
+    return _Policy.apply(logits, actions, old_logp, advantages, weights,
+                         ref_logp, clip_low, clip_high, kl_coef)

@@ -1,0 +1,538 @@
+"""8-bit activation checkpoints on the GPU against their float64 definition:
+pack and unpack bit for bit, the activations and the weight gradient within
+bounds counted from their roundings."""
+import numpy as np
+import pytest
+import torch
+
+import mixed_precision_optimizer_mta_amd as M
+from mixed_precision_optimizer_mta_amd import _binding as B
+import ops_oracle as R
+
+pytestmark = pytest.mark.gpu
+ACTS = ["relu", "silu", "gelu", "gelu_tanh"]
+TYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def activations(shape, dtype, seed=0, pad=0):
+    """Normal values with loud channels, in rows padded by `pad`."""
+    g = gen(seed)
+    x = torch.randn(*shape[:-1], shape[-1] + pad, generator=g)
+    x *= torch.where(torch.rand(shape[-1] + pad, generator=g) < 0.1, 30.0, 1.0)
+    return x.to(dtype).cuda()[..., :shape[-1]]
+
+
+def codes(ck):
+    rows, nb = ck._layout(ck.shape)
+    return (ck.q.cpu().numpy().reshape(rows, nb * 32),
+            ck.scale.cpu().numpy().reshape(rows, nb))
+
+
+def check_pack(x, ck):
+    q, s, kept = R.pack(x)
+    gq, gs = codes(ck)
+    assert np.array_equal(gs, s)
+    # a NaN keeps no sign
+    assert np.array_equal(np.where(gq == 255, 127, gq), q)
+    for dt in R.DTYPES.values():
+        y = ck.unpack(dt)
+        assert y.shape == x.shape and y.dtype == dt
+        want = torch.from_numpy(kept)
+        if dt == torch.float16:
+            want = want.clamp(-65504, 65504)
+        assert np.array_equal(R.to64(y).reshape(kept.shape),
+                              want.to(dt).double().numpy(), equal_nan=True)
+
+
+SHAPES = [(1, 1), (1, 31), (3, 32), (5, 33), (7, 64), (129, 97), (33, 1600),
+          (2, 8197), (2, 3, 5, 40), (70, 7), (1030, 9), (1, 768), (768,)]
+
+
+@pytest.mark.parametrize("dtype", list(R.DTYPES))
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_pack_is_the_definition(shape, dtype):
+    x = activations(shape, R.DTYPES[dtype])
+    check_pack(x, M.ckpt_pack(x))
+
+
+@pytest.mark.parametrize("dtype", list(R.DTYPES))
+@pytest.mark.parametrize("pad", [1, 3, 8])
+def test_pack_of_padded_rows_at_odd_addresses(dtype, pad):
+    for cols in (1, 40, 65, 96):
+        x = activations((37, cols + 1), R.DTYPES[dtype], cols, pad)[:, 1:]
+        check_pack(x, M.ckpt_pack(x))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_every_16_bit_pattern(dtype):
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16)
+    v = bits.view(R.DTYPES[dtype])
+    # alone in its block, and beside a value that sets the scale
+    alone = v.reshape(-1, 1).cuda()
+    check_pack(alone, M.ckpt_pack(alone))
+    for anchor in (448.0, 449.0, 3.5e-3, 2.0 ** -16):
+        x = torch.full((65536 // 16, 32), anchor, dtype=v.dtype)
+        x[:, :16] = v.reshape(-1, 16)
+        check_pack(x.cuda(), M.ckpt_pack(x.cuda()))
+
+
+def test_special_float32_values():
+    big = torch.finfo(torch.float32).max
+    rows = [[0.0] * 32, [-0.0] + [0.0] * 31, [2.0 ** -149] * 32,
+            [2.0 ** -126, 2.0 ** -130] * 16, [big, 1.0] * 16,
+            [float("nan")] * 32, [float("inf"), 1.0, -float("inf"), 3.0] * 8,
+            [float("nan"), 448.0, 1e-3, -0.0] * 8, [448.0 * 2.0 ** -117] * 32,
+            [np.nextafter(np.float32(448), np.float32(449))] * 32,
+            [464.0, 1.0] * 16, [1.875 * 2.0 ** 127, 2.0 ** 100] * 16]
+    for k in range(-40, 40, 7):          # ties of every code at a scale
+        mid = (R.E4M3[:126] + R.E4M3[1:127]) / 2 * 2.0 ** k
+        full = np.concatenate([mid, -mid])
+        for i in range(0, 252, 31):
+            r = np.full(32, 448 * 2.0 ** k)
+            r[:len(full[i:i + 31])] = full[i:i + 31]
+            rows.append(list(r))
+    x = torch.tensor(np.array(rows), dtype=torch.float32).cuda()
+    check_pack(x, M.ckpt_pack(x))
+
+
+def test_lists_take_one_call_and_skip_empty_tensors():
+    g = np.random.default_rng(3)
+    xs = [activations((int(g.integers(0, 40)), int(g.integers(1, 200))),
+                      torch.bfloat16, i) for i in range(70)]
+    for x, ck in zip(xs, M.ckpt_pack(xs)):
+        if x.numel():
+            check_pack(x, ck)
+    back = M.ckpt_unpack(M.ckpt_pack(xs))
+    assert [b.shape for b in back] == [x.shape for x in xs]
+    for shape in ((0, 5), (3, 0), (0,)):
+        e = torch.zeros(shape, device="cuda")
+        assert M.ckpt_pack(e).unpack().shape == e.shape
+
+
+def test_nothing_outside_the_buffers_is_written():
+    rows, cols = 9, 45
+    x = activations((rows, cols), torch.bfloat16)
+    q = torch.full((16 + rows * 64 + 16,), 0x55, dtype=torch.uint8).cuda()
+    s = torch.full((16 + rows * 2 + 16,), 0x55, dtype=torch.uint8).cuda()
+    y = torch.full((rows, 50), 7.0, dtype=torch.bfloat16).cuda()
+    e = (x.data_ptr(), y[:, 3:].data_ptr(), q.data_ptr() + 16,
+         s.data_ptr() + 16, rows, cols, cols, 50)
+    B.mta_ckpt_pack([e], 1, 1)
+    torch.cuda.synchronize()
+    assert (q[:16] == 0x55).all() and (q[-16:] == 0x55).all()
+    assert (s[:16] == 0x55).all() and (s[-16:] == 0x55).all()
+    assert (y[:, :3] == 7).all() and (y[:, 3 + cols:] == 7).all()
+    oq, osc, _ = R.pack(x)
+    assert np.array_equal(q[16:-16].cpu().numpy().reshape(rows, 64), oq)
+    assert np.array_equal(s[16:-16].cpu().numpy().reshape(rows, 2), osc)
+    assert torch.equal(y[:, 3:3 + cols], x.clamp_min(0))
+
+
+# Activation values and slopes are float32 expressions of at most a dozen
+# operations (each half a step, 2^-24 relative), a 2^x and a reciprocal of the
+# hardware's (a step each, 2^-23), whose error in the exponent, |u| 2^-23, is
+# weighted with x u' s (1 - s): below 3 for all four.  16 * 2^-23 = 2^-19 of
+# (1 + |x|) bounds their sum.  The result is rounded once more.
+ACT = 2.0 ** -19
+
+
+def act_inputs(dtype):
+    # to every magnitude that its squares and cubes leave finite, and beyond
+    x = torch.cat([torch.linspace(-12, 12, 3001),
+                   torch.tensor([0.0, -0.0, 1e-30, -1e-30, 60.0, -60.0, 100.0,
+                                 -100.0, 3e4, -3e4, float("inf"),
+                                 -float("inf"), float("nan")])])
+    if dtype != torch.float16:
+        x = torch.cat([x, torch.tensor([1e13, -1e13, 3e38, -3e38])])
+    return x.to(dtype).cuda()
+
+
+@pytest.mark.parametrize("dtype", list(R.DTYPES))
+@pytest.mark.parametrize("act", ACTS)
+def test_activation_values(act, dtype):
+    dt = R.DTYPES[dtype]
+    x = act_inputs(dt)
+    y, ck = M.ckpt_act(x, act)
+    check_pack(x, ck)
+    x64 = R.to64(x)
+    want = R.act(x64, act)[0]
+    got = R.to64(y)
+    fine = np.isfinite(want)
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    assert np.array_equal(got[np.isinf(want)], want[np.isinf(want)])
+    bound = R.half_step(dt) * np.abs(want[fine]) + ACT * (
+        1 + np.minimum(np.abs(x64[fine]), np.abs(want[fine]) + 1))
+    assert (np.abs(got[fine] - want[fine]) <= bound).all()
+
+
+@pytest.mark.parametrize("dtype", list(R.DTYPES))
+@pytest.mark.parametrize("act", ACTS)
+def test_activation_backward(act, dtype):
+    dt = R.DTYPES[dtype]
+    x = act_inputs(dt)
+    _, ck = M.ckpt_act(x, act)
+    kept = R.to64(ck.unpack(torch.float32))
+    dy = torch.randn(x.shape, generator=gen(5)).to(dt).cuda()
+    got = R.to64(M.ckpt_act_backward(ck, dy, act))
+    want = R.to64(dy) * R.act(kept, act)[1]
+    fine = np.isfinite(want)
+    assert np.array_equal(np.isnan(got), np.isnan(want))
+    bound = R.half_step(dt) * np.abs(want) + 2 * ACT * np.abs(R.to64(dy))
+    if dt == torch.float16:
+        bound = bound + 2.0 ** -25
+    assert (np.abs(got - want)[fine] <= bound[fine]).all()
+
+
+@pytest.mark.parametrize("act", ACTS)
+def test_slope_is_the_values_difference(act):
+    # away from relu's corner: central differences of the float64 value over
+    # h = 2^-13 are off by h^2/6 times the third derivative (below 3)
+    x = torch.linspace(-4, 4, 400).cuda() + 0.003
+    ck = M.ckpt_pack(x)
+    kept = R.to64(ck.unpack())
+    h = 2.0 ** -13
+    num = (R.act(kept + h, act)[0] - R.act(kept - h, act)[0]) / (2 * h)
+    got = R.to64(M.ckpt_act_backward(ck, torch.ones_like(x), act))
+    away = np.abs(kept) > h
+    assert (np.abs(got - num)[away] <= 2 * ACT + h * h).all()
+
+
+@pytest.mark.parametrize("shape,pad", [((5, 33), 3), ((130, 96), 0),
+                                       ((2, 3, 70), 1), ((1, 1), 0)], ids=str)
+@pytest.mark.parametrize("dtype", list(R.DTYPES))
+def test_activation_shapes_strides_and_mixed_types(shape, pad, dtype):
+    dt = R.DTYPES[dtype]
+    x = activations(shape, torch.float32, 1, pad)
+    y, ck = M.ckpt_act(x, "silu")
+    check_pack(x, ck)
+    assert y.shape == x.shape
+    dy = activations(shape, dt, 2, pad)
+    got = R.to64(M.ckpt_act_backward(ck, dy, "silu"))
+    want = R.to64(dy) * R.act(R.to64(ck.unpack()), "silu")[1]
+    assert (np.abs(got - want) <= R.half_step(dt) * np.abs(want) +
+            2 * ACT * np.abs(R.to64(dy)) + 2.0 ** -25).all()
+
+
+def test_activation_in_place():
+    for dt in R.DTYPES.values():
+        x = activations((67, 75), dt)
+        y, ck = M.ckpt_act(x, "gelu")
+        x2 = x.clone()
+        ck2 = M.Checkpoint8.empty(x.shape, dt, x.device)
+        B.mta_ckpt_pack([(x2.data_ptr(), x2.data_ptr(), ck2.q.data_ptr(),
+                          ck2.scale.data_ptr(), 67, 75, 75, 75)], TYPE[dt], 3)
+        assert torch.equal(x2, y) and torch.equal(ck2.q, ck.q)
+        assert torch.equal(ck2.scale, ck.scale)
+        dy = activations((67, 75), dt, 9)
+        dx = M.ckpt_act_backward(ck, dy, "gelu")
+        B.mta_ckpt_act_backward(
+            [(dy.data_ptr(), dy.data_ptr(), ck.q.data_ptr(),
+              ck.scale.data_ptr(), 67, 75, 75, 75)], TYPE[dt], 3)
+        assert torch.equal(dx, dy)
+
+
+def test_offsets_past_32_bits():
+    # 4.3e9 elements; the last rows are those of a small tensor
+    rows, cols = 1_350_000, 3200
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    x.fill_(1.0)
+    tail = activations((50, cols), torch.bfloat16)
+    x[-50:] = tail
+    x[:50] = tail
+    y, ck = M.ckpt_act(x, "relu")
+    small = M.ckpt_pack(tail)
+    for part in (ck.q.view(rows, cols)[-50:], ck.q.view(rows, cols)[:50]):
+        assert torch.equal(part.reshape(-1), small.q)
+    assert torch.equal(ck.scale.view(rows, -1)[-50:].reshape(-1), small.scale)
+    assert torch.equal(y[-50:], tail.clamp_min(0))
+    del y
+    back = ck.unpack()
+    assert torch.equal(back[-50:], small.unpack())
+    assert torch.equal(back[rows // 2], torch.ones_like(back[0]))
+
+
+# --------------------------------------------------------------------------
+# weight gradient
+# --------------------------------------------------------------------------
+
+def wgrad_case(tokens, fin, fout, dtype, seed=0, pad=0):
+    x = activations((tokens, fin), torch.float32, seed)
+    ck = M.ckpt_pack(x)
+    dy = torch.randn(tokens, fout + pad, generator=gen(seed + 1)).to(
+        dtype).cuda()[:, :fout]
+    kept = R.to64(ck.unpack()) if tokens and fin else np.zeros((tokens, fin))
+    return ck, dy, kept
+
+
+def check_wgrad(dw, db, dy, kept, old_w=0.0, old_b=0.0):
+    """Each of the products' float32 additions is off by half a step of the
+    partial sum it makes, and no partial sum passes the sum of magnitudes: at
+    most tokens + 64 (parts, waves, the old value) of them, 2^-24 each."""
+    d = R.to64(dy)
+    n = (d.shape[0] + 64) * 2.0 ** -24
+    for got, want, mass in (
+            (dw, old_w + d.T @ kept, np.abs(d).T @ np.abs(kept)),
+            (db, old_b + d.sum(0), np.abs(d).sum(0))):
+        if got is None:
+            continue
+        mass = mass + np.abs(old_w if got is dw else old_b)
+        bound = n * mass + R.half_step(got.dtype) * np.abs(want)
+        if got.dtype == torch.float16:
+            bound = bound + 2.0 ** -25
+        assert (np.abs(R.to64(got) - want) <= bound).all()
+
+
+@pytest.mark.parametrize("dtype", list(R.DTYPES))
+@pytest.mark.parametrize("tokens,fin,fout", [
+    (1, 1, 1), (1, 32, 8), (2, 33, 9), (31, 7, 130), (32, 128, 128),
+    (33, 129, 127), (64, 257, 16), (100, 40, 300), (257, 96, 40),
+    (1000, 130, 260), (4099, 65, 33), (640, 520, 516)])
+def test_wgrad_shapes(tokens, fin, fout, dtype):
+    ck, dy, kept = wgrad_case(tokens, fin, fout, R.DTYPES[dtype])
+    dw, db = M.ckpt_wgrad(ck, dy)
+    assert dw.shape == (fout, fin) and dw.dtype == torch.float32
+    check_wgrad(dw, db, dy, kept)
+    again = M.ckpt_wgrad(ck, dy)
+    assert torch.equal(again[0], dw) and torch.equal(again[1], db)
+
+
+@pytest.mark.parametrize("gtype", list(R.DTYPES))
+@pytest.mark.parametrize("dtype", list(R.DTYPES))
+@pytest.mark.parametrize("tokens", [70, 3000])
+def test_wgrad_accumulates_into_strided_gradients(tokens, dtype, gtype):
+    fin, fout, gt = 75, 141, R.DTYPES[gtype]
+    ck, dy, kept = wgrad_case(tokens, fin, fout, R.DTYPES[dtype], pad=3)
+    wide = (torch.randn(fout, fin + 5, generator=gen(8)) * 50).to(gt).cuda()
+    before = wide.clone()
+    db = (torch.randn(fout, generator=gen(9)) * 50).to(gt).cuda()
+    old_b = R.to64(db)
+    got = M.ckpt_wgrad(ck, dy, out=wide[:, 2:2 + fin], out_bias=db,
+                       accumulate=True)
+    assert got[0].data_ptr() == wide[:, 2:].data_ptr() and got[1] is db
+    check_wgrad(wide[:, 2:2 + fin], db, dy, kept,
+                R.to64(before[:, 2:2 + fin]), old_b)
+    assert torch.equal(wide[:, :2], before[:, :2])
+    assert torch.equal(wide[:, 2 + fin:], before[:, 2 + fin:])
+
+
+def test_wgrad_of_no_tokens_and_no_features():
+    ck, dy, _ = wgrad_case(0, 40, 24, torch.bfloat16)
+    dw, db = M.ckpt_wgrad(ck, dy)
+    assert (dw == 0).all() and (db == 0).all()
+    out, ob = torch.ones(24, 40).cuda(), torch.ones(24).cuda()
+    M.ckpt_wgrad(ck, dy, out=out, out_bias=ob, accumulate=True)
+    assert (out == 1).all() and (ob == 1).all()
+    ck, dy, kept = wgrad_case(37, 0, 24, torch.float32)
+    dw, db = M.ckpt_wgrad(ck, dy)
+    assert dw.shape == (24, 0)
+    check_wgrad(None, db, dy, kept)
+    ck, dy, kept = wgrad_case(37, 24, 0, torch.float32)
+    assert M.ckpt_wgrad(ck, dy)[0].shape == (0, 24)
+
+
+def test_wgrad_without_bias_and_in_three_dimensions():
+    x = activations((3, 50, 96), torch.bfloat16)
+    dy = activations((3, 50, 40), torch.bfloat16, 4, pad=8)
+    ck = M.ckpt_pack(x)
+    dw, db = M.ckpt_wgrad(ck, dy, bias=False, dtype=torch.bfloat16)
+    assert db is None and dw.dtype == torch.bfloat16
+    check_wgrad(dw, None, dy.reshape(150, 40),
+                R.to64(ck.unpack()).reshape(150, 96))
+
+
+@pytest.mark.parametrize("dtype", list(R.DTYPES))
+def test_not_finite_gradients_stay_in_their_row(dtype):
+    ck, dy, kept = wgrad_case(130, 70, 60, R.DTYPES[dtype])
+    dy[5, 7], dy[129, 40], dy[64, 59] = float("inf"), float("nan"), -float(
+        "inf")
+    dw, db = M.ckpt_wgrad(ck, dy)
+    bad = [7, 40, 59]
+    ok = [o for o in range(60) if o not in bad]
+    assert not torch.isfinite(db[bad]).any()
+    # every kept value of these tokens is nonzero, so no product is 0 * inf
+    assert not torch.isfinite(dw[bad]).any()
+    assert db[7] == float("inf") and db[59] == -float("inf")
+    check_wgrad(dw[ok], db[ok], dy[:, ok], kept)
+
+
+def test_infinite_activations_reach_the_gradient():
+    x = activations((64, 96), torch.bfloat16)
+    x[10, 33] = float("inf")
+    ck = M.ckpt_pack(x)
+    dy = activations((64, 16), torch.bfloat16, 2)
+    dw, db = M.ckpt_wgrad(ck, dy)
+    assert torch.isnan(dw[:, 33]).all() and torch.isfinite(db).all()
+    assert torch.isfinite(dw[:, :33]).all() and torch.isfinite(
+        dw[:, 34:]).all()
+
+
+def test_float32_gradients_are_not_rounded_to_16_bits():
+    # one token: each result is one product, off by float32 roundings alone
+    ck, dy, kept = wgrad_case(1, 64, 64, torch.float32)
+    dw, db = M.ckpt_wgrad(ck, dy)
+    want = R.to64(dy).T @ kept
+    assert (np.abs(R.to64(dw) - want) <= 3 * 2.0 ** -24 * np.abs(want)).all()
+    assert torch.equal(db, dy[0])
+    # and at both ends of the range
+    for s in (1e-30, 1e30):
+        dw = M.ckpt_wgrad(ck, dy * s)[0]
+        want = R.to64(dy * s).T @ kept
+        assert (np.abs(R.to64(dw) - want) <=
+                3 * 2.0 ** -24 * np.abs(want)).all()
+
+
+def test_wgrad_offsets_past_32_bits():
+    # rows of dy 131,072 apart: the last start past 2^32 elements
+    tokens, fin, fout, ld = 33000, 33, 24, 131072
+    base = torch.zeros(tokens, ld, dtype=torch.bfloat16, device="cuda")
+    ck, dy, kept = wgrad_case(tokens, fin, fout, torch.bfloat16)
+    base[:, -fout:] = dy
+    got = M.ckpt_wgrad(ck, base[:, -fout:])
+    want = M.ckpt_wgrad(ck, dy)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    check_wgrad(got[0], got[1], dy, kept)
+
+
+def test_refusals_of_tensors():
+    ck, dy, _ = wgrad_case(10, 40, 24, torch.bfloat16)
+    cases = [
+        lambda: M.ckpt_wgrad(ck, dy[:5]),
+        lambda: M.ckpt_wgrad(ck, dy.t()),
+        lambda: M.ckpt_wgrad(ck, dy.cpu()),
+        lambda: M.ckpt_wgrad(ck, dy, accumulate=True),
+        lambda: M.ckpt_wgrad(ck, dy, out=torch.zeros(40, 24).cuda()),
+        lambda: M.ckpt_wgrad(ck, dy, out=torch.zeros(24, 40).cuda(),
+                             out_bias=torch.zeros(24).cuda().half()),
+        lambda: M.ckpt_wgrad(ck, dy, bias=False,
+                             out_bias=torch.zeros(24).cuda()),
+        lambda: M.ckpt_act_backward(ck, dy, "relu"),
+        lambda: M.Checkpoint8(ck.q, ck.scale, (11, 40)),
+        lambda: M.Checkpoint8(ck.q, ck.scale.cpu(), (10, 40)),
+    ]
+    for c in cases:
+        with pytest.raises(ValueError):
+            c()
+    for c in (lambda: M.ckpt_wgrad(ck, dy.double()),
+              lambda: M.ckpt_wgrad(ck, dy, dtype=torch.float64),
+              lambda: M.ckpt_pack([dy, dy.float()]),
+              lambda: ck.unpack(torch.float64)):
+        with pytest.raises(TypeError):
+            c()
+    # a workspace that is too small is refused by the library
+    big = M.ckpt_pack(torch.zeros(4096, 32).cuda())
+    need = B.mta_ckpt_wgrad_workspace(4096, 32, 24, 0)
+    assert need > 0
+    g = torch.zeros(4096, 24).cuda()
+    w, ws = torch.zeros(24, 32).cuda(), torch.zeros(need).byte().cuda()
+    with pytest.raises(M.MtaError):
+        B.mta_ckpt_wgrad(B.mta_ckpt_wgrad_args(
+            big.q.data_ptr(), big.scale.data_ptr(), g.data_ptr(),
+            w.data_ptr(), None, ws.data_ptr(), need - 1, 4096, 32, 24, 24, 32,
+            0, 0, 0, 0))
+
+
+# --------------------------------------------------------------------------
+# streams, graphs, autograd
+# --------------------------------------------------------------------------
+
+def test_a_side_stream_orders_its_own_work():
+    x = activations((4000, 800), torch.bfloat16)
+    want = M.ckpt_pack(x)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        y = torch.zeros_like(x)
+        for _ in range(20):          # the pack has to wait for the last add
+            y += 0
+        y += x
+        got = M.ckpt_pack(y)
+        dw, _ = M.ckpt_wgrad(got, y)
+    s.synchronize()
+    assert torch.equal(got.q, want.q) and torch.equal(got.scale, want.scale)
+    assert torch.equal(dw, M.ckpt_wgrad(want, x)[0])
+
+
+def test_captured_calls_replay_on_new_inputs():
+    def work(x, dy, g):
+        y, ck = M.ckpt_act(x, "gelu_tanh")
+        dx = M.ckpt_act_backward(ck, dy, "gelu_tanh")
+        M.ckpt_wgrad(ck, dy, bias=False, out=g, accumulate=True)
+        return y, dx
+
+    x, dy = (activations((3000, 96), torch.bfloat16, s) for s in (1, 2))
+    g1, g2 = torch.zeros(96, 96).cuda(), torch.zeros(96, 96).cuda()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        work(x, dy, g1.clone())
+    torch.cuda.current_stream().wait_stream(s)
+    graph, other = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, dx = work(x, dy, g1)
+    with torch.cuda.graph(other):       # a second graph with its own buffers
+        y2, dx2 = work(x, dy, g2)
+    g1.zero_()
+    g2.zero_()
+    want = torch.zeros_like(g1)
+    for seed in range(4):
+        x.copy_(activations((3000, 96), torch.bfloat16, 10 + seed))
+        dy.copy_(activations((3000, 96), torch.bfloat16, 20 + seed))
+        graph.replay()
+        other.replay()
+        torch.cuda.synchronize()
+        ey, edx = work(x, dy, want)
+        for a, b in ((y, ey), (dx, edx), (y2, ey), (dx2, edx), (g1, want),
+                     (g2, want)):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("wdtype", list(R.DTYPES))
+def test_checkpointed_layers_have_the_formulas_gradients(wdtype):
+    wt = R.DTYPES[wdtype]
+    x = activations((6, 20, 64), torch.bfloat16).requires_grad_()
+    w = (torch.randn(48, 64, generator=gen(3)) * 0.1).to(wt).cuda()
+    b = torch.randn(48, generator=gen(4)).to(wt).cuda()
+    w.requires_grad_(), b.requires_grad_()
+    h = M.checkpointed_linear(x, w, b)
+    a = M.checkpointed_act(h, "silu")
+    da = torch.randn(a.shape, generator=gen(6)).bfloat16().cuda()
+    a.backward(da)
+    assert w.grad.dtype == wt and b.grad.dtype == wt
+    kx = R.to64(M.ckpt_pack(x.detach()).unpack()).reshape(120, 64)
+    kh = R.to64(M.ckpt_pack(h.detach()).unpack()).reshape(120, 48)
+    dh = R.to64(da).reshape(120, 48) * R.act(kh, "silu")[1]
+    # dh is rounded to bfloat16 on its way, half a step 2^-9 relative and
+    # the activation's own bound; so its sums are off by that of their mass
+    err = np.abs(dh) * 2.0 ** -8 + 2 * ACT * np.abs(R.to64(da).reshape(
+        120, 48))
+    n = 184 * 2.0 ** -24
+    want = dh.T @ kx
+    mass = np.abs(dh).T @ np.abs(kx)
+    bound = err.T @ np.abs(kx) + n * mass + 2.0 * R.half_step(wt) * np.abs(
+        want)
+    assert (np.abs(R.to64(w.grad) - want) <= bound).all()
+    bound = err.sum(0) + n * np.abs(dh).sum(0) + 2 * R.half_step(
+        wt) * np.abs(dh.sum(0))
+    assert (np.abs(R.to64(b.grad) - dh.sum(0)) <= bound).all()
+    # x's gradient is the plain product of the rounded dh
+    assert x.grad.shape == x.shape and torch.isfinite(x.grad).all()
+    # expanded gradients (of a sum) are taken
+    x2 = x.detach().requires_grad_()
+    M.checkpointed_act(M.checkpointed_linear(x2, w, b), "relu").sum().backward()
+    assert torch.isfinite(x2.grad).all()
+
+
+def test_layers_skip_what_needs_no_gradient():
+    x = activations((5, 32), torch.float32)
+    w = torch.randn(8, 32).cuda()
+    y = M.checkpointed_linear(x.requires_grad_(), w)
+    y.sum().backward()
+    assert torch.equal(x.grad, w.sum(0).expand(5, 32)) or torch.allclose(
+        x.grad, w.sum(0).expand(5, 32), atol=32 * 2.0 ** -23)
+    b = torch.zeros(8, device="cuda", requires_grad=True)
+    M.checkpointed_linear(x.detach(), w, b).sum().backward()
+    assert torch.equal(b.grad, torch.full((8,), 5.0).cuda())
