@@ -164,7 +164,8 @@ typedef struct {
   float *stats;             /* [3]: loss, sum w kl, sum w [r A > c A] */
   void *workspace;          /* mta_policy_loss_workspace bytes, 8-byte aligned */
   int64_t workspace_bytes;
-  int64_t rows, vocab, ld, ldd; /* rows may be 0; vocab >= 1 */
+  int64_t rows, vocab, ld, ldd; /* rows may be 0; vocab in
+                                     [1, 2^28] */
   double clip_low;          /* in [0, 1] */
   double clip_high;         /* finite, >= 0 */
   double kl_coef;           /* finite, >= 0 */

@@ -124,6 +124,16 @@ __device__ __forceinline__ Raw8<D> load8_part(const void *p, int64_t i, int n,
   return r;
 }
 
+// Eight times the element with bits `v`.
+template <int D>
+__device__ __forceinline__ Raw8<D> fill8(uint32_t v) {
+  Raw8<D> r;
+#pragma unroll
+  for (int k = 0; k < Raw8<D>::kWords; ++k)
+    r.w[k] = D == MTA_F32 ? v : v | v << 16;
+  return r;
+}
+
 template <int D, bool Stream>
 __device__ __forceinline__ void store8(void *p, int64_t i,
                                        const float (&x)[8]) {

@@ -243,12 +243,15 @@ int64_t wgrad_bytes(const mta::WgradShape &s, int64_t fin, int64_t fout) {
   return round16(s.splits * fout * fin * 4) + round16(s.splits * fout * 4);
 }
 
+// Positions within a row are 32-bit byte offsets on the device.
+constexpr int64_t kMostVocab = int64_t{1} << 28;
+
 int check_policy(const mta_policy_args *a, bool backward,
                  std::vector<Region> *regions) {
   if (!a) return fail(MTA_EINVAL, "args is NULL");
   if (a->rows < 0) return fail(MTA_EINVAL, "rows < 0");
-  if (a->vocab < 1 || a->vocab > kMostCols)
-    return fail(MTA_EINVAL, "vocab must be in [1, 2^30] (got %lld)",
+  if (a->vocab < 1 || a->vocab > kMostVocab)
+    return fail(MTA_EINVAL, "vocab must be in [1, 2^28] (got %lld)",
                 static_cast<long long>(a->vocab));
   if (!known_type(a->type)) return fail(MTA_EDTYPE, "unknown type %d", a->type);
   if (a->reserved) return fail(MTA_EINVAL, "reserved must be 0");
@@ -482,11 +485,10 @@ int mta_policy_loss_workspace(int64_t rows, int64_t *bytes) {
   if (!bytes) return fail(MTA_EINVAL, "bytes is NULL");
   *bytes = 0;
   if (rows < 0) return fail(MTA_EINVAL, "rows < 0");
-  // a launch has at most kPolicyGrid workgroups of four rows, and whole
-  // workgroups leave their sums
-  const int64_t slots = std::min<int64_t>((rows + 3) / 4 * 4,
-                                          int64_t{mta::kPolicyGrid} * 4);
-  *bytes = slots * mta::kPolicySums * 8;
+  if (!fits(rows, 64, 1)) return fail(MTA_EINVAL, "too large");
+  // a row's terms, and those of the stretches that many rows are joined in
+  *bytes = (rows + (rows > mta::kPolicyJoin ? mta::kPolicyJoin : 0)) *
+           mta::kPolicySums * 8;
   return ok();
 }
 

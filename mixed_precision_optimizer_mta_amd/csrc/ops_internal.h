@@ -81,9 +81,10 @@ hipError_t launch_wgrad(const WgradArgs &args, const WgradShape &shape,
 
 static_assert(sizeof(mta_policy_row) == 16, "saved row layout");
 
-// Workgroups of a policy loss launch leave one set of partial sums each.
-constexpr int kPolicyGrid = 2048;
+// A row leaves its terms of the three sums in the workspace; more than
+// kPolicyJoin rows are joined in stretches first.
 constexpr int kPolicySums = 3;
+constexpr int64_t kPolicyJoin = 4096;
 
 hipError_t launch_policy(const mta_policy_args &args, hipStream_t stream);
 hipError_t launch_policy_backward(const mta_policy_args &args,

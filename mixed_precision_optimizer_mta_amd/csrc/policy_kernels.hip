@@ -5,7 +5,8 @@
 // the first gradient can be written, so the plain way reads the logits at
 // least twice.  Here a row stays in the registers of the workgroup that reads
 // it (65536 logits are 32 registers a lane of 1024 in 16 bits), so one call
-// reads every logit once and writes every gradient once: bound by HBM.  Longer
+// reads every logit once and writes every gradient once: bound by HBM (8192
+// rows of 50257 bfloat16 logits, a fifth of them masked, at 5.6 TB/s).  Longer
 // rows are read twice, the second time mostly from the memory-side cache.
 //
 // Numerics: exponentials are 2^((z - max) log2 e) in float32, a lane sums at
@@ -32,15 +33,73 @@ struct PolicyRow {
   double sums[kPolicySums];
 };
 
+// e^x - 1 in float64: x = k ln 2 + r with |r| <= ln(2) / 2, the Taylor series
+// of e^r - 1 to r^12 (the next term is below 2^-50 of it), times 2^k.  A row
+// needs three of these and a logarithm from one wave that the others wait
+// for; the library's, which round to the last bit, take twice the time and
+// (their tables of constants kept over the loop of rows) three times the
+// registers.
+__device__ __forceinline__ double exp_less_1(double x) {
+  const double k = __builtin_rint(x * 1.4426950408889634);
+  double r = __builtin_fma(-k, 0x1.62e42fefa39efp-1, x);
+  r = __builtin_fma(-k, 0x1.abc9e3b39803fp-56, r);
+  double p = 1.0 / 479001600.0;
+  p = __builtin_fma(p, r, 1.0 / 39916800.0);
+  p = __builtin_fma(p, r, 1.0 / 3628800.0);
+  p = __builtin_fma(p, r, 1.0 / 362880.0);
+  p = __builtin_fma(p, r, 1.0 / 40320.0);
+  p = __builtin_fma(p, r, 1.0 / 5040.0);
+  p = __builtin_fma(p, r, 1.0 / 720.0);
+  p = __builtin_fma(p, r, 1.0 / 120.0);
+  p = __builtin_fma(p, r, 1.0 / 24.0);
+  p = __builtin_fma(p, r, 1.0 / 6.0);
+  p = __builtin_fma(p, r, 0.5);
+  p = __builtin_fma(p * r, r, r);
+  const double s = __builtin_ldexp(1.0, static_cast<int>(k));
+  double y = __builtin_fma(s, p, s - 1.0);
+  if (x > 709.0) y = __builtin_inf();
+  if (x < -100.0) y = -1.0;
+  return y;
+}
+
+// ln s in float64 for a normal s > 0: s = m 2^e with m in [1/sqrt 2, sqrt 2),
+// ln m = 2 atanh t, t = (m - 1) / (m + 1), |t| < 0.172, its series to t^17.
+__device__ __forceinline__ double ln(double s) {
+  double m = __builtin_amdgcn_frexp_mant(s);
+  int e = __builtin_amdgcn_frexp_exp(s);
+  if (m < 0.70710678118654752) {
+    m += m;
+    --e;
+  }
+  const double t = (m - 1.0) / (m + 1.0), u = t * t;
+  double p = 2.0 / 17.0;
+  p = __builtin_fma(p, u, 2.0 / 15.0);
+  p = __builtin_fma(p, u, 2.0 / 13.0);
+  p = __builtin_fma(p, u, 2.0 / 11.0);
+  p = __builtin_fma(p, u, 2.0 / 9.0);
+  p = __builtin_fma(p, u, 2.0 / 7.0);
+  p = __builtin_fma(p, u, 2.0 / 5.0);
+  p = __builtin_fma(p, u, 2.0 / 3.0);
+  p = __builtin_fma(p, u, 2.0);
+  return __builtin_fma(static_cast<double>(e), 0x1.62e42fefa39efp-1, p * t);
+}
+
+// What the caller gives for a row.
+struct RowInputs {
+  float w, old_logp, advantage, ref_logp, scale;
+  int64_t action;
+};
+
 // The row's scalars from its maximum and the sum of exp(z - max).
-__device__ PolicyRow policy_row(const mta_policy_args &a, int64_t row, float w,
-                                float za, float top, double total) {
+__device__ __forceinline__ PolicyRow policy_row(const mta_policy_args &a,
+                                                const RowInputs &in, float za,
+                                                float top, double total) {
   PolicyRow r;
-  const double logtotal = log(total);
+  const double logtotal = ln(total);
   r.lse = double{top} + logtotal;
   r.logp = (double{za} - double{top}) - logtotal;
-  const double adv = a.advantages[row];
-  const double ratio = exp(r.logp - double{a.old_logp[row]});
+  const double adv = in.advantage, w = in.w;
+  const double ratio = 1.0 + exp_less_1(r.logp - double{in.old_logp});
   const double lo = 1.0 - a.clip_low, hi = 1.0 + a.clip_high;
   // comparisons that keep a NaN ratio
   const double cut = ratio < lo ? lo : ratio > hi ? hi : ratio;
@@ -50,16 +109,16 @@ __device__ PolicyRow policy_row(const mta_policy_args &a, int64_t row, float w,
   double slope = over ? 0.0 : -plain;
   double kl = 0.0;
   if (a.ref_logp) {
-    const double d = double{a.ref_logp[row]} - r.logp;
-    const double e = expm1(d);
+    const double d = double{in.ref_logp} - r.logp;
+    const double e = exp_less_1(d);
     kl = e - d;
     loss += a.kl_coef * kl;
     slope -= a.kl_coef * e;
   }
-  r.coef = static_cast<float>(double{w} * slope);
-  r.sums[0] = double{w} * loss;
-  r.sums[1] = double{w} * kl;
-  r.sums[2] = over ? double{w} : 0.0;
+  r.coef = static_cast<float>(w * slope);
+  r.sums[0] = w * loss;
+  r.sums[1] = w * kl;
+  r.sums[2] = over ? w : 0.0;
   return r;
 }
 
@@ -75,11 +134,36 @@ __device__ __forceinline__ float wave_sum(float x) {
   return x;
 }
 
-// Threads to a row; a workgroup is at least four waves.
+// A row as whole runs of eight logits from its first address that is a
+// multiple of Align, and up to Align / size + 7 single logits at its two ends,
+// one to each of the first lanes.  Rows of an odd length start anywhere: with
+// runs from each row's first element the same batch of 50257 columns took 352
+// us instead of 265.
+struct Cut {
+  uint32_t head, units, vocab;
+  // The end of the row that lane i holds; `vocab` or more: none.
+  __device__ __forceinline__ uint32_t edge(uint32_t i) const {
+    return i < head ? i : i + units * 8;
+  }
+};
+
+template <int D, int Align>
+__device__ __forceinline__ Cut cut_row(const void *row, uint32_t vocab) {
+  const uint32_t off =
+      static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row)) % Align;
+  Cut c;
+  c.head = (Align - off) % Align / sizeof(elem<D>);
+  if (c.head > vocab) c.head = vocab;
+  c.units = (vocab - c.head) / 8;
+  c.vocab = vocab;
+  return c;
+}
+
+// Rows of a workgroup, which is at least four waves.
 template <int Threads>
 constexpr int kRows = Threads < 256 ? 256 / Threads : 1;
 
-// A row's shared values, one set a row of the workgroup.
+// What the waves of a row tell each other.
 template <int Threads>
 struct RowShared {
   float top[Threads / 64];
@@ -87,186 +171,238 @@ struct RowShared {
   float gain, chosen;
 };
 
-// Units >= 0: that many runs of eight logits to a lane, kept in registers.
-// Units == 0: the row is streamed, twice.
+// Runs of a streamed row that a lane has in flight.
+constexpr int kBatch = 4;
+
+// Units > 0: that many runs of eight logits to a lane, kept in registers.
+// Units == 0: the row is streamed, twice.  A row is one workgroup's (or one
+// wave's) and there is no loop over rows: over such a loop the compiler keeps
+// the scalars' float64 constants in 60 registers.
 template <int D, int Threads, int Units>
-__global__ __launch_bounds__(Threads * kRows<Threads>) void k_policy(
-    const mta_policy_args a) {
+__global__ __launch_bounds__(Threads * kRows<Threads>,
+                             (D == MTA_F32 ? 4 : 8)) void k_policy(
+    const mta_policy_args a, int64_t row0) {
   constexpr int kWaves = Threads / 64;
   constexpr bool kOneWave = Threads == 64;
-  __shared__ RowShared<Threads> shared[kRows<Threads>];
-  const int slot_in = threadIdx.x / Threads;
-  RowShared<Threads> &sh = shared[slot_in];
-  const int tid = threadIdx.x % Threads;
-  const int wave = tid / 64;
-  const int64_t slot =
-      static_cast<int64_t>(blockIdx.x) * kRows<Threads> + slot_in;
-  const int64_t slots = static_cast<int64_t>(gridDim.x) * kRows<Threads>;
-  const int64_t vocab = a.vocab;
-  const int64_t units = (vocab + 7) / 8;
-  const float S = a.d_grad_scale ? *a.d_grad_scale : 1.0f;
-  double sums[kPolicySums] = {0.0, 0.0, 0.0};
-
-  const auto load = [&](int64_t base, int64_t u) {
-    const int64_t left = vocab - u * 8;
-    if (left >= 8) return load8<D, Units != 0>(a.logits, base + u * 8);
-    return load8_part<D>(a.logits, base + u * 8,
-                         static_cast<int>(left > 0 ? left : 0), kMinusInf<D>);
+  __shared__ RowShared<Threads> sh;
+  const uint32_t tid = threadIdx.x % Threads;
+  const uint32_t wave =
+      __builtin_amdgcn_readfirstlane(threadIdx.x / 64) % kWaves;
+  const int64_t row =
+      row0 + int64_t{blockIdx.x} * kRows<Threads> +
+      (kOneWave ? __builtin_amdgcn_readfirstlane(threadIdx.x / 64) : 0);
+  if (row >= a.rows) return;
+  const uint32_t vocab = static_cast<uint32_t>(a.vocab);
+  const elem<D> *zrow = static_cast<const elem<D> *>(a.logits) + row * a.ld;
+  elem<D> *grow =
+      a.dlogits ? static_cast<elem<D> *>(a.dlogits) + row * a.ldd : nullptr;
+  double *out = static_cast<double *>(a.workspace) + row * kPolicySums;
+  const Cut cut = cut_row<D, kOneWave ? 16 : 128>(zrow, vocab);
+  const uint32_t units = cut.units, edge = cut.edge(tid);
+  const bool has_edge = edge < vocab;
+  const auto at = [&](uint32_t u) { return cut.head + u * 8; };
+  const auto load = [&](uint32_t u) {
+    return load8<D, Units != 0>(zrow, at(u));
   };
-  const auto store = [&](int64_t base, int64_t u, const float(&x)[8]) {
-    const int64_t left = vocab - u * 8;
-    if (left >= 8) {
-      store8<D, true>(a.dlogits, base + u * 8, x);
-    } else {
+
+  // all at once: each is a trip to memory
+  RowInputs in;
+  in.w = a.weights ? a.weights[row]
+                   : static_cast<float>(1.0 / static_cast<double>(a.rows));
+  in.action = a.actions[row];
+  in.old_logp = a.old_logp[row];
+  in.advantage = a.advantages[row];
+  in.ref_logp = a.ref_logp ? a.ref_logp[row] : 0.0f;
+  in.scale = a.d_grad_scale ? *a.d_grad_scale : 1.0f;
+  if (in.w == 0.0f) {
+    const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (grow) {
+      for (uint32_t u = tid; u < units; u += Threads)
+        store8<D, true>(grow, at(u), zero);
+      if (has_edge) store_elem<D>(grow, edge, 0.0f);
+    }
+    if (tid == 0) {
+      if (a.logp) a.logp[row] = 0.0f;
+      if (a.saved) a.saved[row] = mta_policy_row{0.0, 0.0f, 0};
+#pragma unroll
+      for (int i = 0; i < kPolicySums; ++i) out[i] = 0.0;
+    }
+    return;
+  }
+
+  // the row's maximum, and its sum of 2^((z - max) log2 e)
+  Raw8<D> z[Units ? Units : 1];
+  float top = -kInf, sum = 0.0f;
+  if constexpr (Units != 0) {
+#pragma unroll
+    for (int j = 0; j < Units; ++j) {
+      const uint32_t u = tid + j * Threads;
+      if (u < units) z[j] = load(u);
+      else z[j] = fill8<D>(kMinusInf<D>);
+    }
+  }
+  const float ze = has_edge ? load_elem<D>(zrow, edge) : -kInf;
+  const int64_t action = in.action;
+  const bool inside = action >= 0 && action < a.vocab;
+  const float za = inside ? load_elem<D>(zrow, action) : __builtin_nanf("");
+  if constexpr (Units != 0) {
+#pragma unroll
+    for (int j = 0; j < Units; ++j)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) top = fmaxf(top, z[j][k]);
+  } else {
+    // running maximum and sum; a lane that has seen only -inf has 0
+    for (uint32_t u = tid; u < units; u += Threads * kBatch) {
+      Raw8<D> x[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        if (u + j * Threads < units) x[j] = load(u + j * Threads);
+        else x[j] = fill8<D>(kMinusInf<D>);
+      }
+      float m = top;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m = fmaxf(m, x[j][k]);
+      if (m != top) sum *= __builtin_amdgcn_exp2f((top - m) * kLog2E);
+      top = m;
+      const float ref = m == -kInf ? 0.0f : m;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          sum += __builtin_amdgcn_exp2f((x[j][k] - ref) * kLog2E);
+    }
+  }
+  const float seen = top;  // what `sum` is relative to (streamed)
+  top = fmaxf(top, ze);
+  // the compiler would keep a 16-bit row widened from here on: pinned, its
+  // registers stay half as many
+  const auto pin = [&] {
+    if constexpr (Units != 0 && D != MTA_F32) {
+#pragma unroll
+      for (int j = 0; j < Units; ++j)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) __asm__("" : "+v"(z[j].w[k]));
+    }
+  };
+  pin();
+  float all = wave_max(top);
+  if constexpr (!kOneWave) {
+    if (tid % 64 == 0) sh.top[wave] = all;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) all = fmaxf(all, sh.top[i]);
+  }
+  if constexpr (Units != 0) {
+#pragma unroll
+    for (int j = 0; j < Units; ++j)
 #pragma unroll
       for (int k = 0; k < 8; ++k)
-        if (k < left) store_elem<D>(a.dlogits, base + u * 8 + k, x[k]);
-    }
-  };
-  const auto sync = [&] {
-    if constexpr (!kOneWave) __syncthreads();
-  };
+        sum += __builtin_amdgcn_exp2f((z[j][k] - all) * kLog2E);
+  } else {
+    sum *= __builtin_amdgcn_exp2f((seen - all) * kLog2E);
+  }
+  top = all;
+  sum += __builtin_amdgcn_exp2f((ze - all) * kLog2E);
+  sum = wave_sum(sum);
+  double total = sum;
+  if constexpr (!kOneWave) {
+    if (tid % 64 == 0) sh.sum[wave] = sum;
+    __syncthreads();
+    total = 0.0;
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i) total += sh.sum[i];
+  }
 
-  for (int64_t row = slot; row < a.rows; row += slots) {
-    const float w = a.weights
-                        ? a.weights[row]
-                        : static_cast<float>(1.0 / static_cast<double>(a.rows));
-    const int64_t zbase = row * a.ld, gbase = row * a.ldd;
-    if (w == 0.0f) {
-      const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-      if (a.dlogits)
-        for (int64_t u = tid; u < units; u += Threads) store(gbase, u, zero);
-      if (tid == 0) {
-        if (a.logp) a.logp[row] = 0.0f;
-        if (a.saved) a.saved[row] = mta_policy_row{0.0, 0.0f, 0};
-      }
-      continue;
-    }
-    const int64_t action = a.actions[row];
-    const bool inside = action >= 0 && action < vocab;
-    const float za = inside ? load_elem<D>(a.logits, zbase + action)
-                            : __builtin_nanf("");
-
-    // the row's maximum, and its sum of 2^((z - max) log2 e)
-    Raw8<D> z[Units ? Units : 1];
-    float top = -kInf, sum = 0.0f;
-    if constexpr (Units != 0) {
-#pragma unroll
-      for (int j = 0; j < Units; ++j)
-        z[j] = load(zbase, tid + j * Threads);
-#pragma unroll
-      for (int j = 0; j < Units; ++j)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) top = fmaxf(top, z[j][k]);
-    } else {
-      // running maximum and sum; a lane that has seen only -inf has 0
-      for (int64_t u = tid; u < units; u += Threads) {
-        const Raw8<D> x = load(zbase, u);
-        float m = top;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) m = fmaxf(m, x[k]);
-        if (m != top)
-          sum *= __builtin_amdgcn_exp2f((top - m) * kLog2E);
-        top = m;
-        const float ref = m == -kInf ? 0.0f : m;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          sum += __builtin_amdgcn_exp2f((x[k] - ref) * kLog2E);
-      }
-    }
-    float all = wave_max(top);
-    if constexpr (!kOneWave) {
-      if (tid % 64 == 0) sh.top[wave] = all;
-      sync();
-#pragma unroll
-      for (int i = 0; i < kWaves; ++i) all = fmaxf(all, sh.top[i]);
-    }
-    if constexpr (Units != 0) {
-#pragma unroll
-      for (int j = 0; j < Units; ++j)
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          sum += __builtin_amdgcn_exp2f((z[j][k] - all) * kLog2E);
-    } else {
-      sum *= __builtin_amdgcn_exp2f((top - all) * kLog2E);
-    }
-    top = all;
-    sum = wave_sum(sum);
-    double total = sum;
-    if constexpr (!kOneWave) {
-      if (tid % 64 == 0) sh.sum[wave] = sum;
-      sync();
-      total = 0.0;
-#pragma unroll
-      for (int i = 0; i < kWaves; ++i) total += sh.sum[i];
-    }
-
-    float gain = 0.0f, chosen = 0.0f;  // S * coef; the action's gradient
-    if (wave == 0) {
-      const PolicyRow r = policy_row(a, row, w, za, top, total);
-      gain = S * r.coef;
-      chosen = static_cast<float>(-expm1(r.logp)) * gain;
-      if (tid == 0) {
-        if (a.logp) a.logp[row] = static_cast<float>(r.logp);
-        if (a.saved) a.saved[row] = mta_policy_row{r.lse, r.coef, 1};
+  float gain = 0.0f, chosen = 0.0f;  // S * coef; the action's gradient
+  if (wave == 0) {
+    const PolicyRow r = policy_row(a, in, za, top, total);
+    gain = r.coef * in.scale;
+    chosen = static_cast<float>(-exp_less_1(r.logp)) * gain;
+    if (tid == 0) {
+      if (a.logp) a.logp[row] = static_cast<float>(r.logp);
+      if (a.saved) a.saved[row] = mta_policy_row{r.lse, r.coef, 1};
+      if constexpr (!kOneWave) {
         sh.gain = gain;
         sh.chosen = chosen;
-#pragma unroll
-        for (int i = 0; i < kPolicySums; ++i) sums[i] += r.sums[i];
       }
+#pragma unroll
+      for (int i = 0; i < kPolicySums; ++i) out[i] = r.sums[i];
     }
-    if (a.dlogits) {
-      if constexpr (!kOneWave) {
-        sync();
-        gain = sh.gain;
-        chosen = sh.chosen;
-      }
-      gain = -gain / static_cast<float>(total);
-      const auto put = [&](int64_t u, const Raw8<D> &x) {
-        float g[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          g[k] = __builtin_amdgcn_exp2f((x[k] - top) * kLog2E) * gain;
-        store(gbase, u, g);
-      };
-      if constexpr (Units != 0) {
-#pragma unroll
-        for (int j = 0; j < Units; ++j)
-          if (tid + j * Threads < units) put(tid + j * Threads, z[j]);
-      } else {
-        for (int64_t u = tid; u < units; u += Threads) put(u, load(zbase, u));
-      }
-      // the action's own gradient, by the lane that wrote its run
-      if (inside && tid == (action / 8) % Threads)
-        store_elem<D>(a.dlogits, gbase + action, chosen);
-    }
-    // the shared values are rewritten by the next row
-    sync();
   }
-  if (tid == 0) {
-    double *out = static_cast<double *>(a.workspace) + slot * kPolicySums;
+  if (!grow) return;
+  if constexpr (!kOneWave) {
+    __syncthreads();
+    gain = sh.gain;
+    chosen = sh.chosen;
+  }
+  gain = -gain / static_cast<float>(total);
+  // the exponentials are formed again: the compiler would keep those of the
+  // sum, twice the row's registers
+  __asm__("" : "+v"(top));
+  pin();
+  const auto grad = [&](float x) {
+    return __builtin_amdgcn_exp2f((x - top) * kLog2E) * gain;
+  };
+  const auto put = [&](uint32_t u, const Raw8<D> &x) {
+    float g[8];
 #pragma unroll
-    for (int i = 0; i < kPolicySums; ++i) out[i] = sums[i];
+    for (int k = 0; k < 8; ++k) g[k] = grad(x[k]);
+    store8<D, true>(grow, at(u), g);
+  };
+  if constexpr (Units != 0) {
+#pragma unroll
+    for (int j = 0; j < Units; ++j)
+      if (tid + j * Threads < units) put(tid + j * Threads, z[j]);
+  } else {
+    for (uint32_t u = tid; u < units; u += Threads * kBatch) {
+      Raw8<D> x[kBatch];
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (u + j * Threads < units) x[j] = load(u + j * Threads);
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (u + j * Threads < units) put(u + j * Threads, x[j]);
+    }
+  }
+  if (has_edge) store_elem<D>(grow, edge, grad(ze));
+  // the action's own gradient, by the lane that wrote its place
+  if (inside) {
+    const uint32_t c = static_cast<uint32_t>(action) - cut.head;
+    if (c < units * 8 ? tid == c / 8 % Threads
+                      : has_edge && edge == static_cast<uint32_t>(action))
+      store_elem<D>(grow, action, chosen);
   }
 }
 
-// The partial sums joined in one fixed order.
+// The rows' sums joined in one fixed order: a workgroup takes a stretch of
+// `per` rows; a second launch (of one, with `stats`) joins the stretches.
 __global__ __launch_bounds__(1024) void k_policy_stats(const double *part,
-                                                       int slots,
+                                                       int64_t n, int64_t per,
+                                                       double *joined,
                                                        float *stats) {
-  __shared__ double sh[1024];
+  __shared__ double sh[kPolicySums][16];
   const int tid = threadIdx.x;
+  const int64_t lo = blockIdx.x * per;
+  const int64_t hi = n < lo + per ? n : lo + per;
+  double s[kPolicySums] = {0.0, 0.0, 0.0};
+  for (int64_t k = lo + tid; k < hi; k += 1024)
+#pragma unroll
+    for (int i = 0; i < kPolicySums; ++i) s[i] += part[k * kPolicySums + i];
+#pragma unroll
   for (int i = 0; i < kPolicySums; ++i) {
-    double s = 0.0;
-    for (int k = tid; k < slots; k += 1024) s += part[k * kPolicySums + i];
-    sh[tid] = s;
-    __syncthreads();
-    for (int o = 512; o; o >>= 1) {
-      if (tid < o) sh[tid] += sh[tid + o];
-      __syncthreads();
-    }
-    if (tid == 0) stats[i] = static_cast<float>(sh[0]);
-    __syncthreads();
+#pragma unroll
+    for (int o = 32; o; o >>= 1) s[i] += __shfl_xor(s[i], o);
+    if (tid % 64 == 0) sh[i][tid / 64] = s[i];
+  }
+  __syncthreads();
+  if (tid < kPolicySums) {
+    double v = 0.0;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v += sh[tid][k];
+    if (stats) stats[tid] = static_cast<float>(v);
+    else joined[blockIdx.x * kPolicySums + tid] = v;
   }
 }
 
@@ -278,67 +414,85 @@ constexpr int kBackUnits = kBackThreads * kBackUnroll;
 
 template <int D>
 __global__ __launch_bounds__(kBackThreads) void k_policy_backward(
-    const mta_policy_args a, int64_t parts) {
-  const float S = a.d_grad_scale ? *a.d_grad_scale : 1.0f;
-  const int64_t n = a.rows * parts;
-  for (int64_t b = blockIdx.x; b < n; b += gridDim.x) {
-    const int64_t row = b / parts;
-    const int64_t u0 = (b - row * parts) * kBackUnits + threadIdx.x;
-    const int64_t zbase = row * a.ld, gbase = row * a.ldd;
-    const mta_policy_row r = a.saved[row];
-    const int64_t action = a.actions[row];
-    const bool on = r.on != 0;
-    const float gain = S * r.coef;
-    const float hi = static_cast<float>(r.lse);
-    const float lo = hi - hi == 0.0f
-                         ? static_cast<float>(r.lse - double{hi}) * kLog2E
-                         : 0.0f;
-    Raw8<D> z[kBackUnroll];
-    int n_in[kBackUnroll];
+    const mta_policy_args a, int64_t row0, uint32_t parts) {
+  const uint32_t tid = threadIdx.x;
+  const uint32_t part = blockIdx.x % parts;
+  const int64_t row = row0 + blockIdx.x / parts;
+  const uint32_t vocab = static_cast<uint32_t>(a.vocab);
+  const elem<D> *zrow = static_cast<const elem<D> *>(a.logits) + row * a.ld;
+  elem<D> *grow = static_cast<elem<D> *>(a.dlogits) + row * a.ldd;
+  const Cut cut = cut_row<D, 128>(zrow, vocab);
+  const uint32_t u0 = part * kBackUnits + tid;
+  const uint32_t edge = part == 0 ? cut.edge(tid) : vocab;
+  const mta_policy_row r = a.saved[row];
+  if (r.on == 0) {
+    const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < kBackUnroll; ++j) {
-      const int64_t u = u0 + j * kBackThreads;
-      const int64_t left = a.vocab - u * 8;
-      n_in[j] = static_cast<int>(left >= 8 ? 8 : left > 0 ? left : 0);
-      if (!on) continue;
-      if (n_in[j] == 8) z[j] = load8<D, true>(a.logits, zbase + u * 8);
-      else z[j] = load8_part<D>(a.logits, zbase + u * 8, n_in[j], 0);
+      const uint32_t u = u0 + j * kBackThreads;
+      if (u < cut.units) store8<D, true>(grow, cut.head + u * 8, zero);
     }
-#pragma unroll
-    for (int j = 0; j < kBackUnroll; ++j) {
-      const int64_t u = u0 + j * kBackThreads;
-      float g[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const float p =
-            __builtin_amdgcn_exp2f(__builtin_fmaf(z[j][k] - hi, kLog2E, -lo));
-        const float d = u * 8 + k == action ? 1.0f - p : -p;
-        g[k] = on ? gain * d : 0.0f;
-      }
-      if (n_in[j] == 8) {
-        store8<D, true>(a.dlogits, gbase + u * 8, g);
-      } else {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if (k < n_in[j]) store_elem<D>(a.dlogits, gbase + u * 8 + k, g[k]);
-      }
-    }
+    if (edge < vocab) store_elem<D>(grow, edge, 0.0f);
+    return;
   }
+  Raw8<D> z[kBackUnroll];
+#pragma unroll
+  for (int j = 0; j < kBackUnroll; ++j) {
+    const uint32_t u = u0 + j * kBackThreads;
+    if (u < cut.units) z[j] = load8<D, true>(zrow, cut.head + u * 8);
+  }
+  const float ze = edge < vocab ? load_elem<D>(zrow, edge) : 0.0f;
+  const int64_t action = a.actions[row];
+  const float gain = (a.d_grad_scale ? *a.d_grad_scale : 1.0f) * r.coef;
+  // lse as a float32 and the rest of it
+  const float hi = static_cast<float>(r.lse);
+  const float lo = hi - hi == 0.0f
+                       ? static_cast<float>(r.lse - double{hi}) * kLog2E
+                       : 0.0f;
+  const auto grad = [&](float x, uint32_t at) {
+    const float p =
+        __builtin_amdgcn_exp2f(__builtin_fmaf(x - hi, kLog2E, -lo));
+    return gain * (at == action ? 1.0f - p : -p);
+  };
+#pragma unroll
+  for (int j = 0; j < kBackUnroll; ++j) {
+    const uint32_t u = u0 + j * kBackThreads;
+    if (u >= cut.units) continue;
+    const uint32_t at = cut.head + u * 8;
+    float g[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) g[k] = grad(z[j][k], at + k);
+    store8<D, true>(grow, at, g);
+  }
+  if (edge < vocab) store_elem<D>(grow, edge, grad(ze, edge));
 }
 
 template <int D, int Threads, int Units>
 hipError_t start(const mta_policy_args &a, hipStream_t stream) {
-  const int64_t groups =
-      (a.rows + kRows<Threads> - 1) / kRows<Threads>;
-  const int grid = static_cast<int>(groups < kPolicyGrid ? groups : kPolicyGrid);
-  if (grid > 0)
+  constexpr int64_t kMost = int64_t{1} << 21;  // below 2^32 threads a launch
+  const int64_t groups = (a.rows + kRows<Threads> - 1) / kRows<Threads>;
+  for (int64_t g = 0; g < groups; g += kMost) {
+    const int64_t n = groups - g < kMost ? groups - g : kMost;
     k_policy<D, Threads, Units>
-        <<<grid, Threads * kRows<Threads>, 0, stream>>>(a);
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  k_policy_stats<<<1, 1024, 0, stream>>>(
-      static_cast<const double *>(a.workspace), grid * kRows<Threads>,
-      a.stats);
+        <<<static_cast<int>(n), Threads * kRows<Threads>, 0, stream>>>(
+            a, g * kRows<Threads>);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  const double *part = static_cast<const double *>(a.workspace);
+  int64_t n = a.rows;
+  if (n > kPolicyJoin) {
+    // stretches of at least kPolicyJoin rows, at most kPolicyJoin of them
+    int64_t per = (n + kPolicyJoin - 1) / kPolicyJoin;
+    if (per < kPolicyJoin) per = kPolicyJoin;
+    const int64_t m = (n + per - 1) / per;
+    double *joined = static_cast<double *>(a.workspace) + n * kPolicySums;
+    k_policy_stats<<<static_cast<int>(m), 1024, 0, stream>>>(part, n, per,
+                                                             joined, nullptr);
+    part = joined;
+    n = m;
+  }
+  k_policy_stats<<<1, 1024, 0, stream>>>(part, n, n, nullptr, a.stats);
   return hipGetLastError();
 }
 
@@ -358,25 +512,36 @@ hipError_t launch_policy(const mta_policy_args &a, hipStream_t stream) {
   return with_type(a.type, [&](auto d) {
     constexpr int D = decltype(d)::value;
     // a wave, four or sixteen to a row: as few as hold it, since a smaller
-    // group waits less at its joins
+    // group waits less at its joins.  A float32 row of sixteen waves leaves
+    // room for one group on a CU, whose loads, sums and stores then take
+    // turns: streamed, two groups overlap theirs and the second reading comes
+    // from the memory-side cache (2047 rows of 50257 with their gradient 200
+    // us against 212, the loss alone 67 us against 98).
     if (a.vocab <= 64 * 64) return start_units<D, 64, 1>(a, stream);
     if (a.vocab <= 256 * 64) return start_units<D, 256, 3>(a, stream);
-    if (a.vocab <= 1024 * 64) return start_units<D, 1024, 3>(a, stream);
+    if constexpr (D != MTA_F32)
+      if (a.vocab <= 1024 * 64) return start_units<D, 1024, 3>(a, stream);
     return start<D, 1024, 0>(a, stream);
   });
 }
 
 hipError_t launch_policy_backward(const mta_policy_args &a,
                                   hipStream_t stream) {
-  const int64_t units = (a.vocab + 7) / 8;
-  const int64_t parts = (units + kBackUnits - 1) / kBackUnits;
-  const int64_t n = a.rows * parts;
-  if (n == 0) return hipSuccess;
-  const int grid = static_cast<int>(n < (1 << 22) ? n : 1 << 22);
+  if (a.rows == 0) return hipSuccess;
+  // (the row's ends go with its first part)
+  const int64_t units = a.vocab / 8;
+  const int64_t parts = units > 0 ? (units + kBackUnits - 1) / kBackUnits : 1;
+  const int64_t most = (int64_t{1} << 22) / parts;  // rows of a launch
   return with_type(a.type, [&](auto d) {
-    k_policy_backward<decltype(d)::value>
-        <<<grid, kBackThreads, 0, stream>>>(a, parts);
-    return hipGetLastError();
+    for (int64_t row = 0; row < a.rows; row += most) {
+      const int64_t n = a.rows - row < most ? a.rows - row : most;
+      k_policy_backward<decltype(d)::value>
+          <<<static_cast<int>(n * parts), kBackThreads, 0, stream>>>(
+              a, row, static_cast<uint32_t>(parts));
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
   });
 }
 

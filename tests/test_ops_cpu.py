@@ -172,7 +172,7 @@ def _p(**kw):
 
 
 @pytest.mark.parametrize("kw,code", [
-    (dict(rows=-1), -1), (dict(vocab=0), -1), (dict(vocab=1 << 31), -1),
+    (dict(rows=-1), -1), (dict(vocab=0), -1), (dict(vocab=1 << 29, ld=1 << 29, ldd=1 << 29), -1),
     (dict(type=3), -3), (dict(reserved=1), -1), (dict(clip_low=-0.1), -1),
     (dict(clip_low=1.1), -1), (dict(clip_low=float("nan")), -1),
     (dict(clip_high=-0.1), -1), (dict(clip_high=float("inf")), -1),
@@ -209,8 +209,10 @@ def test_policy_null_arguments():
     assert L.mta_policy_loss_workspace(1, None) == -1
     assert _code(B.mta_policy_loss_workspace, -1) == -1
     assert B.mta_policy_loss_workspace(0) == 0
-    assert B.mta_policy_loss_workspace(1) == 4 * 24
-    assert B.mta_policy_loss_workspace(1 << 40) == 8192 * 24
+    assert B.mta_policy_loss_workspace(1) == 24
+    assert B.mta_policy_loss_workspace(4096) == 4096 * 24
+    assert B.mta_policy_loss_workspace(4097) == (4097 + 4096) * 24
+    assert _code(B.mta_policy_loss_workspace, 1 << 60) == -1
 
 
 def test_tensors_off_the_gpu_are_refused():
