@@ -51,30 +51,36 @@ hipError_t launch_ckpt(int mode, int type, int act, const CkptList &list,
 
 // ---- weight gradient from a checkpoint ----------------------------------
 
-struct WgradShape {
-  int tile_o, tile_i;  // output tile of a workgroup
-  int step;            // tokens of one pass through LDS
-  int terms;           // bfloat16 values a dy is taken as the sum of
-  int64_t tiles;       // output tiles
-  int splits;          // parts the tokens are cut into
-  int64_t per_split;   // tokens of a part, a multiple of `step`
+constexpr int kWgradTile = 128;  // outputs of a workgroup, each way
+constexpr int kWgradStep = 32;   // tokens it takes at a time
+constexpr int kWgradRanges = 256;  // answers about the scales' range, at most
+
+// The workgroups of a launch: `whole` tiles of the output over all tokens,
+// then `cut` tiles in `parts` parts of `part_tokens` each.
+struct WgradGrid {
+  int64_t tiles_o, tiles_i;
+  int64_t whole, cut;
+  int64_t part_tokens;
+  int parts;
+  int ranges;  // workgroups that look at the scales (float16 dy)
 };
 
-WgradShape wgrad_shape(int64_t tokens, int64_t fin, int64_t fout, int type,
-                       int cus);
+WgradGrid wgrad_grid(int64_t tokens, int64_t fin, int64_t fout, int type,
+                     int cus);
 
 struct WgradArgs {
   const uint8_t *q, *scale;
   const void *dy;
   void *dw, *db;
-  float *part;     // [splits][fout * fin] when splits > 1
-  float *part_db;  // [splits][fout] when splits > 1
+  float *part;     // [cut][parts][tile][tile]
+  float *part_db;  // [parts][fout]
+  int *range;      // [ranges]
   int64_t tokens, fin, fout, lddy, lddw;
   int64_t ldq;
   int type, gtype, accumulate;
 };
 
-hipError_t launch_wgrad(const WgradArgs &args, const WgradShape &shape,
+hipError_t launch_wgrad(const WgradArgs &args, const WgradGrid &grid,
                         hipStream_t stream);
 
 // ---- policy loss --------------------------------------------------------

@@ -3,89 +3,124 @@
 //
 //   dW[o][i] = sum_t dY[t][o] * kept[t][i],   db[o] = sum_t dY[t][o]
 //
-// A kept value is an e4m3 code times a power of two: exact in bfloat16, so
-// the product runs on the bfloat16 matrix instructions without any rounding
-// but that of its float32 sums, and the checkpoint is read at one byte a
-// value.  A float16 (float32) dY is split into two (three) bfloat16 values
-// whose sum it is, one matrix product each.
+// A kept value is an e4m3 code times a power of two: exact in bfloat16, so the
+// product runs on the bfloat16 matrix instructions without any rounding but
+// that of its float32 sums, and the checkpoint is read at one byte a value.
+// A float16 dY is multiplied on the float16 instructions where every kept
+// value is exact in float16 too, as those of float16 activations are; a
+// kernel looks at the scales first.  Otherwise a float16 (float32) dY is split
+// into the two (three) bfloat16 values whose sum it is, one product each.
 //
 // Both operands lie with the contracted index t as their rows, while a matrix
 // instruction wants eight consecutive t of one column in a lane.  They are
-// staged in LDS as they lie, and read back with the transposing LDS load
-// (16 lanes read four rows of 16 columns and get four rows of one column
-// each).
+// staged in LDS as they lie (the codes converted on the way) and read back
+// with the transposing LDS load: 16 lanes read four rows of 16 columns and
+// each gets four rows of one column.
+//
+// Bound by the LDS and the matrix pipes together: a step of a workgroup, 32
+// tokens, is 32 KiB of transposing reads (which reach 128 bytes a clock here),
+// 16 KiB of writes (78), 16 loads a wave apart and 64 matrix instructions.  A
+// workgroup of four waves takes a tile of 128 x 128, and three share a CU, so
+// that one's reads run under another's products: 8192 tokens of 4096 x 4096 in
+// bfloat16 at 890 TFLOP/s, against 820 to 880 for one workgroup of 256 x 256
+// with the same inner loop, whose eight waves keep step, and 800 without the
+// order that sched_group_barrier asks for.
 #include "ops_device.h"
 
 namespace mta {
 namespace {
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
+constexpr int kTile = kWgradTile;  // outputs of a workgroup, each way
+constexpr int kStep = kWgradStep;  // tokens at a time
+constexpr int kThreads = 256;
 // 64 bytes behind each LDS row: the four rows of a transposing load, and the
 // two column halves that are read together, then lie in distinct banks.
-constexpr int kPad = 32;
+constexpr int kPitch = kTile + 32;
 
-template <int D>
-constexpr int kTerms = D == MTA_BF16 ? 1 : D == MTA_F16 ? 2 : 3;
+// How dY is multiplied.
+enum Mode { kBf16, kF16, kF16Split, kF32Split };
 
-// The bfloat16 values that a dy is the sum of, largest first.  Each takes the
-// next eight significant bits of what is left by cutting the lower ones off,
-// so a difference is exact and no value grows past its source.  An infinity
-// or NaN is carried by the first alone.
-template <int D>
-__device__ __forceinline__ void split8(const Raw8<D> &x,
-                                       uint32_t (&w)[kTerms<D>][4]) {
-  if constexpr (D == MTA_BF16) {
+template <int M>
+struct Stage {
+  static constexpr int kType =
+      M == kBf16 ? MTA_BF16 : M == kF32Split ? MTA_F32 : MTA_F16;
+  static constexpr int kTerms = M == kF32Split ? 3 : M == kF16Split ? 2 : 1;
+  // Two buffers of 18 KiB and 9 for each term, 64 accumulators and up to 104
+  // other registers a lane.
+  static constexpr int kWavesPerSimd = 4 - kTerms;
+  struct Operand {
+    uint16_t at[kStep][kPitch];
+  };
+  struct Buffer {
+    Operand o[kTerms], i;
+  };
+};
+
+// The bfloat16 values that v is the sum of, largest first, each in the upper
+// half of a word.  Each takes the next eight significant bits of what is left
+// by cutting the lower ones off, so a difference is exact and no value grows
+// past its source.  An infinity or NaN is carried by the first alone.
+template <int Terms>
+__device__ __forceinline__ void split(float v, uint32_t (&b)[Terms]) {
+  const bool fine = __builtin_fabsf(v) < __builtin_inff();
 #pragma unroll
-    for (int k = 0; k < 4; ++k) w[0][k] = x.w[k];
+  for (int t = 0; t < Terms; ++t) {
+    b[t] = __float_as_uint(v) & 0xFFFF0000u;
+    // a NaN of low bits only would be cut to an infinity
+    if (t == 0 && v != v) b[t] = 0x7FC00000u;
+    v = fine ? v - __uint_as_float(b[t]) : 0.0f;
+  }
+}
+
+// Four codes of one block times their scale, as two words of 16-bit values.
+template <int M>
+__device__ __forceinline__ void kept4(uint32_t code, float scale,
+                                      uint32_t &lo, uint32_t &hi) {
+  if constexpr (M == kF16) {
+    lo = __builtin_bit_cast(
+        uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(code, scale, false));
+    hi = __builtin_bit_cast(
+        uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(code, scale, true));
   } else {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      uint32_t u[2][kTerms<D>];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float v = x[2 * k + h];
-        const bool fine = __builtin_fabsf(v) < __builtin_inff();
-#pragma unroll
-        for (int t = 0; t < kTerms<D>; ++t) {
-          uint32_t b = __float_as_uint(v) & 0xFFFF0000u;
-          // a NaN of low bits only would be cut to an infinity
-          if (t == 0 && v != v) b = 0x7FC00000u;
-          u[h][t] = b;
-          v = fine ? v - __uint_as_float(b) : 0.0f;
-        }
-      }
-#pragma unroll
-      for (int t = 0; t < kTerms<D>; ++t)
-        w[t][k] = (u[0][t] >> 16) | u[1][t];
-    }
+    lo = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(
+                                          code, scale, false));
+    hi = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(
+                                          code, scale, true));
   }
 }
 
-// Sixteen codes of one block to bfloat16.
-__device__ __forceinline__ void kept16(const u32x4 &code, uint32_t sb,
-                                       u32x4 (&out)[2]) {
-  const float s = __uint_as_float(sb << 23);
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    out[k / 2][2 * (k % 2)] = __builtin_bit_cast(
-        uint32_t,
-        __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code[k], s, false));
-    out[k / 2][2 * (k % 2) + 1] = __builtin_bit_cast(
-        uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(code[k], s, true));
-  }
-}
-
-__device__ __forceinline__ bf16x8 transposed(const uint16_t *lds, int stride) {
+// Eight tokens of one column, from `p` in this lane's place.
+__device__ __forceinline__ s16x8 transposed(const uint16_t *p) {
   typedef __attribute__((address_space(3))) s16x4 lds4;
-  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)lds);
+  const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)p);
   const s16x4 b =
-      __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(lds + 4 * stride));
-  typedef short s16x8 __attribute__((ext_vector_type(8)));
-  const s16x8 v = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
-  return __builtin_bit_cast(bf16x8, v);
+      __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4 *)(p + 4 * kPitch));
+  return s16x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+}
+
+template <int M>
+__device__ __forceinline__ f32x16 multiply(s16x8 a, s16x8 b, f32x16 c) {
+  if constexpr (M == kF16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(
+        __builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+        __builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0,
+        0);
+}
+
+// An address kept in scalar registers: the compiler would fold a lane's offset
+// into it and add the two in every lane.
+__device__ __forceinline__ const MTA_GLOBAL uint8_t *scalar(
+    const MTA_GLOBAL uint8_t *p) {
+  __asm__("" : "+s"(p));
+  return p;
 }
 
 // A sum into dw or db, in the gradient's type.
@@ -103,244 +138,380 @@ __device__ __forceinline__ void put(void *p, int64_t i, float x, int gtype,
   }
 }
 
-// A workgroup's tile of BO x BI outputs over its part of the tokens; WO x WI
-// waves of 32 x 32 matrix tiles; Step tokens at a time through two LDS
-// buffers.
-template <int D, int BO, int BI, int WO, int WI, int Step>
-struct Wgrad {
-  static constexpr int kThreads = 64 * WO * WI;
-  static constexpr int kT = kTerms<D>;
-  static constexpr int kStrideO = BO + kPad, kStrideI = BI + kPad;
-  static constexpr int kUnitsO = Step * (BO / 8);   // 8 values each
-  static constexpr int kUnitsI = Step * (BI / 16);  // 16 codes each
-  static constexpr int kPerO = kUnitsO / kThreads, kPerI = kUnitsI / kThreads;
-  static constexpr int kMo = BO / WO / 32, kMi = BI / WI / 32;
-  static_assert(kUnitsO % kThreads == 0 && kUnitsI % kThreads == 0, "");
-  static_assert(kThreads % (BO / 8) == 0 && kThreads % (BI / 16) == 0, "");
-  struct Buffer {
-    uint16_t o[kT][Step * kStrideO];
-    uint16_t i[Step * kStrideI];
-  };
-};
+// The output tile number t: down bands of eight rows of tiles, so that tiles
+// that run together share their operands' columns.
+__device__ __forceinline__ void tile_at(const WgradGrid &g, int64_t t,
+                                        int64_t &o, int64_t &i) {
+  constexpr int64_t kBand = 8;
+  const int64_t band = t / (kBand * g.tiles_i), first = band * kBand;
+  const int64_t height = min(kBand, g.tiles_o - first);
+  const int64_t u = t - first * g.tiles_i;
+  o = (first + u % height) * kTile;
+  i = u / height * kTile;
+}
 
-template <int D, int BO, int BI, int WO, int WI, int Step>
-__global__ __launch_bounds__(64 * WO *WI) void k_wgrad(const WgradArgs a,
-                                                       int tiles_i, int tiles,
-                                                       int64_t per_split) {
-  using K = Wgrad<D, BO, BI, WO, WI, Step>;
-  __shared__ __attribute__((aligned(16))) typename K::Buffer buf[2];
-  const int tid = threadIdx.x, lane = tid % 64, wave = tid / 64;
-  const int split = blockIdx.x / tiles, tile = blockIdx.x % tiles;
-  const int64_t o0 = int64_t{tile / tiles_i} * BO;
-  const int64_t i0 = int64_t{tile % tiles_i} * BI;
-  const int64_t t0 = split * per_split;
-  const int64_t t1 = min(a.tokens, t0 + per_split);
-  const int steps = static_cast<int>((t1 - t0 + Step - 1) / Step);
-  const bool bias = a.db && i0 == 0;
+// Work item `w` of n, such that workgroups that run on one of the eight XCDs
+// (blocks are dealt out in turn) take neighbouring ones.
+__device__ __forceinline__ int64_t neighbours(int64_t w, int64_t n) {
+  const int64_t x = w % 8, each = n / 8, more = n % 8;
+  return x * each + min(x, more) + w / 8;
+}
 
-  // what this lane stages: fixed columns, kPerO (kPerI) of the step's rows
-  const int co = tid % (BO / 8), ro = tid / (BO / 8);
-  const int ci = tid % (BI / 16), ri = tid / (BI / 16);
-  constexpr int kRowsO = K::kThreads / (BO / 8);
-  constexpr int kRowsI = K::kThreads / (BI / 16);
-  const int64_t left_o = a.fout - (o0 + co * 8);
-  const int n_o = static_cast<int>(left_o >= 8 ? 8 : left_o > 0 ? left_o : 0);
-  const bool in_i = i0 + ci * 16 < a.ldq;
+// Whether every kept value is exact in float16: a scale in [2^-15, 2^7] makes
+// the smallest code 2^-24 and the largest 57344; the smallest scale marks a
+// block that may be all zeros.  A workgroup answers for a stretch of blocks.
+__global__ __launch_bounds__(256) void k_wgrad_range(const WgradArgs a,
+                                                     int64_t blocks) {
+  int fine = 1;
+  for (int64_t e = int64_t{blockIdx.x} * 256 + threadIdx.x; e < blocks;
+       e += int64_t{gridDim.x} * 256) {
+    const uint32_t s = ((const MTA_GLOBAL uint8_t *)a.scale)[e];
+    if (s >= 112 && s <= 134) continue;
+    uint32_t any = s == 10 ? 0 : 1;
+    if (!any) {
+      const auto *q = (const MTA_GLOBAL u32x4 *)a.q + e * 2;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) any |= (q[0][k] | q[1][k]) & 0x7F7F7F7Fu;
+    }
+    if (any) fine = 0;
+  }
+  fine = __syncthreads_and(fine);
+  if (threadIdx.x == 0) a.range[blockIdx.x] = fine;
+}
 
-  Raw8<D> y[K::kPerO];
-  u32x4 code[K::kPerI];
-  uint32_t sb[K::kPerI];
+template <int M>
+__global__ __launch_bounds__(kThreads)
+    __attribute__((amdgpu_waves_per_eu(Stage<M>::kWavesPerSimd))) void
+    k_wgrad(const WgradArgs a, const WgradGrid g) {
+  using K = Stage<M>;
+  constexpr int D = K::kType, kTerms = K::kTerms;
+  constexpr int kRounds = kStep / 16;
+  const int tid = threadIdx.x, lane = tid % 64;
+  const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
+
+  if constexpr (M == kF16 || M == kF16Split) {
+    const int fine =
+        __syncthreads_and(tid < g.ranges ? a.range[tid] : 1);
+    if (fine != (M == kF16)) return;
+  }
+
+  // Whole tiles first, then the parts of the cut ones.
+  const int64_t block = blockIdx.x;
+  const bool cut = block >= g.whole;
+  int64_t tile, part = 0;
+  if (!cut) {
+    tile = neighbours(block, g.whole);
+  } else {
+    const int64_t w = neighbours(block - g.whole, g.cut * g.parts);
+    part = w / g.cut;
+    tile = g.whole + w % g.cut;
+  }
+  int64_t o0, i0;
+  tile_at(g, tile, o0, i0);
+  const int64_t t0 = cut ? part * g.part_tokens : 0;
+  const int64_t t1 = cut ? min(a.tokens, t0 + g.part_tokens) : a.tokens;
+  const int steps = static_cast<int>((t1 - t0 + kStep - 1) / kStep);
+
+  __shared__ typename K::Buffer buf[2];
+
+  // A lane stages eight columns of dY in tokens row_o and row_o + 16, and
+  // sixteen of the checkpoint in token row_i.
+  constexpr int kRowsO = kThreads / (kTile / 8), kRowsI = kThreads / (kTile / 16);
+  constexpr int kNO = kStep / kRowsO;
+  static_assert(kNO == 2 && kRowsI == kStep, "a step is staged in one go");
+  const int co = tid % (kTile / 8) * 8, row_o = tid / (kTile / 8);
+  const int ci = tid % (kTile / 16) * 16, row_i = tid / (kTile / 16);
+  const int64_t pitch_s = a.ldq / MTA_CKPT_BLOCK;
+  // Columns past the last whole run are the last one's again: what comes of
+  // them is not written.
+  const int64_t col_o = min(o0 + co, max(int64_t{0}, a.fout - 8));
+  const int64_t col_i = min(i0 + ci, max(int64_t{0}, a.ldq - 16));
+  const int64_t lane_o = (col_o - o0 + row_o * a.lddy) * int64_t{sizeof(elem<D>)};
+  const uint32_t lane_i = static_cast<uint32_t>(col_i - i0 + row_i * a.ldq);
+  const uint32_t lane_s = static_cast<uint32_t>(
+      col_i / MTA_CKPT_BLOCK - i0 / MTA_CKPT_BLOCK + row_i * pitch_s);
+
+  struct Raw {
+    Raw8<D> o[kNO];
+    u32x4 code;
+    uint32_t scale;
+  } raw[2];
   float db[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 
-  const auto fetch = [&](int step) {
-    const int64_t t = t0 + int64_t{step} * Step;
+  // A step that lies inside the tensors, loaded without a test.
+  const auto fetch = [&](int step, Raw &x) {
+    const int64_t t = t0 + int64_t{step} * kStep;
 #pragma unroll
-    for (int j = 0; j < K::kPerO; ++j) {
-      const int64_t r = t + ro + j * kRowsO;
-      const int64_t at = r * a.lddy + o0 + co * 8;
-      if (r < t1 && n_o == 8) y[j] = load8<D, false>(a.dy, at);
-      else y[j] = load8_part<D>(a.dy, at, r < t1 ? n_o : 0, 0);
-    }
+    for (int j = 0; j < kNO; ++j) {
+      const auto *p = scalar(
+          (const MTA_GLOBAL uint8_t *)a.dy +
+          ((t + j * kRowsO) * a.lddy + o0) * int64_t{sizeof(elem<D>)});
 #pragma unroll
-    for (int j = 0; j < K::kPerI; ++j) {
-      const int64_t r = t + ri + j * kRowsI;
-      code[j] = u32x4{0, 0, 0, 0};
-      sb[j] = 0;
-      if (r < t1 && in_i) {
-        const int64_t at = r * a.ldq + i0 + ci * 16;
-        code[j] = *(const MTA_GLOBAL u32x4 *)(a.q + at);
-        sb[j] = ((const MTA_GLOBAL uint8_t *)a.scale)[at / MTA_CKPT_BLOCK];
+      for (int h = 0; h < Raw8<D>::kWords / 4; ++h) {
+        const u32x4 v =
+            *(const MTA_GLOBAL typename Wide<D>::type *)(p + lane_o + h * 16);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x.o[j].w[4 * h + k] = v[k];
       }
     }
+    x.code = *(const MTA_GLOBAL u32x4 *)(
+        scalar((const MTA_GLOBAL uint8_t *)a.q + t * a.ldq + i0) + lane_i);
+    x.scale = *(scalar((const MTA_GLOBAL uint8_t *)a.scale + t * pitch_s +
+                       i0 / MTA_CKPT_BLOCK) +
+                lane_s);
   };
-  const auto stage = [&](typename K::Buffer &b) {
+  // Any step: what lies outside is zero.
+  const auto fetch_edge = [&](int step, Raw &x) {
+    const int64_t t = t0 + int64_t{step} * kStep;
+    const int64_t left = a.fout - (o0 + co);
+    const int n = static_cast<int>(left >= 8 ? 8 : left > 0 ? left : 0);
 #pragma unroll
-    for (int j = 0; j < K::kPerO; ++j) {
-      uint32_t w[K::kT][4];
-      split8<D>(y[j], w);
+    for (int j = 0; j < kNO; ++j) {
+      const int64_t r = t + row_o + j * kRowsO;
+      const int64_t at = r * a.lddy + o0 + co;
+      if (r < t1 && n == 8) x.o[j] = load8<D, false>(a.dy, at);
+      else x.o[j] = load8_part<D>(a.dy, at, r < t1 ? n : 0, 0);
+    }
+    x.code = u32x4{0, 0, 0, 0};
+    x.scale = 0;
+    const int64_t r = t + row_i;
+    if (r < t1 && i0 + ci < a.ldq) {
+      const int64_t at = r * a.ldq + i0 + ci;
+      x.code = *(const MTA_GLOBAL u32x4 *)(a.q + at);
+      x.scale = ((const MTA_GLOBAL uint8_t *)a.scale)[at / MTA_CKPT_BLOCK];
+    }
+  };
+  const auto stage = [&](typename K::Buffer &b, const Raw &x, auto with_bias) {
 #pragma unroll
-      for (int t = 0; t < K::kT; ++t)
-        *(u32x4 *)&b.o[t][(ro + j * kRowsO) * K::kStrideO + co * 8] =
+    for (int j = 0; j < kNO; ++j) {
+      uint32_t w[kTerms][4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if constexpr (kTerms == 1) {
+          w[0][k] = x.o[j].w[k];
+        } else {
+          uint32_t u[kTerms], v[kTerms];
+          split<kTerms>(x.o[j][2 * k], u);
+          split<kTerms>(x.o[j][2 * k + 1], v);
+#pragma unroll
+          for (int t = 0; t < kTerms; ++t) w[t][k] = (u[t] >> 16) | v[t];
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < kTerms; ++t)
+        *(u32x4 *)&b.o[t].at[row_o + j * kRowsO][co] =
             u32x4{w[t][0], w[t][1], w[t][2], w[t][3]};
-      if (bias) {
+      if constexpr (decltype(with_bias)::value) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) db[k] += y[j][k];
+        for (int k = 0; k < 8; ++k) db[k] += x.o[j][k];
       }
     }
+    const float s = __uint_as_float(x.scale << 23);
 #pragma unroll
-    for (int j = 0; j < K::kPerI; ++j) {
-      u32x4 v[2];
-      kept16(code[j], sb[j], v);
-      u32x4 *at = (u32x4 *)&b.i[(ri + j * kRowsI) * K::kStrideI + ci * 16];
-      at[0] = v[0];
-      at[1] = v[1];
+    for (int h = 0; h < 2; ++h) {
+      uint32_t w[4];
+      kept4<M>(x.code[2 * h], s, w[0], w[1]);
+      kept4<M>(x.code[2 * h + 1], s, w[2], w[3]);
+      *(u32x4 *)&b.i.at[row_i][ci + h * 8] = u32x4{w[0], w[1], w[2], w[3]};
     }
   };
 
-  f32x16 acc[K::kMo][K::kMi];
+  // Waves lie two by two, each with 2 x 2 matrix tiles of 32 x 32.
+  // The second and third terms of a float32 dY have their own sums: three
+  // roundings to the first one's size for every sixteen tokens would be 1.3e-6
+  // of the result after 16384, where one is 5e-7.
+  constexpr int kSums = kTerms == 3 ? 2 : 1;
+  f32x16 acc[kSums][2][2];
 #pragma unroll
-  for (int x = 0; x < K::kMo; ++x)
+  for (int u = 0; u < kSums; ++u)
 #pragma unroll
-    for (int v = 0; v < K::kMi; ++v)
+    for (int x = 0; x < 2; ++x)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) acc[x][v][r] = 0.0f;
-
-  const int wo = (wave / WI) * (BO / WO), wi = (wave % WI) * (BI / WI);
+      for (int v = 0; v < 2; ++v)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[u][x][v][r] = 0.0f;
+  const int wo = wave / 2 * 64, wi = wave % 2 * 64;
   // this lane's place in a transposing load of 32 columns x 16 tokens
   const int tr = (lane / 32) * 8 + (lane % 16) / 4;
   const int tc = ((lane / 16) % 2) * 16 + (lane % 4) * 4;
+  s16x8 fo[2][kTerms][2], fi[2][2];
+  const auto read = [&](const typename K::Buffer &b, int k, int set) {
+#pragma unroll
+    for (int v = 0; v < 2; ++v)
+      fi[set][v] = transposed(&b.i.at[k * 16 + tr][wi + v * 32 + tc]);
+#pragma unroll
+    for (int t = 0; t < kTerms; ++t)
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        fo[set][t][x] = transposed(&b.o[t].at[k * 16 + tr][wo + x * 32 + tc]);
+  };
 
-  if (steps > 0) {
-    fetch(0);
-    stage(buf[0]);
-    fetch(1);
-  }
-  __syncthreads();
-  for (int s = 0; s < steps; ++s) {
-    const typename K::Buffer &b = buf[s & 1];
+  // Steps [from, to), each fetched by `get`.  While step s is multiplied, step
+  // s + 1 goes to LDS and steps s + 2 and s + 3 are on their way.
+  const auto run = [&](int from, int to, auto &&get, auto with_bias) {
+    const int n = to - from;
+    if (n <= 0) return;
+    get(from, raw[0]);
+    stage(buf[0], raw[0], with_bias);
+    // (past the end: the last step again)
+    get(min(from + 1, to - 1), raw[0]);
+    get(min(from + 2, to - 1), raw[1]);
+    __syncthreads();
+    const auto step = [&](int s, typename K::Buffer &b, typename K::Buffer &next,
+                          Raw &x, auto steady) {
+      read(b, 0, 0);
 #pragma unroll
-    for (int k = 0; k < Step / 16; ++k) {
-      bf16x8 fi[K::kMi];
+      for (int k = 0; k < kRounds; ++k) {
+        if (k + 1 < kRounds) read(b, k + 1, (k + 1) & 1);
 #pragma unroll
-      for (int v = 0; v < K::kMi; ++v)
-        fi[v] = transposed(
-            &b.i[(k * 16 + tr) * K::kStrideI + wi + v * 32 + tc], K::kStrideI);
+        for (int t = kTerms - 1; t >= 0; --t)
 #pragma unroll
-      for (int t = K::kT - 1; t >= 0; --t) {
+          for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int x = 0; x < K::kMo; ++x) {
-          const bf16x8 fo = transposed(
-              &b.o[t][(k * 16 + tr) * K::kStrideO + wo + x * 32 + tc],
-              K::kStrideO);
-#pragma unroll
-          for (int v = 0; v < K::kMi; ++v)
-            acc[x][v] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                fo, fi[v], acc[x][v], 0, 0, 0);
+            for (int v = 0; v < 2; ++v) {
+              f32x16 &sum = acc[t == 0 ? 0 : kSums - 1][m][v];
+              sum = multiply<M>(fo[k & 1][t][m], fi[k & 1][v], sum);
+            }
+        if (k == 0) {
+          if (decltype(steady)::value || s + 1 < n) stage(next, x, with_bias);
+          if (decltype(steady)::value || s + 3 < n) get(from + s + 3, x);
         }
+        if constexpr (kTerms == 1) {
+          // a product, two reads of the next round's operands, a few others'
+          // instructions, and so on
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+            if (k == 0) __builtin_amdgcn_sched_group_barrier(0x002, 3, 0);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
       }
+      __syncthreads();
+    };
+    int s = 0;
+    for (; s + 4 < n; s += 2) {
+      step(s, buf[0], buf[1], raw[0], std::true_type{});
+      step(s + 1, buf[1], buf[0], raw[1], std::true_type{});
     }
-    if (s + 1 < steps) {
-      stage(buf[(s + 1) & 1]);
-      fetch(s + 2);
+    for (; s < n; s += 2) {
+      step(s, buf[0], buf[1], raw[0], std::false_type{});
+      if (s + 1 < n) step(s + 1, buf[1], buf[0], raw[1], std::false_type{});
     }
     __syncthreads();
+  };
+  const bool bias = a.db && i0 == 0;
+  const bool inside = (o0 + kTile <= a.fout || a.fout % 8 == 0) && a.ldq > 0;
+  const int inner = inside ? static_cast<int>((t1 - t0) / kStep) : 0;
+  if (bias) {
+    run(0, inner, fetch, std::true_type{});
+    run(inner, steps, fetch_edge, std::true_type{});
+  } else {
+    run(0, inner, fetch, std::false_type{});
+    run(inner, steps, fetch_edge, std::false_type{});
   }
 
   // D[o][i]: lane % 32 is the column i, the rows o are 4 (lane / 32) +
-  // r % 4 + 8 (r / 4)
+  // r % 4 + 8 (r / 4).  A part's tile goes to the workspace whole.
+  float *out = cut ? a.part + ((tile - g.whole) * g.parts + part) *
+                                  int64_t{kTile * kTile}
+                   : nullptr;
 #pragma unroll
-  for (int x = 0; x < K::kMo; ++x)
+  for (int x = 0; x < 2; ++x)
 #pragma unroll
-    for (int v = 0; v < K::kMi; ++v) {
-      const int64_t i = i0 + wi + v * 32 + lane % 32;
-      if (i >= a.fin) continue;
+    for (int v = 0; v < 2; ++v) {
+      const int i = wi + v * 32 + lane % 32;
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const int64_t o =
-            o0 + wo + x * 32 + (lane / 32) * 4 + r % 4 + 8 * (r / 4);
-        if (o >= a.fout) continue;
-        if (a.part)
-          a.part[(split * a.fout + o) * a.fin + i] = acc[x][v][r];
-        else
-          put(a.dw, o * a.lddw + i, acc[x][v][r], a.gtype, a.accumulate);
+        const int o = wo + x * 32 + (lane / 32) * 4 + r % 4 + 8 * (r / 4);
+        float y = acc[0][x][v][r];
+        if constexpr (kSums == 2) y += acc[1][x][v][r];
+        if (cut)
+          out[o * kTile + i] = y;
+        else if (o0 + o < a.fout && i0 + i < a.fin)
+          put(a.dw, (o0 + o) * a.lddw + i0 + i, y, a.gtype, a.accumulate);
       }
     }
   if (bias) {
-    // the rows of a column are joined in order
+    // a column's rows are joined in order
     float *sum = (float *)&buf[0];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sum[ro * BO + co * 8 + k] = db[k];
+    for (int k = 0; k < 8; ++k) sum[row_o * kTile + co + k] = db[k];
     __syncthreads();
-    for (int c = tid; c < BO; c += K::kThreads) {
-      if (o0 + c >= a.fout) continue;
+    if (tid < kTile && o0 + tid < a.fout) {
       float s = 0.0f;
-      for (int r = 0; r < kRowsO; ++r) s += sum[r * BO + c];
-      if (a.part_db) a.part_db[split * a.fout + o0 + c] = s;
-      else put(a.db, o0 + c, s, a.gtype, a.accumulate);
+      for (int r = 0; r < kRowsO; ++r) s += sum[r * kTile + tid];
+      if (cut) a.part_db[part * a.fout + o0 + tid] = s;
+      else put(a.db, o0 + tid, s, a.gtype, a.accumulate);
     }
   }
 }
 
-// The parts' sums joined in order.
+// The cut tiles' parts joined in order: a workgroup takes 16 rows of a tile.
 __global__ __launch_bounds__(256) void k_wgrad_join(const WgradArgs a,
-                                                    int splits) {
-  const int64_t n = a.fout * a.fin;
-  const int64_t all = n + (a.db ? a.fout : 0);
-  for (int64_t e = int64_t{blockIdx.x} * 256 + threadIdx.x; e < all;
-       e += int64_t{gridDim.x} * 256) {
-    const bool w = e < n;
-    const float *p = w ? a.part + e : a.part_db + (e - n);
-    const int64_t pitch = w ? n : a.fout;
-    float s = 0.0f;
-    for (int k = 0; k < splits; ++k) s += p[k * pitch];
-    if (w) put(a.dw, e / a.fin * a.lddw + e % a.fin, s, a.gtype, a.accumulate);
-    else put(a.db, e - n, s, a.gtype, a.accumulate);
+                                                    const WgradGrid g) {
+  constexpr int kStrips = kTile / 16;
+  const int64_t which = blockIdx.x / kStrips;
+  const int strip = blockIdx.x % kStrips;
+  int64_t o0, i0;
+  tile_at(g, g.whole + which, o0, i0);
+  const float *p = a.part + which * g.parts * int64_t{kTile * kTile} +
+                   strip * 16 * kTile;
+  f32x4 s[2] = {};
+  const int at = threadIdx.x * 4;
+  for (int k = 0; k < g.parts; ++k)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      s[j] += *(const MTA_GLOBAL f32x4 *)(p + k * int64_t{kTile * kTile} + at +
+                                          j * 1024);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int64_t o = o0 + strip * 16 + (at + j * 1024) / kTile;
+    const int64_t i = i0 + at % kTile;
+    if (o >= a.fout) continue;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (i + k < a.fin)
+        put(a.dw, o * a.lddw + i + k, s[j][k], a.gtype, a.accumulate);
+  }
+  if (a.db && i0 == 0 && strip == 0 && threadIdx.x < kTile) {
+    const int64_t o = o0 + threadIdx.x;
+    if (o < a.fout) {
+      float b = 0.0f;
+      for (int k = 0; k < g.parts; ++k) b += a.part_db[k * a.fout + o];
+      put(a.db, o, b, a.gtype, a.accumulate);
+    }
   }
 }
 
-constexpr int kTileO = 128, kTileI = 128, kStep = 32;
+template <int M>
+hipError_t start(const WgradArgs &a, const WgradGrid &g, hipStream_t stream) {
+  k_wgrad<M><<<static_cast<int>(g.whole + g.cut * g.parts), kThreads, 0,
+               stream>>>(a, g);
+  return hipGetLastError();
+}
 
 }  // namespace
 
-WgradShape wgrad_shape(int64_t tokens, int64_t fin, int64_t fout, int type,
-                       int cus) {
-  WgradShape s{};
-  s.tile_o = kTileO;
-  s.tile_i = kTileI;
-  s.step = kStep;
-  s.terms = type == MTA_BF16 ? 1 : type == MTA_F16 ? 2 : 3;
-  // no input features: the bias gradient alone still takes a column of tiles
-  s.tiles = ((fout + kTileO - 1) / kTileO) *
-            (((fin > 0 ? fin : 1) + kTileI - 1) / kTileI);
-  const int64_t steps = (tokens + kStep - 1) / kStep;
-  int64_t splits = s.tiles > 0 ? (2 * cus + s.tiles - 1) / s.tiles : 1;
-  if (splits > steps / 8) splits = steps / 8;
-  if (splits < 1) splits = 1;
-  s.per_split = (steps + splits - 1) / splits * kStep;
-  s.splits = s.per_split > 0
-                 ? static_cast<int>((tokens + s.per_split - 1) / s.per_split)
-                 : 1;
-  if (s.splits < 1) s.splits = 1;
-  return s;
-}
-
-hipError_t launch_wgrad(const WgradArgs &a, const WgradShape &s,
+hipError_t launch_wgrad(const WgradArgs &a, const WgradGrid &g,
                         hipStream_t stream) {
-  const int tiles_i =
-      static_cast<int>(((a.fin > 0 ? a.fin : 1) + s.tile_i - 1) / s.tile_i);
-  const int grid = static_cast<int>(s.tiles * s.splits);
-  if (grid == 0) return hipSuccess;
-  const hipError_t e = with_type(a.type, [&](auto d) {
-    k_wgrad<decltype(d)::value, kTileO, kTileI, 2, 2, kStep>
-        <<<grid, 256, 0, stream>>>(a, tiles_i, static_cast<int>(s.tiles),
-                                   s.per_split);
-    return hipGetLastError();
-  });
-  if (e != hipSuccess || s.splits == 1) return e;
-  const int64_t n = a.fout * a.fin + (a.db ? a.fout : 0);
-  const int64_t blocks = (n + 255) / 256;
-  k_wgrad_join<<<static_cast<int>(blocks < 65536 ? blocks : 65536), 256, 0,
-                 stream>>>(a, s.splits);
+  hipError_t e;
+  if (a.type == MTA_BF16) {
+    e = start<kBf16>(a, g, stream);
+  } else if (a.type == MTA_F32) {
+    e = start<kF32Split>(a, g, stream);
+  } else {
+    // one of the two finds that it is not wanted and ends
+    if (g.ranges > 0)
+      k_wgrad_range<<<g.ranges, 256, 0, stream>>>(
+          a, a.tokens * (a.ldq / MTA_CKPT_BLOCK));
+    e = start<kF16>(a, g, stream);
+    if (e == hipSuccess) e = start<kF16Split>(a, g, stream);
+  }
+  if (e != hipSuccess || g.cut == 0) return e;
+  k_wgrad_join<<<static_cast<int>(g.cut * (kTile / 16)), 256, 0, stream>>>(a,
+                                                                           g);
   return hipGetLastError();
 }
 
