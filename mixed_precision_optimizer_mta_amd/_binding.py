@@ -408,6 +408,8 @@ def mta_amp_step(handle, opt, d_amp, d_coef, stream=0):
 
 
 def _ckpt_table(tensors):
+    if len(tensors) == 1:
+        return mta_ckpt_tensor(*tensors[0])
     arr = (mta_ckpt_tensor * max(1, len(tensors)))()
     for i, t in enumerate(tensors):
         arr[i] = t

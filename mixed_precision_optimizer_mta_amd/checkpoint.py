@@ -22,23 +22,18 @@ from .torch_list import _G, _raw_stream
 BLOCK = B.MTA_CKPT_BLOCK
 
 
-class _on:
-    """The device of the tensors made current for a call, where it is not."""
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
-    def __init__(self, device):
-        self.device = device
 
-    def __enter__(self):
-        self.was = torch.cuda.current_device()
-        if self.device.index != self.was:
-            torch.cuda.set_device(self.device)
-        if _raw_stream is not None:
-            return _raw_stream(self.device.index)
-        return torch.cuda.current_stream(self.device).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.device.index != self.was:
-            torch.cuda.set_device(self.was)
+def _on_stream(index, call, *args):
+    """call(*args, stream) on the current stream of device `index`, made the
+    current device for the call where it is not."""
+    if _device() != index:
+        with torch.cuda.device(index):
+            return _on_stream(index, call, *args)
+    stream = _raw_stream(index) if _raw_stream is not None else \
+        torch.cuda.current_stream(index).cuda_stream
+    return call(*args, stream)
 
 
 def _check_type(t, what):
@@ -56,6 +51,8 @@ def _as_rows(t, what):
         raise ValueError(f"{what} needs at least one dimension")
     cols = t.shape[-1]
     rows = t.numel() // cols if cols else 0
+    if rows and t.is_contiguous():
+        return rows, cols, cols
     if rows == 0:
         return 0, cols, max(1, cols)
     if cols > 1 and t.stride(-1) != 1:
@@ -89,12 +86,12 @@ class Checkpoint8:
     e4m3 codes), ``scale`` (uint8 [rows, blocks of 32], biased exponents),
     the tensor's ``shape`` and ``dtype``."""
 
-    __slots__ = ("q", "scale", "shape", "dtype")
+    __slots__ = ("_q", "_scale", "shape", "dtype", "rows", "blocks")
 
     def __init__(self, q, scale, shape, dtype=torch.float32):
-        self.q, self.scale, self.dtype = q, scale, dtype
+        self._q, self._scale, self.dtype = q, scale, dtype
         self.shape = shape = tuple(shape)
-        rows, blocks = self._layout(shape)
+        self.rows, self.blocks = rows, blocks = self._layout(shape)
         if q.dtype != torch.uint8 or scale.dtype != torch.uint8:
             raise TypeError("q and scale are uint8")
         if dtype not in _G:
@@ -120,25 +117,38 @@ class Checkpoint8:
     def empty(cls, shape, dtype, device):
         """A checkpoint with room for a tensor, its contents not set.  One
         allocation holds the codes, then the scales."""
-        rows, blocks = cls._layout(shape)
-        n = rows * blocks
-        buf = torch.empty(n * (BLOCK + 1), dtype=torch.uint8, device=device)
         self = cls.__new__(cls)
-        self.q = buf[:n * BLOCK]
-        self.scale = buf[n * BLOCK:]
+        self.rows, self.blocks = cls._layout(shape)
+        self._q = torch.empty(self.rows * self.blocks * (BLOCK + 1),
+                              dtype=torch.uint8, device=device)
+        self._scale = None
         self.shape, self.dtype = tuple(shape), dtype
         return self
 
     @property
-    def device(self):
-        return self.q.device
+    def q(self):
+        if self._scale is None:
+            return self._q[:self.rows * self.blocks * BLOCK]
+        return self._q
 
     @property
-    def rows(self):
-        return self._layout(self.shape)[0]
+    def scale(self):
+        if self._scale is None:
+            return self._q[self.rows * self.blocks * BLOCK:]
+        return self._scale
+
+    @property
+    def device(self):
+        return self._q.device
+
+    def pointers(self):
+        """The addresses of the codes and of the scales."""
+        q = self._q.data_ptr()
+        return q, (q + self.rows * self.blocks * BLOCK
+                   if self._scale is None else self._scale.data_ptr())
 
     def nbytes(self):
-        return self.q.numel() + self.scale.numel()
+        return self.rows * self.blocks * (BLOCK + 1)
 
     def unpack(self, dtype=None):
         return ckpt_unpack(self, dtype)
@@ -167,10 +177,8 @@ def _pack(tensors, act):
         cks.append(ck)
         ys.append(y)
         entries.append((t.data_ptr(), None if y is None else y.data_ptr(),
-                        ck.q.data_ptr(), ck.scale.data_ptr(), rows, cols, ld,
-                        cols))
-    with _on(dev) as stream:
-        B.mta_ckpt_pack(entries, _G[dt], code, stream)
+                        *ck.pointers(), rows, cols, ld, cols))
+    _on_stream(dev.index, B.mta_ckpt_pack, entries, _G[dt], code)
     return cks, ys
 
 
@@ -197,14 +205,13 @@ def ckpt_unpack(ck, dtype=None):
     dev = cks[0].device
     outs, entries = [], []
     for c in cks:
-        _same_device(dev, c.q)
+        _same_device(dev, c)
         y = torch.empty(c.shape, dtype=dt, device=dev)
         cols = c.shape[-1]
         outs.append(y)
-        entries.append((None, y.data_ptr(), c.q.data_ptr(),
-                        c.scale.data_ptr(), c.rows, cols, cols, cols))
-    with _on(dev) as stream:
-        B.mta_ckpt_unpack(entries, _G[dt], stream)
+        entries.append((None, y.data_ptr(), *c.pointers(), c.rows, cols, cols,
+                        cols))
+    _on_stream(dev.index, B.mta_ckpt_unpack, entries, _G[dt])
     return outs
 
 
@@ -226,11 +233,9 @@ def ckpt_act_backward(ck, dy, act):
                          f"{ck.shape}")
     rows, cols, ld = _as_rows(dy, "dy")
     dx = torch.empty(ck.shape, dtype=dy.dtype, device=dy.device)
-    with _on(dy.device) as stream:
-        B.mta_ckpt_act_backward(
-            [(dy.data_ptr(), dx.data_ptr(), ck.q.data_ptr(),
-              ck.scale.data_ptr(), rows, cols, ld, cols)],
-            _G[dy.dtype], code, stream)
+    _on_stream(dy.device.index, B.mta_ckpt_act_backward,
+               [(dy.data_ptr(), dx.data_ptr(), *ck.pointers(), rows, cols, ld,
+                 cols)], _G[dy.dtype], code)
     return dx
 
 
@@ -271,14 +276,14 @@ def ckpt_wgrad(ck, dy, bias=True, out=None, out_bias=None, accumulate=False,
                  or not out_bias.is_contiguous()):
         raise ValueError(f"out_bias is [{fout}], contiguous, of out's dtype")
     gt = _G[dy.dtype]
-    with _on(dev) as stream:
-        need = B.mta_ckpt_wgrad_workspace(tokens, fin, fout, gt)
-        ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        B.mta_ckpt_wgrad(B.mta_ckpt_wgrad_args(
-            ck.q.data_ptr(), ck.scale.data_ptr(), dy.data_ptr(),
-            out.data_ptr(), out_bias.data_ptr() if bias else None,
-            ws.data_ptr() if need else None, need, tokens, fin, fout, lddy,
-            lddw, gt, _G[dtype], 1 if accumulate else 0, 0), stream)
+    need = _on_stream(dev.index, lambda *x: B.mta_ckpt_wgrad_workspace(
+        *x[:-1]), tokens, fin, fout, gt)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    _on_stream(dev.index, B.mta_ckpt_wgrad, B.mta_ckpt_wgrad_args(
+        *ck.pointers(), dy.data_ptr(), out.data_ptr(),
+        out_bias.data_ptr() if bias else None,
+        ws.data_ptr() if need else None, need, tokens, fin, fout, lddy, lddw,
+        gt, _G[dtype], 1 if accumulate else 0, 0))
     return out, out_bias
 
 

@@ -51,9 +51,9 @@ struct Stage {
   static constexpr int kType =
       M == kBf16 ? MTA_BF16 : M == kF32Split ? MTA_F32 : MTA_F16;
   static constexpr int kTerms = M == kF32Split ? 3 : M == kF16Split ? 2 : 1;
-  // Two buffers of 18 KiB and 9 for each term, 64 accumulators and up to 104
-  // other registers a lane.
-  static constexpr int kWavesPerSimd = 4 - kTerms;
+  // Two buffers of 10 KiB and 10 for each term; three, two and two workgroups
+  // of 168, 256 and 256 registers a lane.
+  static constexpr int kWavesPerSimd = kTerms == 1 ? 3 : 2;
   struct Operand {
     uint16_t at[kStep][kPitch];
   };
@@ -334,7 +334,10 @@ __global__ __launch_bounds__(kThreads)
   // this lane's place in a transposing load of 32 columns x 16 tokens
   const int tr = (lane / 32) * 8 + (lane % 16) / 4;
   const int tc = ((lane / 16) % 2) * 16 + (lane % 4) * 4;
-  s16x8 fo[2][kTerms][2], fi[2][2];
+  // the next round's operands beside this one's, but for three terms, whose
+  // second sums have the registers
+  constexpr int kSets = kTerms == 3 ? 1 : 2;
+  s16x8 fo[kSets][kTerms][2], fi[kSets][2];
   const auto read = [&](const typename K::Buffer &b, int k, int set) {
 #pragma unroll
     for (int v = 0; v < 2; ++v)
@@ -359,10 +362,12 @@ __global__ __launch_bounds__(kThreads)
     __syncthreads();
     const auto step = [&](int s, typename K::Buffer &b, typename K::Buffer &next,
                           Raw &x, auto steady) {
-      read(b, 0, 0);
+      if constexpr (kSets == 2) read(b, 0, 0);
 #pragma unroll
       for (int k = 0; k < kRounds; ++k) {
-        if (k + 1 < kRounds) read(b, k + 1, (k + 1) & 1);
+        const int set = k % kSets;
+        if constexpr (kSets == 1) read(b, k, 0);
+        else if (k + 1 < kRounds) read(b, k + 1, (k + 1) % kSets);
 #pragma unroll
         for (int t = kTerms - 1; t >= 0; --t)
 #pragma unroll
@@ -370,7 +375,7 @@ __global__ __launch_bounds__(kThreads)
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
               f32x16 &sum = acc[t == 0 ? 0 : kSums - 1][m][v];
-              sum = multiply<M>(fo[k & 1][t][m], fi[k & 1][v], sum);
+              sum = multiply<M>(fo[set][t][m], fi[set][v], sum);
             }
         if (k == 0) {
           if (decltype(steady)::value || s + 1 < n) stage(next, x, with_bias);

@@ -13,7 +13,7 @@ from collections import namedtuple
 import torch
 
 from . import _binding as B
-from .checkpoint import _as_rows, _check_type, _on, _same_device
+from .checkpoint import _as_rows, _check_type, _on_stream, _same_device
 from .torch_list import _G
 
 #: stats: float32 [3] on the device, (loss, sum w kl, sum of the weights of
@@ -60,12 +60,10 @@ def _run(logits, actions, old_logp, advantages, weights, ref_logp, clip_low,
             dlogits, ldd = out, _as_rows(out, "out")[2]
     # one allocation: partial sums, what is saved, logp, stats
     need = B.mta_policy_loss_workspace(rows)
-    kept = 16 * rows if save else 0
-    buf = torch.empty(need + kept + 4 * rows + 16, dtype=torch.uint8,
-                      device=dev)
+    at_saved = need // 4
+    at_logp = at_saved + (4 * rows if save else 0)
+    buf = torch.empty(at_logp + rows + 3, dtype=f32, device=dev)
     base = buf.data_ptr()
-    logp = buf[need + kept:need + kept + 4 * rows].view(f32)
-    stats = buf[need + kept + 4 * rows:][:12].view(f32)
     args = B.mta_policy_args(
         logits.data_ptr(), _vector(actions, torch.int64, rows, dev, "actions"),
         _vector(old_logp, f32, rows, dev, "old_logp"),
@@ -74,13 +72,15 @@ def _run(logits, actions, old_logp, advantages, weights, ref_logp, clip_low,
         _vector(ref_logp, f32, rows, dev, "ref_logp"),
         _scalar(grad_scale, dev),
         None if dlogits is None else dlogits.data_ptr(),
-        base + need if save else None, base + need + kept,
-        base + need + kept + 4 * rows, base, need, rows, vocab, ld, ldd,
+        base + 4 * at_saved if save else None, base + 4 * at_logp,
+        base + 4 * (at_logp + rows), base, need, rows, vocab, ld, ldd,
         clip_low, clip_high, kl_coef, _G[logits.dtype], 0)
-    with _on(dev) as stream:
-        B.mta_policy_loss(args, stream)
-    saved = buf[need:need + kept] if save else None
-    return PolicyLoss(stats, logp.view(logits.shape[:-1]), saved, dlogits)
+    _on_stream(dev.index, B.mta_policy_loss, args)
+    logp = buf[at_logp:at_logp + rows]
+    if logits.dim() != 2:
+        logp = logp.view(logits.shape[:-1])
+    return PolicyLoss(buf[at_logp + rows:], logp,
+                      buf[at_saved:at_logp] if save else None, dlogits)
 
 
 def policy_loss_grad(logits, actions, old_logp, advantages, weights=None,
@@ -112,7 +112,8 @@ def policy_loss_backward(logits, actions, saved, grad_scale=None, out=None):
     _check_type(logits, "logits")
     rows, vocab, ld = _as_rows(logits, "logits")
     dev = logits.device
-    if saved.numel() != 16 * rows or saved.device != dev:
+    if saved.numel() != 4 * rows or saved.dtype != torch.float32 or \
+            saved.device != dev or not saved.is_contiguous():
         raise ValueError("saved is that of a forward over the same rows")
     if out is None:
         out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
@@ -125,8 +126,7 @@ def policy_loss_backward(logits, actions, saved, grad_scale=None, out=None):
         d_grad_scale=_scalar(grad_scale, dev), dlogits=out.data_ptr(),
         saved=saved.data_ptr(), rows=rows, vocab=vocab, ld=ld,
         ldd=_as_rows(out, "out")[2], type=_G[logits.dtype])
-    with _on(dev) as stream:
-        B.mta_policy_loss_backward(args, stream)
+    _on_stream(dev.index, B.mta_policy_loss_backward, args)
     return out
 
 

@@ -27,7 +27,7 @@ def activations(shape, dtype, seed=0, pad=0):
 
 
 def codes(ck):
-    rows, nb = ck._layout(ck.shape)
+    rows, nb = ck.rows, ck.blocks
     return (ck.q.cpu().numpy().reshape(rows, nb * 32),
             ck.scale.cpu().numpy().reshape(rows, nb))
 
