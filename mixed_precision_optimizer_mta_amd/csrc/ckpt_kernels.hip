@@ -1,11 +1,11 @@
 // ckpt_kernels.hip -- 8-bit activation checkpoints on gfx950: pack (with an
 // activation function's value), unpack, and the activation's backward.
 //
-// One kernel walks all three.  A lane takes eight consecutive columns (16
-// bytes of a 16-bit tensor), four neighbouring lanes share a block of 32 and
-// find its largest magnitude with two quad permutes; the scale is a power of
-// two, so its exponent comes from the bits of that magnitude and both the
-// scaling and the kept value are exact, and the only rounding is the
+// One kernel walks all three.  A lane takes 16 bytes of a tensor, eight
+// columns in 16 bits or four in 32; the four or eight neighbouring lanes of a
+// block of 32 find its largest magnitude with two or three permutes.  The scale
+// is a power of two, so its exponent comes from the bits of that magnitude and
+// both the scaling and the kept value are exact; the only rounding is the
 // hardware's nearest-even conversion to e4m3.
 //
 // Bound by HBM: 3.03 bytes move per element of a 16-bit pack or unpack, 5.03
@@ -73,14 +73,21 @@ __device__ __forceinline__ float act_slope(float x) {
   }
 }
 
-// The largest of the four lanes of a block.
-__device__ __forceinline__ float quad_max(float x) {
+// The largest of the four or eight lanes of a block.
+template <int Lanes>
+__device__ __forceinline__ float block_max(float x) {
   const int a = __builtin_amdgcn_mov_dpp(__float_as_int(x), 0xB1, 0xF, 0xF,
                                          false);  // lanes 1 0 3 2
   x = fmaxf(x, __int_as_float(a));
   const int b = __builtin_amdgcn_mov_dpp(__float_as_int(x), 0x4E, 0xF, 0xF,
                                          false);  // lanes 2 3 0 1
-  return fmaxf(x, __int_as_float(b));
+  x = fmaxf(x, __int_as_float(b));
+  if constexpr (Lanes == 8) {
+    const int c = __builtin_amdgcn_mov_dpp(__float_as_int(x), 0x141, 0xF, 0xF,
+                                           false);  // lanes 7 6 5 4 3 2 1 0
+    x = fmaxf(x, __int_as_float(c));
+  }
+  return x;
 }
 
 // The largest magnitude kept of a type: four significant bits below its
@@ -96,11 +103,17 @@ __device__ __forceinline__ uint32_t scale_byte(float top) {
   return static_cast<uint32_t>(max(b, 10));
 }
 
-// Where a lane's run of eight columns lies.
+// Where a lane's run of columns lies.
 struct Place {
   int64_t row;
   uint32_t col;   // first column
-  int valid;      // columns of it inside the tensor, 0..8
+  int valid;      // columns of it inside the tensor; -1: no run
+};
+
+// A run's codes: four to a word.
+template <int N>
+struct Codes {
+  typedef uint32_t type __attribute__((ext_vector_type(N / 4)));
 };
 
 template <int D, int Mode, int Act>
@@ -109,6 +122,8 @@ __global__ __launch_bounds__(kCkptThreads) void k_ckpt(const CkptList list) {
   uint32_t t = 0;
   while (t + 1 < list.count && blockIdx.x >= list.first[t + 1]) ++t;
   const CkptItem &it = list.item[t];
+  constexpr int kN = ckpt_unit(D), kLanes = MTA_CKPT_BLOCK / kN;
+  typedef typename Codes<kN>::type codes;
   const uint32_t lane = threadIdx.x;
   const uint64_t stride =
       uint64_t{list.first[t + 1] - list.first[t]} * kCkptChunk;
@@ -121,39 +136,39 @@ __global__ __launch_bounds__(kCkptThreads) void k_ckpt(const CkptList list) {
         flat ? 0 : static_cast<uint32_t>(base - row0 * it.row_units);
 
     Place at[kCkptUnroll];
-    Raw8<D> in[kCkptUnroll];
-    u32x2 code[kCkptUnroll];
+    Raw<D, kN> in[kCkptUnroll];
+    codes code[kCkptUnroll];
     uint32_t sb[kCkptUnroll];
     // every load of the chunk before any use
 #pragma unroll
     for (int j = 0; j < kCkptUnroll; ++j) {
       const uint64_t u = base + j * kCkptThreads + lane;
-      if (u >= it.units) {  // whole blocks of four lanes at a time
+      if (u >= it.units) {  // whole blocks at a time
         at[j].valid = -1;
         continue;
       }
       int64_t ex;
       if (flat) {
-        at[j] = Place{0, 0, 8};
-        ex = static_cast<int64_t>(u) * kCkptUnit;
+        at[j] = Place{0, 0, kN};
+        ex = static_cast<int64_t>(u) * kN;
       } else {
         const uint32_t o = off0 + j * kCkptThreads + lane;
         const uint32_t dr = o / it.row_units;
-        const uint32_t col = (o - dr * it.row_units) * kCkptUnit;
+        const uint32_t col = (o - dr * it.row_units) * kN;
         const int left = static_cast<int>(it.cols) - static_cast<int>(col);
         at[j].row = static_cast<int64_t>(row0 + dr);
         at[j].col = col;
-        at[j].valid = max(0, min(kCkptUnit, left));
+        at[j].valid = max(0, min(kN, left));
         ex = at[j].row * it.ldx + col;
       }
       if constexpr (Mode != kCkptUnpack) {
-        if (at[j].valid == kCkptUnit) in[j] = load8<D, true>(it.x, ex);
-        else in[j] = load8_part<D>(it.x, ex, at[j].valid, 0);
+        if (at[j].valid == kN) in[j] = load<D, kN, true>(it.x, ex);
+        else in[j] = load_part<D, kN>(it.x, ex, at[j].valid, 0);
       }
       if constexpr (Mode != kCkptPack) {
         code[j] = __builtin_nontemporal_load(
-            (const MTA_GLOBAL u32x2 *)(it.q) + u);
-        sb[j] = ((const MTA_GLOBAL uint8_t *)it.scale)[u / 4];
+            (const MTA_GLOBAL codes *)(it.q) + u);
+        sb[j] = ((const MTA_GLOBAL uint8_t *)it.scale)[u / kLanes];
       }
     }
 #pragma unroll
@@ -161,13 +176,13 @@ __global__ __launch_bounds__(kCkptThreads) void k_ckpt(const CkptList list) {
       if (at[j].valid < 0) continue;
       const uint64_t u = base + j * kCkptThreads + lane;
       const int64_t ey =
-          flat ? static_cast<int64_t>(u) * kCkptUnit
+          flat ? static_cast<int64_t>(u) * kN
                : at[j].row * it.ldy + at[j].col;
-      float out[8];
+      float out[kN];
       if constexpr (Mode == kCkptPack) {
-        float v[8], top = 0.0f;
+        float v[kN], top = 0.0f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < kN; ++k) {
           const float x = in[j][k];
           const float a = __builtin_fabsf(x);
           const bool fine = a < kInf;
@@ -176,11 +191,11 @@ __global__ __launch_bounds__(kCkptThreads) void k_ckpt(const CkptList list) {
                       : __builtin_nanf("");
           if constexpr (Act != MTA_ACT_NONE) out[k] = act_value<Act>(x);
         }
-        const uint32_t b = scale_byte(quad_max(fminf(top, kMost<D>)));
+        const uint32_t b = scale_byte(block_max<kLanes>(fminf(top, kMost<D>)));
         const float inv = __uint_as_float((254u - b) << 23);
-        uint32_t w[2];
+        codes w;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < kN / 4; ++h) {
           int c = __builtin_amdgcn_cvt_pk_fp8_f32(v[4 * h] * inv,
                                                   v[4 * h + 1] * inv, 0,
                                                   false);
@@ -188,13 +203,14 @@ __global__ __launch_bounds__(kCkptThreads) void k_ckpt(const CkptList list) {
                                               v[4 * h + 3] * inv, c, true);
           w[h] = static_cast<uint32_t>(c);
         }
-        ((MTA_GLOBAL u32x2 *)it.q)[u] = u32x2{w[0], w[1]};
-        if ((lane & 3) == 0)
-          ((MTA_GLOBAL uint8_t *)it.scale)[u / 4] = static_cast<uint8_t>(b);
+        ((MTA_GLOBAL codes *)it.q)[u] = w;
+        if (lane % kLanes == 0)
+          ((MTA_GLOBAL uint8_t *)it.scale)[u / kLanes] =
+              static_cast<uint8_t>(b);
       } else {
         const float s = __uint_as_float(sb[j] << 23);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < kN / 4; ++h) {
           const int c = static_cast<int>(code[j][h]);
           const f32x2 lo = __builtin_amdgcn_cvt_pk_f32_fp8(c, false);
           const f32x2 hi = __builtin_amdgcn_cvt_pk_f32_fp8(c, true);
@@ -204,7 +220,7 @@ __global__ __launch_bounds__(kCkptThreads) void k_ckpt(const CkptList list) {
           out[4 * h + 3] = hi[1] * s;
         }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < kN; ++k) {
           if constexpr (Mode == kCkptBackward)
             out[k] = in[j][k] * act_slope<Act>(out[k]);
           else if constexpr (D == MTA_F16)  // a NaN passes the comparisons
@@ -214,11 +230,11 @@ __global__ __launch_bounds__(kCkptThreads) void k_ckpt(const CkptList list) {
         }
       }
       if constexpr (Mode != kCkptPack || Act != MTA_ACT_NONE) {
-        if (at[j].valid == kCkptUnit) {
-          store8<D, true>(it.y, ey, out);
+        if (at[j].valid == kN) {
+          store<D, kN, true>(it.y, ey, out);
         } else {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
+          for (int k = 0; k < kN; ++k)
             if (k < at[j].valid) store_elem<D>(it.y, ey + k, out[k]);
         }
       }

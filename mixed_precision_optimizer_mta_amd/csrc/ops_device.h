@@ -61,11 +61,11 @@ __device__ __forceinline__ void store_elem(void *p, int64_t i, float x) {
   ((MTA_GLOBAL elem<D> *)p)[i] = narrow<D>(x);
 }
 
-// Eight consecutive elements as they lie in memory: 16 bytes of a 16-bit
-// type, 32 of float32.
-template <int D>
-struct Raw8 {
-  static constexpr int kWords = D == MTA_F32 ? 8 : 4;
+// N consecutive elements as they lie in memory, in words of 16 bytes.
+template <int D, int N>
+struct Raw {
+  static constexpr int kWords = D == MTA_F32 ? N : N / 2;
+  static_assert(kWords % 4 == 0, "whole 16-byte accesses");
   uint32_t w[kWords];
 
   __device__ __forceinline__ float operator[](int k) const {
@@ -75,6 +75,9 @@ struct Raw8 {
     else return widen<D>((k & 1 ? w[k / 2] >> 16 : w[k / 2]) & 0xFFFFu);
   }
 };
+
+template <int D>
+using Raw8 = Raw<D, 8>;
 
 // A 16-byte access at an element's address.  gfx950 serves it at any
 // alignment in one instruction, so rows of odd lengths need no element path.
@@ -89,14 +92,14 @@ struct Wide<MTA_F32> {
   typedef u32x4_at4 type;
 };
 
-template <int D, bool Stream>
-__device__ __forceinline__ Raw8<D> load8(const void *p, int64_t i) {
+template <int D, int N, bool Stream>
+__device__ __forceinline__ Raw<D, N> load(const void *p, int64_t i) {
   const auto *a =
       (const MTA_GLOBAL typename Wide<D>::type *)((const MTA_GLOBAL elem<D> *)p +
                                                   i);
-  Raw8<D> r;
+  Raw<D, N> r;
 #pragma unroll
-  for (int h = 0; h < Raw8<D>::kWords / 4; ++h) {
+  for (int h = 0; h < Raw<D, N>::kWords / 4; ++h) {
     const u32x4 v = Stream ? __builtin_nontemporal_load(a + h) : a[h];
 #pragma unroll
     for (int k = 0; k < 4; ++k) r.w[4 * h + k] = v[k];
@@ -104,13 +107,13 @@ __device__ __forceinline__ Raw8<D> load8(const void *p, int64_t i) {
   return r;
 }
 
-// The first n (0..7) of eight elements; the rest are `fill`.
-template <int D>
-__device__ __forceinline__ Raw8<D> load8_part(const void *p, int64_t i, int n,
-                                              uint32_t fill) {
-  Raw8<D> r;
+// The first n (below N) of N elements; the rest are `fill`.
+template <int D, int N>
+__device__ __forceinline__ Raw<D, N> load_part(const void *p, int64_t i, int n,
+                                               uint32_t fill) {
+  Raw<D, N> r;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
+  for (int k = 0; k < N; ++k) {
     uint32_t v = fill;
     if (k < n) {
       const auto e = ((const MTA_GLOBAL elem<D> *)p)[i + k];
@@ -134,12 +137,11 @@ __device__ __forceinline__ Raw8<D> fill8(uint32_t v) {
   return r;
 }
 
-template <int D, bool Stream>
-__device__ __forceinline__ void store8(void *p, int64_t i,
-                                       const float (&x)[8]) {
+template <int D, int N, bool Stream>
+__device__ __forceinline__ void store(void *p, int64_t i, const float (&x)[N]) {
   auto *a = (MTA_GLOBAL typename Wide<D>::type *)((MTA_GLOBAL elem<D> *)p + i);
 #pragma unroll
-  for (int h = 0; h < Raw8<D>::kWords / 4; ++h) {
+  for (int h = 0; h < Raw<D, N>::kWords / 4; ++h) {
     u32x4 v;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -149,6 +151,22 @@ __device__ __forceinline__ void store8(void *p, int64_t i,
     if constexpr (Stream) __builtin_nontemporal_store(v, a + h);
     else a[h] = v;
   }
+}
+
+// The same of eight elements.
+template <int D, bool Stream>
+__device__ __forceinline__ Raw8<D> load8(const void *p, int64_t i) {
+  return load<D, 8, Stream>(p, i);
+}
+template <int D>
+__device__ __forceinline__ Raw8<D> load8_part(const void *p, int64_t i, int n,
+                                              uint32_t fill) {
+  return load_part<D, 8>(p, i, n, fill);
+}
+template <int D, bool Stream>
+__device__ __forceinline__ void store8(void *p, int64_t i,
+                                       const float (&x)[8]) {
+  store<D, 8, Stream>(p, i, x);
 }
 
 // Calls f(std::integral_constant<int, T>) for the run-time element type.

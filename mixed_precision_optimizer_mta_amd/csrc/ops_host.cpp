@@ -190,7 +190,8 @@ int run_ckpt(const mta_ckpt_tensor *ts, int64_t count, int mode, int type,
       it.ldx = has_x ? t.ldx : t.cols;
       it.ldy = has_y ? t.ldy : t.cols;
       it.cols = static_cast<uint32_t>(t.cols);
-      it.row_units = static_cast<uint32_t>(blocks_of(t.cols) * 4);
+      it.row_units = static_cast<uint32_t>(
+          blocks_of(t.cols) * (MTA_CKPT_BLOCK / mta::ckpt_unit(type)));
       it.units = static_cast<uint64_t>(t.rows) * it.row_units;
       if (t.cols % MTA_CKPT_BLOCK == 0 &&
           (t.rows == 1 || (it.ldx == t.cols && it.ldy == t.cols)))

@@ -14,17 +14,19 @@ namespace mta {
 // ---- 8-bit checkpoints --------------------------------------------------
 
 constexpr int kCkptThreads = 256;
-constexpr int kCkptUnit = 8;    // elements a lane handles at a time
+// Elements a lane handles at a time, 16 bytes: a wave's accesses are then one
+// run of memory.
+constexpr int ckpt_unit(int type) { return type == MTA_F32 ? 4 : 8; }
 constexpr int kCkptUnroll = 4;  // units a lane has in flight
 constexpr int kCkptChunk = kCkptThreads * kCkptUnroll;  // units a workgroup
                                                         // handles at a time
 constexpr int kCkptTensors = 32;  // tensors in one launch (they travel in the
                                   // kernel's arguments, 4 KiB at most)
 
-// One tensor of a launch.  Its work is `units` runs of 8 columns, row by row
-// and `row_units` to a row (a multiple of 4, so that the four lanes of a
-// scale's block never part).  A tensor whose rows follow each other without
-// gaps and are whole blocks long is one row (flat).
+// One tensor of a launch.  Its work is `units` runs of ckpt_unit columns, row
+// by row and `row_units` to a row (whole blocks of them, so that the four or
+// eight lanes of a scale's block never part).  A tensor whose rows follow each
+// other without gaps and are whole blocks long is one row (flat).
 struct CkptItem {
   const void *x;
   void *y;

@@ -231,7 +231,7 @@ __global__ __launch_bounds__(kThreads)
   const uint32_t lane_s = static_cast<uint32_t>(
       col_i / MTA_CKPT_BLOCK - i0 / MTA_CKPT_BLOCK + row_i * pitch_s);
 
-  struct Raw {
+  struct Fetched {
     Raw8<D> o[kNO];
     u32x4 code;
     uint32_t scale;
@@ -239,7 +239,7 @@ __global__ __launch_bounds__(kThreads)
   float db[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 
   // A step that lies inside the tensors, loaded without a test.
-  const auto fetch = [&](int step, Raw &x) {
+  const auto fetch = [&](int step, Fetched &x) {
     const int64_t t = t0 + int64_t{step} * kStep;
 #pragma unroll
     for (int j = 0; j < kNO; ++j) {
@@ -261,7 +261,7 @@ __global__ __launch_bounds__(kThreads)
                 lane_s);
   };
   // Any step: what lies outside is zero.
-  const auto fetch_edge = [&](int step, Raw &x) {
+  const auto fetch_edge = [&](int step, Fetched &x) {
     const int64_t t = t0 + int64_t{step} * kStep;
     const int64_t left = a.fout - (o0 + co);
     const int n = static_cast<int>(left >= 8 ? 8 : left > 0 ? left : 0);
@@ -281,7 +281,7 @@ __global__ __launch_bounds__(kThreads)
       x.scale = ((const MTA_GLOBAL uint8_t *)a.scale)[at / MTA_CKPT_BLOCK];
     }
   };
-  const auto stage = [&](typename K::Buffer &b, const Raw &x, auto with_bias) {
+  const auto stage = [&](typename K::Buffer &b, const Fetched &x, auto with_bias) {
 #pragma unroll
     for (int j = 0; j < kNO; ++j) {
       uint32_t w[kTerms][4];
@@ -361,7 +361,7 @@ __global__ __launch_bounds__(kThreads)
     get(min(from + 2, to - 1), raw[1]);
     __syncthreads();
     const auto step = [&](int s, typename K::Buffer &b, typename K::Buffer &next,
-                          Raw &x, auto steady) {
+                          Fetched &x, auto steady) {
       if constexpr (kSets == 2) read(b, 0, 0);
 #pragma unroll
       for (int k = 0; k < kRounds; ++k) {
