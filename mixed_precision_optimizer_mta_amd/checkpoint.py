@@ -13,6 +13,11 @@ layer's weight and bias gradient, straight from the kept input, written to a
 new tensor or added into an existing gradient (the float32 ``p.grad`` that an
 MtaOptimizer's clip and step read, for one).  ``checkpointed_linear`` and
 ``checkpointed_act`` are the same as autograd functions.
+
+All of them may be captured into a HIP graph.  As with any autograd function,
+a backward pass is captured whole: capture the forward and its backward
+together, with no graph of an earlier eager forward over the same parameters
+still alive.
 """
 import torch
 
@@ -294,8 +299,10 @@ def ckpt_wgrad(ck, dy, bias=True, out=None, out_bias=None, accumulate=False,
 class _Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias):
-        ctx.ck = ckpt_pack(x) if ctx.needs_input_grad[1] or \
-            ctx.needs_input_grad[2] else None
+        _, need_w, need_b = ctx.needs_input_grad
+        # a bias alone needs no input: a checkpoint of no features
+        ctx.ck = ckpt_pack(_rows_or_copy(x)) if need_w else \
+            Checkpoint8.empty((*x.shape[:-1], 0), x.dtype, x.device)
         ctx.save_for_backward(weight)
         ctx.bias_dtype = None if bias is None else bias.dtype
         b = None if bias is None else bias.to(x.dtype)
@@ -305,24 +312,25 @@ class _Linear(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
         weight, = ctx.saved_tensors
-        dx = dw = db = None
-        if ctx.needs_input_grad[0]:
-            dx = dy.matmul(weight.to(dy.dtype))
-        if ctx.ck is not None:
-            dw, db = ckpt_wgrad(ctx.ck, _rows_or_copy(dy),
-                                bias=ctx.needs_input_grad[2],
-                                dtype=weight.dtype)
-            if not ctx.needs_input_grad[1]:
-                dw = None
-            if db is not None:
-                db = db.to(ctx.bias_dtype)
+        need_x, need_w, need_b = ctx.needs_input_grad
+        dx = dy.matmul(weight.to(dy.dtype)) if need_x else None
+        dw = db = None
+        if need_w or need_b:
+            # parameters of two dtypes: each rounded once, from float32
+            dtype = weight.dtype
+            if need_b and ctx.bias_dtype != dtype:
+                dtype = torch.float32
+            dw, db = ckpt_wgrad(ctx.ck, _rows_or_copy(dy), bias=need_b,
+                                dtype=dtype)
+            dw = dw.to(weight.dtype) if need_w else None
+            db = db.to(ctx.bias_dtype) if need_b else None
         return dx, dw, db
 
 
 class _Act(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, act):
-        y, ctx.ck = ckpt_act(x, act)
+        y, ctx.ck = ckpt_act(_rows_or_copy(x), act)
         ctx.act = act
         return y
 
@@ -336,7 +344,7 @@ def _rows_or_copy(t):
     """t, or a contiguous copy where its rows are not equally spaced (an
     expanded gradient, a transposed one)."""
     try:
-        _as_rows(t, "dy")
+        _as_rows(t, "a tensor")
         return t
     except ValueError:
         return t.contiguous()

@@ -111,9 +111,11 @@ __device__ __forceinline__ PolicyRow policy_row(const mta_policy_args &a,
   if (a.ref_logp) {
     const double d = double{in.ref_logp} - r.logp;
     const double e = exp_less_1(d);
-    kl = e - d;
-    loss += a.kl_coef * kl;
-    slope -= a.kl_coef * e;
+    kl = e > 1e300 ? e : e - d;  // (not infinity - infinity)
+    if (a.kl_coef != 0.0) {  // (0 * infinity)
+      loss += a.kl_coef * kl;
+      slope -= a.kl_coef * e;
+    }
   }
   r.coef = static_cast<float>(w * slope);
   r.sums[0] = w * loss;

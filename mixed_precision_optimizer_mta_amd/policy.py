@@ -58,11 +58,12 @@ def _run(logits, actions, old_logp, advantages, weights, ref_logp, clip_low,
                 raise ValueError("out has the logits' shape and dtype")
             _same_device(dev, out)
             dlogits, ldd = out, _as_rows(out, "out")[2]
-    # one allocation: partial sums, what is saved, logp, stats
+    # partial sums, then stats; what is handed out apart from them has its
+    # own storage
     need = B.mta_policy_loss_workspace(rows)
-    at_saved = need // 4
-    at_logp = at_saved + (4 * rows if save else 0)
-    buf = torch.empty(at_logp + rows + 3, dtype=f32, device=dev)
+    buf = torch.empty(need // 4 + 3, dtype=f32, device=dev)
+    logp = torch.empty(logits.shape[:-1], dtype=f32, device=dev)
+    saved = torch.empty(4 * rows, dtype=f32, device=dev) if save else None
     base = buf.data_ptr()
     args = B.mta_policy_args(
         logits.data_ptr(), _vector(actions, torch.int64, rows, dev, "actions"),
@@ -72,15 +73,11 @@ def _run(logits, actions, old_logp, advantages, weights, ref_logp, clip_low,
         _vector(ref_logp, f32, rows, dev, "ref_logp"),
         _scalar(grad_scale, dev),
         None if dlogits is None else dlogits.data_ptr(),
-        base + 4 * at_saved if save else None, base + 4 * at_logp,
-        base + 4 * (at_logp + rows), base, need, rows, vocab, ld, ldd,
+        saved.data_ptr() if save else None, logp.data_ptr(), base + need, base,
+        need, rows, vocab, ld, ldd,
         clip_low, clip_high, kl_coef, _G[logits.dtype], 0)
     _on_stream(dev.index, B.mta_policy_loss, args)
-    logp = buf[at_logp:at_logp + rows]
-    if logits.dim() != 2:
-        logp = logp.view(logits.shape[:-1])
-    return PolicyLoss(buf[at_logp + rows:], logp,
-                      buf[at_saved:at_logp] if save else None, dlogits)
+    return PolicyLoss(buf[need // 4:], logp, saved, dlogits)
 
 
 def policy_loss_grad(logits, actions, old_logp, advantages, weights=None,
@@ -136,7 +133,8 @@ class _Policy(torch.autograd.Function):
         r = policy_loss_forward(logits, actions, *args)
         ctx.save_for_backward(logits, actions, r.saved)
         ctx.mark_non_differentiable(r.logp)
-        return r.stats[0], r.logp
+        # (not a view: a caller may scale the loss in place)
+        return r.stats[0].clone(), r.logp
 
     @staticmethod
     @torch.autograd.function.once_differentiable

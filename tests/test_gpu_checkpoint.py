@@ -385,6 +385,51 @@ def test_float32_gradients_are_not_rounded_to_16_bits():
                 3 * 2.0 ** -24 * np.abs(want)).all()
 
 
+@pytest.mark.parametrize("dtype,low", [("bf16", -133), ("f16", -24),
+                                       ("f32", -149)])
+def test_products_are_exact_to_the_ends_of_the_range(dtype, low):
+    # one token: a result is one exact product, rounded to float32.  dy runs
+    # over its type's powers of two, subnormal ones included, and the kept
+    # values over scales of which the smallest is 2^-24 / 2^-9 (the last one
+    # exact in float16) and a few beyond float16's range on either side
+    dt = R.DTYPES[dtype]
+    top = 15 if dtype == "f16" else 127
+    dy = torch.tensor([[1.5 * 2.0 ** e for e in range(low + 1, top + 1)] +
+                       [2.0 ** low, 0.0, -2.0 ** low]],
+                      dtype=torch.float64).to(dt).cuda()
+    for ks in (range(-15, 8), (-117, -60, -16, 8, 40), (-117,)):
+        x = torch.zeros(1, 32 * len(ks))
+        for j, k in enumerate(ks):
+            x[0, 32 * j:32 * j + 32] = torch.tensor(
+                [448.0 if i == 0 else (1 + i % 8) * 2.0 ** -9 if i < 9 else
+                 float(i) for i in range(32)]) * 2.0 ** k
+        ck = M.ckpt_pack(x.cuda())
+        kept = R.to64(ck.unpack())
+        dw, db = M.ckpt_wgrad(ck, dy)
+        want = R.to64(dy).T @ kept
+        err = np.abs(R.to64(dw) - want)
+        fine = np.abs(want) < 2.0 ** 127
+        bound = 3 * 2.0 ** -24 * np.abs(want) + 2.0 ** -149
+        # a float32's third eight bits fall below 2^-133 from 2^-117 on: the
+        # products lose what lies under bfloat16's smallest value
+        if dtype == "f32":
+            bound = bound + 2.0 ** -133 * np.abs(kept)
+        assert (err <= bound)[fine].all(), (ks, err[fine].max())
+
+
+def test_zero_blocks_do_not_cost_float16_its_products():
+    # all-zero blocks (a relu's) beside ordinary ones, and tiny nonzero ones
+    x = activations((200, 96), torch.float16, 3)
+    x[:, 32:64] = 0
+    dy = torch.randn(200, 40, generator=gen(4)).half().cuda()
+    for tiny in (0.0, 1e-34):
+        y = x.float()
+        y[7, 40] = tiny
+        ck = M.ckpt_pack(y)
+        dw, db = M.ckpt_wgrad(ck, dy)
+        check_wgrad(dw, db, dy, R.to64(ck.unpack()))
+
+
 def test_wgrad_offsets_past_32_bits():
     # rows of dy 131,072 apart: the last start past 2^32 elements
     tokens, fin, fout, ld = 33000, 33, 24, 131072
@@ -524,6 +569,28 @@ def test_checkpointed_layers_have_the_formulas_gradients(wdtype):
     x2 = x.detach().requires_grad_()
     M.checkpointed_act(M.checkpointed_linear(x2, w, b), "relu").sum().backward()
     assert torch.isfinite(x2.grad).all()
+
+
+def test_layers_take_any_strides_and_parameter_types():
+    x = activations((12, 40, 32), torch.bfloat16).transpose(0, 1)
+    x.requires_grad_()
+    w = torch.randn(8, 32, generator=gen(1)).bfloat16().cuda()
+    b = torch.zeros(8, device="cuda")
+    w.requires_grad_(), b.requires_grad_()
+    y = M.checkpointed_act(M.checkpointed_linear(x, w, b).transpose(0, 1),
+                           "gelu")
+    assert y.shape == (12, 40, 8)
+    y.sum().backward()
+    assert x.grad.shape == x.shape and w.grad.dtype == torch.bfloat16
+    assert b.grad.dtype == torch.float32
+    # the same from contiguous tensors
+    x2 = x.detach().contiguous().requires_grad_()
+    w2, b2 = w.detach().clone().requires_grad_(), b.detach().clone()
+    b2.requires_grad_()
+    M.checkpointed_act(M.checkpointed_linear(x2, w2, b2), "gelu").sum(
+    ).backward()
+    # (the order of tokens in the sums is the same)
+    assert torch.equal(w2.grad, w.grad) and torch.equal(b2.grad, b.grad)
 
 
 def test_layers_skip_what_needs_no_gradient():

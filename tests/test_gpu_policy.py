@@ -230,6 +230,16 @@ def test_large_logits_keep_their_differences():
             assert abs(r.logp.item() + np.log(5000)) <= sum_error(5000)
 
 
+def test_no_kl_term_ignores_the_reference():
+    d = case(4, 300, "f32", 6, masked=0.0)
+    d["kw"]["kl_coef"] = 0.0
+    want = call(M.policy_loss_grad, {**d, "ref": None})
+    d["ref"][1] = float("inf")
+    got = call(M.policy_loss_grad, d)
+    assert torch.equal(got.dlogits, want.dlogits)
+    assert got.stats[0] == want.stats[0] and got.stats[1] == float("inf")
+
+
 def test_default_weights_and_the_border():
     z = torch.zeros(4, 8).cuda()
     a = torch.arange(4).cuda()
@@ -372,7 +382,9 @@ def test_autograd():
     loss, logp = M.policy_loss(z, d["a"], d["old"], d["adv"], d["w"],
                                d["ref"], 0.2, 0.3, 0.1)
     assert not logp.requires_grad
-    (loss * 1024.0).backward()
+    loss *= 1024.0
+    logp *= 1.0
+    loss.backward()
     check(d, M.PolicyLoss(call(M.policy_loss_forward, d).stats, logp, None,
                           z.grad), 1024.0)
 
