@@ -122,12 +122,18 @@ class Checkpoint8:
     def empty(cls, shape, dtype, device):
         """A checkpoint with room for a tensor, its contents not set.  One
         allocation holds the codes, then the scales."""
+        rows, blocks = cls._layout(shape)
+        return cls._of_storage(
+            torch.empty(rows * blocks * (BLOCK + 1), dtype=torch.uint8,
+                        device=device), tuple(shape), dtype)
+
+    @classmethod
+    def _of_storage(cls, storage, shape, dtype):
+        """The checkpoint that empty() made over `storage`."""
         self = cls.__new__(cls)
         self.rows, self.blocks = cls._layout(shape)
-        self._q = torch.empty(self.rows * self.blocks * (BLOCK + 1),
-                              dtype=torch.uint8, device=device)
-        self._scale = None
-        self.shape, self.dtype = tuple(shape), dtype
+        self._q, self._scale = storage, None
+        self.shape, self.dtype = shape, dtype
         return self
 
     @property
@@ -294,6 +300,9 @@ def ckpt_wgrad(ck, dy, bias=True, out=None, out_bias=None, accumulate=False,
 
 # --------------------------------------------------------------------------
 # autograd
+#
+# A checkpoint's storage is kept as a saved tensor, so that autograd frees it
+# with the graph's other buffers and saved-tensor hooks see it.
 # --------------------------------------------------------------------------
 
 class _Linear(torch.autograd.Function):
@@ -301,9 +310,10 @@ class _Linear(torch.autograd.Function):
     def forward(ctx, x, weight, bias):
         _, need_w, need_b = ctx.needs_input_grad
         # a bias alone needs no input: a checkpoint of no features
-        ctx.ck = ckpt_pack(_rows_or_copy(x)) if need_w else \
+        ck = ckpt_pack(_rows_or_copy(x)) if need_w else \
             Checkpoint8.empty((*x.shape[:-1], 0), x.dtype, x.device)
-        ctx.save_for_backward(weight)
+        ctx.kept = ck.shape, ck.dtype
+        ctx.save_for_backward(weight, ck._q)
         ctx.bias_dtype = None if bias is None else bias.dtype
         b = None if bias is None else bias.to(x.dtype)
         return torch.nn.functional.linear(x, weight.to(x.dtype), b)
@@ -311,7 +321,7 @@ class _Linear(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        weight, = ctx.saved_tensors
+        weight, storage = ctx.saved_tensors
         need_x, need_w, need_b = ctx.needs_input_grad
         dx = dy.matmul(weight.to(dy.dtype)) if need_x else None
         dw = db = None
@@ -320,8 +330,9 @@ class _Linear(torch.autograd.Function):
             dtype = weight.dtype
             if need_b and ctx.bias_dtype != dtype:
                 dtype = torch.float32
-            dw, db = ckpt_wgrad(ctx.ck, _rows_or_copy(dy), bias=need_b,
-                                dtype=dtype)
+            dw, db = ckpt_wgrad(
+                Checkpoint8._of_storage(storage, *ctx.kept),
+                _rows_or_copy(dy), bias=need_b, dtype=dtype)
             dw = dw.to(weight.dtype) if need_w else None
             db = db.to(ctx.bias_dtype) if need_b else None
         return dx, dw, db
@@ -330,14 +341,17 @@ class _Linear(torch.autograd.Function):
 class _Act(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, act):
-        y, ctx.ck = ckpt_act(_rows_or_copy(x), act)
-        ctx.act = act
+        y, ck = ckpt_act(_rows_or_copy(x), act)
+        ctx.save_for_backward(ck._q)
+        ctx.kept, ctx.act = (ck.shape, ck.dtype), act
         return y
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        return ckpt_act_backward(ctx.ck, _rows_or_copy(dy), ctx.act), None
+        storage, = ctx.saved_tensors
+        return ckpt_act_backward(Checkpoint8._of_storage(storage, *ctx.kept),
+                                 _rows_or_copy(dy), ctx.act), None
 
 
 def _rows_or_copy(t):

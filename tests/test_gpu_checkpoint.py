@@ -603,3 +603,52 @@ def test_layers_skip_what_needs_no_gradient():
     b = torch.zeros(8, device="cuda", requires_grad=True)
     M.checkpointed_linear(x.detach(), w, b).sum().backward()
     assert torch.equal(b.grad, torch.full((8,), 5.0).cuda())
+
+
+def test_a_backward_frees_the_checkpoints():
+    x = activations((64, 512), torch.bfloat16).requires_grad_()
+    w = torch.nn.Parameter(torch.randn(96, 512).bfloat16().cuda())
+    act = M.checkpointed_act(x, "relu")
+    lin = M.checkpointed_linear(x, w)
+    torch.autograd.grad(act, x, torch.ones_like(act), retain_graph=True)
+    for y, inputs in ((act, [x]), (lin, [x, w])):
+        before = torch.cuda.memory_allocated()
+        g = torch.autograd.grad(y, inputs, torch.ones_like(y))
+        del g
+        assert before - torch.cuda.memory_allocated() >= 64 * 512 * 33 // 32
+        with pytest.raises(RuntimeError, match="second time"):
+            torch.autograd.grad(y, inputs, torch.ones_like(y))
+
+
+def test_captured_layers_train_as_eager_ones():
+    """Forward and backward of both layers in one graph, the gradients in the
+    buffers that capture made, against eager passes after each replay."""
+    def grads(x, dy, w1, b1, w2):
+        y = M.checkpointed_linear(M.checkpointed_act(
+            M.checkpointed_linear(x, w1, b1), "gelu"), w2)
+        return torch.autograd.grad(y, [x, w1, b1, w2], dy)
+
+    def leaves(seed):
+        r = [(torch.randn(*s, generator=gen(seed + k)) * 0.2).bfloat16().cuda()
+             for k, s in enumerate(((256, 128), (64, 128), (64,), (96, 64)))]
+        return [t.requires_grad_() for t in r]
+
+    p = leaves(1)
+    dy = torch.randn(256, 96, generator=gen(9)).bfloat16().cuda()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        grads(p[0], dy, *p[1:])
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = grads(p[0], dy, *p[1:])
+    for seed in range(4):
+        q = leaves(20 + 10 * seed)
+        with torch.no_grad():
+            for a, b in zip(p, q):
+                a.copy_(b)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(got, grads(q[0], dy, *q[1:])):
+            assert torch.equal(a, b)
