@@ -86,6 +86,14 @@ def _same_device(device, *tensors):
             raise ValueError("the tensors of a call are on one device")
 
 
+def _written(*tensors):
+    """Tensors of the caller's that a call wrote: an autograd graph that saved
+    their old values refuses its backward, as after any in-place operation."""
+    for t in tensors:
+        if t is not None and not t.is_inference():
+            torch.autograd.graph.increment_version(t)
+
+
 class Checkpoint8:
     """A tensor kept in 8 bits: ``q`` (uint8 [rows, cols rounded up to 32],
     e4m3 codes), ``scale`` (uint8 [rows, blocks of 32], biased exponents),
@@ -275,6 +283,7 @@ def ckpt_wgrad(ck, dy, bias=True, out=None, out_bias=None, accumulate=False,
     if dtype not in _G:
         raise TypeError("gradients are float32, bfloat16 or float16")
     dev = dy.device
+    given = out, out_bias
     if out is None:
         out = torch.empty(fout, fin, dtype=dtype, device=dev)
     if bias and out_bias is None:
@@ -295,6 +304,7 @@ def ckpt_wgrad(ck, dy, bias=True, out=None, out_bias=None, accumulate=False,
         out_bias.data_ptr() if bias else None,
         ws.data_ptr() if need else None, need, tokens, fin, fout, lddy, lddw,
         gt, _G[dtype], 1 if accumulate else 0, 0))
+    _written(*given)
     return out, out_bias
 
 

@@ -13,7 +13,7 @@ from collections import namedtuple
 import torch
 
 from . import _binding as B
-from .checkpoint import _as_rows, _check_type, _on_stream, _same_device
+from .checkpoint import _as_rows, _check_type, _on_stream, _same_device, _written
 from .torch_list import _G
 
 #: stats: float32 [3] on the device, (loss, sum w kl, sum of the weights of
@@ -77,6 +77,7 @@ def _run(logits, actions, old_logp, advantages, weights, ref_logp, clip_low,
         need, rows, vocab, ld, ldd,
         clip_low, clip_high, kl_coef, _G[logits.dtype], 0)
     _on_stream(dev.index, B.mta_policy_loss, args)
+    _written(out)
     return PolicyLoss(buf[need // 4:], logp, saved, dlogits)
 
 
@@ -112,6 +113,7 @@ def policy_loss_backward(logits, actions, saved, grad_scale=None, out=None):
     if saved.numel() != 4 * rows or saved.dtype != torch.float32 or \
             saved.device != dev or not saved.is_contiguous():
         raise ValueError("saved is that of a forward over the same rows")
+    given = out
     if out is None:
         out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
     elif out.shape != logits.shape or out.dtype != logits.dtype:
@@ -124,6 +126,7 @@ def policy_loss_backward(logits, actions, saved, grad_scale=None, out=None):
         saved=saved.data_ptr(), rows=rows, vocab=vocab, ld=ld,
         ldd=_as_rows(out, "out")[2], type=_G[logits.dtype])
     _on_stream(dev.index, B.mta_policy_loss_backward, args)
+    _written(given)
     return out
 
 

@@ -389,6 +389,20 @@ def test_autograd():
                           z.grad), 1024.0)
 
 
+def test_a_graph_refuses_logits_overwritten_since():
+    d = case(6, 700, "bf16", 6)
+    z = d["z"].clone().requires_grad_()
+    y = z * 1.0
+    loss, _ = M.policy_loss(y, d["a"], d["old"], d["adv"])
+    call(M.policy_loss_grad, {**d, "z": y.detach()}, out=y.detach())
+    with pytest.raises(RuntimeError, match="modified by an inplace"):
+        loss.backward()
+    with torch.inference_mode():
+        t = d["z"].clone()
+        r = call(M.policy_loss_grad, {**d, "z": t}, out=t)
+    assert torch.equal(r.dlogits, call(M.policy_loss_grad, d).dlogits)
+
+
 def test_a_loss_scaled_step_of_an_output_layer():
     """Hidden states kept in 8 bits, float16 logits and their gradient times
     the device's loss scale, the weight gradient from the checkpoint, one
