@@ -171,7 +171,7 @@ __device__ __forceinline__ void store8(void *p, int64_t i,
 
 // Calls f(std::integral_constant<int, T>) for the run-time element type.
 template <typename F>
-auto with_type(int type, F &&f) {
+__host__ __device__ __forceinline__ auto with_type(int type, F &&f) {
   switch (type) {
     case MTA_BF16: return f(std::integral_constant<int, MTA_BF16>{});
     case MTA_F16: return f(std::integral_constant<int, MTA_F16>{});

@@ -363,20 +363,25 @@ int run_policy(const mta_policy_args *a, bool backward, void *stream,
 
 }  // namespace
 
-// A CU works through about one tile of kWgradTile^2 at a time, however many it
-// holds, so output tiles are dealt in rounds of one to a CU.  Whole rounds
-// take their tiles over all tokens; the tiles of a last, partial round (all of
-// them, when there are fewer than CUs) are cut along the tokens into the
-// number of parts for which rounds of parts, and the time to write the parts
-// and join them, are the shortest.  Measured in bfloat16: a step of a tile
-// takes 0.40 us of a CU that holds one workgroup, 0.365 with two and 0.32 with
-// three, starting and ending a workgroup 2 us, and a part of a tile 0.03 us of
-// the card's memory.  Against whole tiles this takes 454 us instead of 479 for
-// 1600 x 6400 outputs (2.5 rounds) over 16384 tokens, 80 instead of 116 for
-// 1600 x 1600 over 8192 and 78 instead of 398 for 768 x 768 over 32768; the
-// best of twelve numbers of parts was at most 5% faster in each.
+// Output tiles are dealt in rounds of one to a CU.  Whole rounds take their
+// tiles over all tokens; the tiles of a last, partial round (all of them, when
+// there are fewer than CUs) may be cut along the tokens into parts, whose sums
+// a second kernel joins, and when no CU gets more than one, a workgroup may
+// bring as many groups of waves as a CU holds, each with a share of the
+// tokens.  Taken is what these times, measured here, say is the shortest, in
+// us: 7 for a workgroup to start and end and 4 more to join its groups; a step
+// of a tile 0.37 of a CU that holds one workgroup, 0.285 with two, 0.27 with
+// more and 0.265 with groups (float32 dY: 1.1, 0.85, 0.85 and 0.75); 5 for the
+// second kernel and 0.015 a part for its bytes.  Against whole tiles by single
+// groups, in bfloat16: 423 us instead of 479 for 1600 x 6400 outputs (2.5
+// rounds) over 16384 tokens, 71 instead of 102 for 1600 x 1600 over 8192, 59
+// instead of 385 for 768 x 768 over 32768 (66 with parts alone), and 31
+// instead of 42 for 768 x 2304 over 1024 tokens of float32 dY.
 mta::WgradGrid mta::wgrad_grid(int64_t tokens, int64_t fin, int64_t fout,
                                int type, int cus) {
+  static constexpr double kStepUs[2][4] = {{0.37, 0.285, 0.27, 0.265},
+                                           {1.1, 0.85, 0.85, 0.75}};
+  const double *step_us = kStepUs[type == MTA_F32];
   WgradGrid g{};
   g.tiles_o = (fout + kWgradTile - 1) / kWgradTile;
   // no input features: the bias gradient alone still takes a column of tiles
@@ -389,17 +394,20 @@ mta::WgradGrid mta::wgrad_grid(int64_t tokens, int64_t fin, int64_t fout,
   double best = 0.0;
   for (int64_t p = 1; g.cut > 0 && p <= 64 && (p == 1 || p * 4 <= steps);
        ++p) {
-    const int64_t rounds = (g.cut * p + cus - 1) / cus;
+    const int64_t groups = g.whole + g.cut * p;
+    const int64_t held = std::min<int64_t>((groups + cus - 1) / cus, 3);
     const int64_t each = (steps + p - 1) / p;
-    const int64_t held = (g.whole + g.cut * p + cus - 1) / cus;
-    const double step = held == 1 ? 0.40 : held == 2 ? 0.365 : 0.32;
-    const double us = static_cast<double>(rounds) *
-                          (2.0 + step * static_cast<double>(each)) +
-                      (p > 1 ? 4.0 + 0.03 * static_cast<double>(g.cut * p)
-                             : 0.0);
-    if (p == 1 || us < best) {
+    const double taken = static_cast<double>(
+        g.whole / cus * steps + (g.cut * p + cus - 1) / cus * each);
+    const double join =
+        p > 1 ? 5.0 + 0.015 * static_cast<double>(g.cut * p) : 0.0;
+    for (int grouped = 0; grouped <= (groups <= cus ? 1 : 0); ++grouped) {
+      const double us = (grouped ? 11.0 : 7.0) + join +
+                        step_us[grouped ? 3 : held - 1] * taken;
+      if ((p > 1 || grouped) && us >= best) continue;
       best = us;
       g.parts = static_cast<int>(p);
+      g.grouped = grouped;
     }
   }
   if (g.parts == 1) {

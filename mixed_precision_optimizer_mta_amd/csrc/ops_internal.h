@@ -65,6 +65,7 @@ struct WgradGrid {
   int64_t part_tokens;
   int parts;
   int ranges;  // workgroups that look at the scales (float16 dy)
+  int grouped;  // workgroups of as many waves as a CU holds
 };
 
 WgradGrid wgrad_grid(int64_t tokens, int64_t fin, int64_t fout, int type,

@@ -24,7 +24,10 @@
 // that one's reads run under another's products: 8192 tokens of 4096 x 4096 in
 // bfloat16 at 890 TFLOP/s, against 820 to 880 for one workgroup of 256 x 256
 // with the same inner loop, whose eight waves keep step, and 800 without the
-// order that sched_group_barrier asks for.
+// order that sched_group_barrier asks for.  A tile's sums are written with all
+// tests of types outside and, when added to the gradient, with 32 old values
+// on their way at once: one after the other they cost 8 us a workgroup (4
+// steps of tokens 16.3 us, now 8.5; 1024 tokens, 768 -> 2304, 27.0, now 19.4).
 #include "ops_device.h"
 
 namespace mta {
@@ -179,14 +182,20 @@ __global__ __launch_bounds__(256) void k_wgrad_range(const WgradArgs a,
   if (threadIdx.x == 0) a.range[blockIdx.x] = fine;
 }
 
-template <int M>
-__global__ __launch_bounds__(kThreads)
+// Groups > 1: so many times the waves work on a tile, each group of four on
+// its own share of the tokens with its own LDS buffers, and are joined in LDS
+// at the end.
+template <int M, int Groups>
+__global__ __launch_bounds__(kThreads * Groups)
     __attribute__((amdgpu_waves_per_eu(Stage<M>::kWavesPerSimd))) void
     k_wgrad(const WgradArgs a, const WgradGrid g) {
   using K = Stage<M>;
   constexpr int D = K::kType, kTerms = K::kTerms;
   constexpr int kRounds = kStep / 16;
-  const int tid = threadIdx.x, lane = tid % 64;
+  const int group =
+      Groups == 1 ? 0
+                  : __builtin_amdgcn_readfirstlane(threadIdx.x / kThreads);
+  const int tid = threadIdx.x % kThreads, lane = tid % 64;
   const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
 
   if constexpr (M == kF16 || M == kF16Split) {
@@ -210,9 +219,9 @@ __global__ __launch_bounds__(kThreads)
   tile_at(g, tile, o0, i0);
   const int64_t t0 = cut ? part * g.part_tokens : 0;
   const int64_t t1 = cut ? min(a.tokens, t0 + g.part_tokens) : a.tokens;
-  const int steps = static_cast<int>((t1 - t0 + kStep - 1) / kStep);
 
-  __shared__ typename K::Buffer buf[2];
+  __shared__ typename K::Buffer bufs[Groups][2];
+  auto &buf = bufs[group];
 
   // A lane stages eight columns of dY in tokens row_o and row_o + 16, and
   // sixteen of the checkpoint in token row_i.
@@ -408,45 +417,126 @@ __global__ __launch_bounds__(kThreads)
   };
   const bool bias = a.db && i0 == 0;
   const bool inside = (o0 + kTile <= a.fout || a.fout % 8 == 0) && a.ldq > 0;
-  const int inner = inside ? static_cast<int>((t1 - t0) / kStep) : 0;
+  // Every group takes the same number of steps that lie inside, then the same
+  // number of others, some of them past the end.
+  const int steps = static_cast<int>((t1 - t0 + kStep - 1) / kStep);
+  const int inner = inside ? static_cast<int>((t1 - t0) / kStep / Groups) : 0;
+  const int outer = (steps - inner * Groups + Groups - 1) / Groups;
+  const int from = group * inner, edge = inner * Groups + group * outer;
   if (bias) {
-    run(0, inner, fetch, std::true_type{});
-    run(inner, steps, fetch_edge, std::true_type{});
+    run(from, from + inner, fetch, std::true_type{});
+    run(edge, edge + outer, fetch_edge, std::true_type{});
   } else {
-    run(0, inner, fetch, std::false_type{});
-    run(inner, steps, fetch_edge, std::false_type{});
+    run(from, from + inner, fetch, std::false_type{});
+    run(edge, edge + outer, fetch_edge, std::false_type{});
+  }
+  if constexpr (kSums == 2) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int v = 0; v < 2; ++v) acc[0][x][v] += acc[1][x][v];
+  }
+  // the groups' sums joined in order
+  if constexpr (Groups > 1) {
+    f32x4 *at = (f32x4 *)&bufs[0][0];
+    static_assert(sizeof bufs >= kTile * kTile * 4, "a tile fits");
+#pragma unroll
+    for (int u = 1; u < Groups; ++u) {
+      if (group == u) {
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          const f32x16 &c = acc[0][q / 8][q / 4 % 2];
+          const int r = q % 4 * 4;
+          at[q * kThreads + tid] = f32x4{c[r], c[r + 1], c[r + 2], c[r + 3]};
+        }
+      }
+      __syncthreads();
+      if (group == 0) {
+#pragma unroll
+        for (int q = 0; q < 16; ++q) {
+          const f32x4 y = at[q * kThreads + tid];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            acc[0][q / 8][q / 4 % 2][q % 4 * 4 + k] += y[k];
+        }
+      }
+      __syncthreads();
+    }
   }
 
   // D[o][i]: lane % 32 is the column i, the rows o are 4 (lane / 32) +
   // r % 4 + 8 (r / 4).  A part's tile goes to the workspace whole.
-  float *out = cut ? a.part + ((tile - g.whole) * g.parts + part) *
-                                  int64_t{kTile * kTile}
-                   : nullptr;
+  if (group == 0) {
+    const auto row = [](int x, int r) { return x * 32 + r % 4 + 8 * (r / 4); };
+    const int64_t o1 = o0 + wo + (lane / 32) * 4, i1 = i0 + wi + lane % 32;
+    if (cut) {
+      float *out = a.part + ((tile - g.whole) * g.parts + part) *
+                                int64_t{kTile * kTile};
+      const int first = (wo + (lane / 32) * 4) * kTile + wi + lane % 32;
 #pragma unroll
-  for (int x = 0; x < 2; ++x)
+      for (int x = 0; x < 2; ++x)
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const int i = wi + v * 32 + lane % 32;
+        for (int v = 0; v < 2; ++v)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int o = wo + x * 32 + (lane / 32) * 4 + r % 4 + 8 * (r / 4);
-        float y = acc[0][x][v][r];
-        if constexpr (kSums == 2) y += acc[1][x][v][r];
-        if (cut)
-          out[o * kTile + i] = y;
-        else if (o0 + o < a.fout && i0 + i < a.fin)
-          put(a.dw, (o0 + o) * a.lddw + i0 + i, y, a.gtype, a.accumulate);
-      }
+          for (int r = 0; r < 16; ++r)
+            out[first + row(x, r) * kTile + v * 32] = acc[0][x][v][r];
+    } else {
+      const auto write = [&](auto type, auto whole) {
+        constexpr int T = decltype(type)::value;
+        const int64_t place = (lane / 32 * 4 * a.lddw + lane % 32) *
+                              int64_t{sizeof(elem<T>)};
+        const auto at = [&](int x, int v, int r) {
+          return (void *)(scalar((const MTA_GLOBAL uint8_t *)a.dw +
+                                 ((o0 + wo + row(x, r)) * a.lddw + i0 + wi +
+                                  v * 32) *
+                                     int64_t{sizeof(elem<T>)}) +
+                          place);
+        };
+        const auto is = [&](int x, int v, int r) {
+          return decltype(whole)::value ||
+                 (o1 + row(x, r) < a.fout && i1 + v * 32 < a.fin);
+        };
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          // the old values of 32 sums before the first is stored: otherwise
+          // each load waits for the one before it
+          if (a.accumulate) {
+            float old[2][16];
+#pragma unroll
+            for (int v = 0; v < 2; ++v)
+#pragma unroll
+              for (int r = 0; r < 16; ++r)
+                old[v][r] = is(x, v, r) ? load_elem<T>(at(x, v, r), 0) : 0.0f;
+#pragma unroll
+            for (int v = 0; v < 2; ++v)
+#pragma unroll
+              for (int r = 0; r < 16; ++r) acc[0][x][v][r] += old[v][r];
+          }
+#pragma unroll
+          for (int v = 0; v < 2; ++v)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              if (is(x, v, r)) store_elem<T>(at(x, v, r), 0, acc[0][x][v][r]);
+        }
+      };
+      with_type(a.gtype, [&](auto type) {
+        if (o0 + kTile <= a.fout && i0 + kTile <= a.fin)
+          write(type, std::true_type{});
+        else
+          write(type, std::false_type{});
+      });
     }
+  }
   if (bias) {
     // a column's rows are joined in order
-    float *sum = (float *)&buf[0];
+    float *sum = (float *)&bufs[0][0];
+    const int row = group * kRowsO + row_o;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) sum[row_o * kTile + co + k] = db[k];
+    for (int k = 0; k < 8; ++k) sum[row * kTile + co + k] = db[k];
     __syncthreads();
-    if (tid < kTile && o0 + tid < a.fout) {
+    if (threadIdx.x < kTile && o0 + tid < a.fout) {
       float s = 0.0f;
-      for (int r = 0; r < kRowsO; ++r) s += sum[r * kTile + tid];
+      for (int r = 0; r < kRowsO * Groups; ++r) s += sum[r * kTile + tid];
       if (cut) a.part_db[part * a.fout + o0 + tid] = s;
       else put(a.db, o0 + tid, s, a.gtype, a.accumulate);
     }
@@ -465,26 +555,55 @@ __global__ __launch_bounds__(256) void k_wgrad_join(const WgradArgs a,
                    strip * 16 * kTile;
   f32x4 s[2] = {};
   const int at = threadIdx.x * 4;
-  for (int k = 0; k < g.parts; ++k)
+  const auto part = [&](int k, int j) {
+    return *(const MTA_GLOBAL f32x4 *)(p + k * int64_t{kTile * kTile} + at +
+                                       j * 1024);
+  };
+  int k = 0;
+  for (; k + 4 <= g.parts; k += 4) {  // four on their way at a time
+    f32x4 y[4][2];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) y[u][j] = part(k + u, j);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) s[j] += y[u][j];
+  }
+  for (; k < g.parts; ++k)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) s[j] += part(k, j);
+  with_type(a.gtype, [&](auto type) {
+    constexpr int T = decltype(type)::value;
+    const int64_t o = o0 + strip * 16 + at / kTile, i = i0 + at % kTile;
+    const auto is = [&](int j, int u) {
+      return o + j * 8 < a.fout && i + u < a.fin;
+    };
+    if (a.accumulate) {
+      f32x4 old[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          old[j][u] = is(j, u)
+                          ? load_elem<T>(a.dw, (o + j * 8) * a.lddw + i + u)
+                          : 0.0f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) s[j] += old[j];
+    }
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-      s[j] += *(const MTA_GLOBAL f32x4 *)(p + k * int64_t{kTile * kTile} + at +
-                                          j * 1024);
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int64_t o = o0 + strip * 16 + (at + j * 1024) / kTile;
-    const int64_t i = i0 + at % kTile;
-    if (o >= a.fout) continue;
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      if (i + k < a.fin)
-        put(a.dw, o * a.lddw + i + k, s[j][k], a.gtype, a.accumulate);
-  }
+      for (int u = 0; u < 4; ++u)
+        if (is(j, u))
+          store_elem<T>(a.dw, (o + j * 8) * a.lddw + i + u, s[j][u]);
+  });
   if (a.db && i0 == 0 && strip == 0 && threadIdx.x < kTile) {
     const int64_t o = o0 + threadIdx.x;
     if (o < a.fout) {
       float b = 0.0f;
-      for (int k = 0; k < g.parts; ++k) b += a.part_db[k * a.fout + o];
+      for (k = 0; k < g.parts; ++k) b += a.part_db[k * a.fout + o];
       put(a.db, o, b, a.gtype, a.accumulate);
     }
   }
@@ -492,8 +611,13 @@ __global__ __launch_bounds__(256) void k_wgrad_join(const WgradArgs a,
 
 template <int M>
 hipError_t start(const WgradArgs &a, const WgradGrid &g, hipStream_t stream) {
-  k_wgrad<M><<<static_cast<int>(g.whole + g.cut * g.parts), kThreads, 0,
-               stream>>>(a, g);
+  const int n = static_cast<int>(g.whole + g.cut * g.parts);
+  if (g.grouped) {
+    constexpr int kGroups = Stage<M>::kWavesPerSimd;
+    k_wgrad<M, kGroups><<<n, kThreads * kGroups, 0, stream>>>(a, g);
+  } else {
+    k_wgrad<M, 1><<<n, kThreads, 0, stream>>>(a, g);
+  }
   return hipGetLastError();
 }
 

@@ -300,6 +300,22 @@ def test_wgrad_shapes(tokens, fin, fout, dtype):
     assert torch.equal(again[0], dw) and torch.equal(again[1], db)
 
 
+@pytest.mark.parametrize("dtype", list(R.DTYPES))
+@pytest.mark.parametrize("tokens,fin,fout", [
+    (9001, 520, 260), (20011, 129, 200), (20000, 40, 8), (2051, 1601, 1602),
+    (2051, 1600, 1504)])
+def test_wgrad_of_many_tokens_and_few_outputs(tokens, fin, fout, dtype):
+    """Tiles cut along the tokens, and workgroups whose waves share them."""
+    ck, dy, kept = wgrad_case(tokens, fin, fout, R.DTYPES[dtype])
+    dw, db = M.ckpt_wgrad(ck, dy)
+    check_wgrad(dw, db, dy, kept)
+    again = M.ckpt_wgrad(ck, dy)
+    assert torch.equal(again[0], dw) and torch.equal(again[1], db)
+    old = torch.full_like(dw, 3.0), torch.full_like(db, -2.0)
+    M.ckpt_wgrad(ck, dy, out=old[0], out_bias=old[1], accumulate=True)
+    assert torch.equal(old[0], dw + 3.0) and torch.equal(old[1], db - 2.0)
+
+
 @pytest.mark.parametrize("gtype", list(R.DTYPES))
 @pytest.mark.parametrize("dtype", list(R.DTYPES))
 @pytest.mark.parametrize("tokens", [70, 3000])
