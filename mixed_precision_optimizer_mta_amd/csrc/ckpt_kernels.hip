@@ -126,10 +126,13 @@ __global__ __launch_bounds__(kCkptThreads) void k_ckpt(const CkptList list) {
   typedef typename Codes<kN>::type codes;
   const uint32_t lane = threadIdx.x;
   const uint64_t stride =
-      uint64_t{list.first[t + 1] - list.first[t]} * kCkptChunk;
+      uint64_t{list.first[t + 1] - list.first[t]} * it.chunk;
 
-  for (uint64_t base = uint64_t{blockIdx.x - list.first[t]} * kCkptChunk;
+  for (uint64_t base = uint64_t{blockIdx.x - list.first[t]} * it.chunk;
        base < it.units; base += stride) {
+    const uint64_t left = it.units - base;
+    const uint32_t end =
+        left < it.chunk ? static_cast<uint32_t>(left) : it.chunk;
     const bool flat = it.row_units == 0;
     const uint64_t row0 = flat ? 0 : base / it.row_units;
     const uint32_t off0 =
@@ -143,7 +146,7 @@ __global__ __launch_bounds__(kCkptThreads) void k_ckpt(const CkptList list) {
 #pragma unroll
     for (int j = 0; j < kCkptUnroll; ++j) {
       const uint64_t u = base + j * kCkptThreads + lane;
-      if (u >= it.units) {  // whole blocks at a time
+      if (j * kCkptThreads + lane >= end) {  // whole blocks at a time
         at[j].valid = -1;
         continue;
       }

@@ -17,9 +17,7 @@ constexpr int kCkptThreads = 256;
 // Elements a lane handles at a time, 16 bytes: a wave's accesses are then one
 // run of memory.
 constexpr int ckpt_unit(int type) { return type == MTA_F32 ? 4 : 8; }
-constexpr int kCkptUnroll = 4;  // units a lane has in flight
-constexpr int kCkptChunk = kCkptThreads * kCkptUnroll;  // units a workgroup
-                                                        // handles at a time
+constexpr int kCkptUnroll = 4;  // units a lane has in flight, at most
 constexpr int kCkptTensors = 32;  // tensors in one launch (they travel in the
                                   // kernel's arguments, 4 KiB at most)
 
@@ -36,6 +34,7 @@ struct CkptItem {
   uint64_t units;
   uint32_t cols;
   uint32_t row_units;  // 0: flat
+  uint32_t chunk;      // units a workgroup handles at a time
 };
 
 struct CkptList {
