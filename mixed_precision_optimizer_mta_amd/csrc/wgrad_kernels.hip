@@ -19,10 +19,10 @@
 //
 // Bound by the LDS and the matrix pipes together: a step of a workgroup, 32
 // tokens, is 32 KiB of transposing reads (which reach 128 bytes a clock here),
-// 16 KiB of writes (78), 16 loads a wave apart and 64 matrix instructions.  A
-// workgroup of four waves takes a tile of 128 x 128, and three share a CU, so
+// 16 KiB of writes (64 to 77), 16 loads of a wave and 32 matrix instructions.
+// A workgroup of four waves takes a tile of 128 x 128, and three share a CU, so
 // that one's reads run under another's products: 8192 tokens of 4096 x 4096 in
-// bfloat16 at 890 TFLOP/s, against 820 to 880 for one workgroup of 256 x 256
+// bfloat16 at 850 to 890 TFLOP/s, against 820 to 880 for one workgroup of 256^2
 // with the same inner loop, whose eight waves keep step, and 800 without the
 // order that sched_group_barrier asks for.  A tile's sums are written with all
 // tests of types outside and, when added to the gradient, with 32 old values
