@@ -19,6 +19,9 @@
     }                                     \
   } while (0)
 
+int san_wgrad_grid(int64_t tokens, int64_t fin, int64_t fout, int type,
+                   int cus);
+
 static uint64_t state = 88172645463325252ull;
 static uint64_t rnd(void) {
   state ^= state << 13;
@@ -97,16 +100,17 @@ int main(void) {
                                             256, &bytes);
     CHECK(rc == 0 ? bytes >= 0 : rc < 0 && bytes == 0, "workspace");
   }
-  /* workspaces of shapes that are taken */
-  for (int64_t t = 0; t < 70000; t = t * 3 + 1)
+  /* shapes that are taken: their workspace, and their grid */
+  for (int64_t t = 0; t < 300000; t = t * 3 + 1 + (int64_t)(rnd() % 2))
     for (int64_t i = 0; i < 9000; i = i * 2 + 5)
-      for (int64_t o = 1; o < 9000; o = o * 2 + 3)
+      for (int64_t o = 1; o < 60000; o = o * 2 + 3)
         for (int type = 0; type < 3; ++type) {
-          CHECK(mta_ckpt_wgrad_workspace(t, i, o, type, 1 + (int)(rnd() % 400),
-                                         &bytes) == 0 &&
-                    bytes % 16 == 0,
-                "workspace of %lld %lld %lld", (long long)t, (long long)i,
-                (long long)o);
+          const int cus = rnd() % 2 ? 256 : 1 + (int)(rnd() % 400);
+          const int bad = san_wgrad_grid(t, i, o, type, cus);
+          CHECK(mta_ckpt_wgrad_workspace(t, i, o, type, cus, &bytes) == 0 &&
+                    bytes % 16 == 0 && bad == 0,
+                "%lld %lld %lld on %d: %d", (long long)t, (long long)i,
+                (long long)o, cus, bad);
         }
 
   for (int n = 0; n < 20000; ++n) {

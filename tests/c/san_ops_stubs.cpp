@@ -29,3 +29,26 @@ hipError_t launch_policy_backward(const mta_policy_args &, hipStream_t) {
 }
 
 }  // namespace mta
+
+// Whether the weight gradient's grid covers its outputs and tokens once: all
+// tiles, and for the cut ones parts of which none is empty and the last ends
+// past the tokens.
+extern "C" int san_wgrad_grid(int64_t tokens, int64_t fin, int64_t fout,
+                              int type, int cus) {
+  const mta::WgradGrid g = mta::wgrad_grid(tokens, fin, fout, type, cus);
+  const int64_t t = mta::kWgradTile;
+  if (g.tiles_o != (fout + t - 1) / t) return 1;
+  if (g.tiles_i != (fin > 0 ? (fin + t - 1) / t : 1)) return 2;
+  if (g.whole < 0 || g.cut < 0 || g.whole + g.cut != g.tiles_o * g.tiles_i)
+    return 3;
+  if (g.cut == 0 ? g.parts != 1 : g.parts < 2) return 4;
+  if (g.part_tokens % mta::kWgradStep) return 5;
+  if (g.cut && (g.parts * g.part_tokens < tokens ||
+                (g.parts - 1) * g.part_tokens >= tokens))
+    return 6;
+  if (g.grouped && g.whole + g.cut * g.parts > cus) return 7;
+  if (g.ranges < 0 || g.ranges > mta::kWgradRanges ||
+      (g.ranges > 0) != (type == MTA_F16 && tokens > 0 && fin > 0))
+    return 8;
+  return 0;
+}
