@@ -315,6 +315,11 @@ def ckpt_wgrad(ck, dy, bias=True, out=None, out_bias=None, accumulate=False,
 # with the graph's other buffers and saved-tensor hooks see it.
 # --------------------------------------------------------------------------
 
+def _product(x, weight, bias):
+    b = None if bias is None else bias.to(x.dtype)
+    return torch.nn.functional.linear(x, weight.to(x.dtype), b)
+
+
 class _Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias):
@@ -325,8 +330,7 @@ class _Linear(torch.autograd.Function):
         ctx.kept = ck.shape, ck.dtype
         ctx.save_for_backward(weight, ck._q)
         ctx.bias_dtype = None if bias is None else bias.dtype
-        b = None if bias is None else bias.to(x.dtype)
-        return torch.nn.functional.linear(x, weight.to(x.dtype), b)
+        return _product(x, weight, bias)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
@@ -383,6 +387,8 @@ def checkpointed_linear(x, weight, bias=None):
     _check_type(weight, "weight")
     if weight.dim() != 2 or x.shape[-1] != weight.shape[1]:
         raise ValueError("weight is [fout, fin] with x's last dimension fin")
+    if not torch.is_grad_enabled():  # nothing to keep
+        return _product(x, weight, bias)
     return _Linear.apply(x, weight, bias)
 
 

@@ -621,6 +621,22 @@ def test_layers_skip_what_needs_no_gradient():
     assert torch.equal(b.grad, torch.full((8,), 5.0).cuda())
 
 
+def test_layers_without_gradients():
+    x = activations((70, 512), torch.bfloat16)
+    w = torch.nn.Parameter(torch.randn(96, 512).cuda())
+    b = torch.nn.Parameter(torch.randn(96).cuda())
+    want = M.checkpointed_linear(x, w, b)
+    with torch.no_grad():
+        y = M.checkpointed_linear(x, w, b)
+        a = M.checkpointed_act(y, "gelu")
+    assert want.requires_grad and not y.requires_grad and not a.requires_grad
+    assert torch.equal(y, want)
+    assert torch.equal(a, M.checkpointed_act(want, "gelu"))
+    with torch.inference_mode():
+        assert torch.equal(M.checkpointed_linear(x, w, b), want)
+        assert torch.equal(M.checkpointed_act(y, "gelu"), a)
+
+
 def test_a_backward_frees_the_checkpoints():
     # a saved tensor is freed by the backward that uses it (a second one then
     # refuses), and passes the hooks.  (The allocator's count right after a
