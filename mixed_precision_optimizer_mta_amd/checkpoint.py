@@ -192,7 +192,7 @@ def _pack(tensors, act):
         _same_device(dev, t)
         rows, cols, ld = _as_rows(t, "a kept tensor")
         ck = Checkpoint8.empty(t.shape, dt, dev)
-        y = None if act is None else torch.empty(t.shape, dtype=dt, device=dev)
+        y = None if act is None else t.new_empty(t.shape)
         cks.append(ck)
         ys.append(y)
         entries.append((t.data_ptr(), None if y is None else y.data_ptr(),
@@ -251,7 +251,7 @@ def ckpt_act_backward(ck, dy, act):
         raise ValueError(f"dy has shape {tuple(dy.shape)}, the checkpoint "
                          f"{ck.shape}")
     rows, cols, ld = _as_rows(dy, "dy")
-    dx = torch.empty(ck.shape, dtype=dy.dtype, device=dy.device)
+    dx = dy.new_empty(ck.shape)
     _on_stream(dy.device.index, B.mta_ckpt_act_backward,
                [(dy.data_ptr(), dx.data_ptr(), *ck.pointers(), rows, cols, ld,
                  cols)], _G[dy.dtype], code)

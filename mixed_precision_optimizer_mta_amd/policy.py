@@ -52,7 +52,7 @@ def _run(logits, actions, old_logp, advantages, weights, ref_logp, clip_low,
     dlogits, ldd = None, vocab
     if grad:
         if out is None:
-            dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+            dlogits = logits.new_empty(logits.shape)
         else:
             if out.shape != logits.shape or out.dtype != logits.dtype:
                 raise ValueError("out has the logits' shape and dtype")
@@ -62,7 +62,7 @@ def _run(logits, actions, old_logp, advantages, weights, ref_logp, clip_low,
     # own storage
     need = B.mta_policy_loss_workspace(rows)
     buf = torch.empty(need // 4 + 3, dtype=f32, device=dev)
-    logp = torch.empty(logits.shape[:-1], dtype=f32, device=dev)
+    logp = logits.new_empty(logits.shape[:-1], dtype=f32)
     saved = torch.empty(4 * rows, dtype=f32, device=dev) if save else None
     base = buf.data_ptr()
     args = B.mta_policy_args(
@@ -115,7 +115,7 @@ def policy_loss_backward(logits, actions, saved, grad_scale=None, out=None):
         raise ValueError("saved is that of a forward over the same rows")
     given = out
     if out is None:
-        out = torch.empty(logits.shape, dtype=logits.dtype, device=dev)
+        out = logits.new_empty(logits.shape)
     elif out.shape != logits.shape or out.dtype != logits.dtype:
         raise ValueError("out has the logits' shape and dtype")
     _same_device(dev, out)
