@@ -98,6 +98,27 @@ __device__ __forceinline__ void kept4(uint32_t code, float scale,
   }
 }
 
+// The run `n` elements (0 to 7) further on; its last n are anything.
+template <int D>
+__device__ __forceinline__ Raw8<D> slide(Raw8<D> x, int n) {
+  constexpr int kWords = Raw8<D>::kWords, kEach = 8 / kWords;
+#pragma unroll
+  for (int h = 4; h >= kEach; h /= 2) {
+    const int d = h / kEach;
+#pragma unroll
+    for (int k = 0; k < kWords; ++k)
+      x.w[k] = n & h ? x.w[k + d < kWords ? k + d : k] : x.w[k];
+  }
+  if constexpr (kEach == 2) {
+    const uint32_t bits = (n & 1) * 16;
+#pragma unroll
+    for (int k = 0; k < kWords; ++k)
+      x.w[k] = __builtin_amdgcn_alignbit(
+          x.w[k + 1 < kWords ? k + 1 : k], x.w[k], bits);
+  }
+  return x;
+}
+
 // Eight tokens of one column, from `p` in this lane's place.
 __device__ __forceinline__ s16x8 transposed(const uint16_t *p) {
   typedef __attribute__((address_space(3))) s16x4 lds4;
@@ -232,10 +253,13 @@ __global__ __launch_bounds__(kThreads * Groups)
   const int ci = tid % (kTile / 16) * 16, row_i = tid / (kTile / 16);
   const int64_t pitch_s = a.ldq / MTA_CKPT_BLOCK;
   // Columns past the last whole run are the last one's again: what comes of
-  // them is not written.
+  // them is not written.  A run that the last column ends inside is moved to
+  // its place when it is staged (loaded by elements instead, the last tiles
+  // of 1601 outputs made 8192 tokens of 1600 features take 120 us, not 80).
   const int64_t col_o = min(o0 + co, max(int64_t{0}, a.fout - 8));
   const int64_t col_i = min(i0 + ci, max(int64_t{0}, a.ldq - 16));
   const int64_t lane_o = (col_o - o0 + row_o * a.lddy) * int64_t{sizeof(elem<D>)};
+  const int behind = static_cast<int>(min(int64_t{7}, o0 + co - col_o));
   const uint32_t lane_i = static_cast<uint32_t>(col_i - i0 + row_i * a.ldq);
   const uint32_t lane_s = static_cast<uint32_t>(
       col_i / MTA_CKPT_BLOCK - i0 / MTA_CKPT_BLOCK + row_i * pitch_s);
@@ -290,18 +314,21 @@ __global__ __launch_bounds__(kThreads * Groups)
       x.scale = ((const MTA_GLOBAL uint8_t *)a.scale)[at / MTA_CKPT_BLOCK];
     }
   };
-  const auto stage = [&](typename K::Buffer &b, const Fetched &x, auto with_bias) {
+  const auto stage = [&](typename K::Buffer &b, const Fetched &x, auto with_bias,
+                         auto ragged) {
 #pragma unroll
     for (int j = 0; j < kNO; ++j) {
+      Raw8<D> dy = x.o[j];
+      if constexpr (decltype(ragged)::value) dy = slide<D>(dy, behind);
       uint32_t w[kTerms][4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         if constexpr (kTerms == 1) {
-          w[0][k] = x.o[j].w[k];
+          w[0][k] = dy.w[k];
         } else {
           uint32_t u[kTerms], v[kTerms];
-          split<kTerms>(x.o[j][2 * k], u);
-          split<kTerms>(x.o[j][2 * k + 1], v);
+          split<kTerms>(dy[2 * k], u);
+          split<kTerms>(dy[2 * k + 1], v);
 #pragma unroll
           for (int t = 0; t < kTerms; ++t) w[t][k] = (u[t] >> 16) | v[t];
         }
@@ -312,7 +339,7 @@ __global__ __launch_bounds__(kThreads * Groups)
             u32x4{w[t][0], w[t][1], w[t][2], w[t][3]};
       if constexpr (decltype(with_bias)::value) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) db[k] += x.o[j][k];
+        for (int k = 0; k < 8; ++k) db[k] += dy[k];
       }
     }
     const float s = __uint_as_float(x.scale << 23);
@@ -360,11 +387,12 @@ __global__ __launch_bounds__(kThreads * Groups)
 
   // Steps [from, to), each fetched by `get`.  While step s is multiplied, step
   // s + 1 goes to LDS and steps s + 2 and s + 3 are on their way.
-  const auto run = [&](int from, int to, auto &&get, auto with_bias) {
+  const auto run = [&](int from, int to, auto &&get, auto with_bias,
+                       auto ragged) {
     const int n = to - from;
     if (n <= 0) return;
     get(from, raw[0]);
-    stage(buf[0], raw[0], with_bias);
+    stage(buf[0], raw[0], with_bias, ragged);
     // (past the end: the last step again)
     get(min(from + 1, to - 1), raw[0]);
     get(min(from + 2, to - 1), raw[1]);
@@ -387,7 +415,7 @@ __global__ __launch_bounds__(kThreads * Groups)
               sum = multiply<M>(fo[set][t][m], fi[set][v], sum);
             }
         if (k == 0) {
-          if (decltype(steady)::value || s + 1 < n) stage(next, x, with_bias);
+          if (decltype(steady)::value || s + 1 < n) stage(next, x, with_bias, ragged);
           if (decltype(steady)::value || s + 3 < n) get(from + s + 3, x);
         }
         if constexpr (kTerms == 1) {
@@ -416,20 +444,20 @@ __global__ __launch_bounds__(kThreads * Groups)
     __syncthreads();
   };
   const bool bias = a.db && i0 == 0;
-  const bool inside = (o0 + kTile <= a.fout || a.fout % 8 == 0) && a.ldq > 0;
+  const bool inside = a.fout >= 8 && a.ldq > 0;
   // Every group takes the same number of steps that lie inside, then the same
   // number of others, some of them past the end.
   const int steps = static_cast<int>((t1 - t0 + kStep - 1) / kStep);
   const int inner = inside ? static_cast<int>((t1 - t0) / kStep / Groups) : 0;
   const int outer = (steps - inner * Groups + Groups - 1) / Groups;
   const int from = group * inner, edge = inner * Groups + group * outer;
-  if (bias) {
-    run(from, from + inner, fetch, std::true_type{});
-    run(edge, edge + outer, fetch_edge, std::true_type{});
-  } else {
-    run(from, from + inner, fetch, std::false_type{});
-    run(edge, edge + outer, fetch_edge, std::false_type{});
-  }
+  if (o0 + kTile > a.fout && a.fout % 8 != 0)
+    run(from, from + inner, fetch, std::true_type{}, std::true_type{});
+  else if (bias)
+    run(from, from + inner, fetch, std::true_type{}, std::false_type{});
+  else
+    run(from, from + inner, fetch, std::false_type{}, std::false_type{});
+  run(edge, edge + outer, fetch_edge, std::true_type{}, std::false_type{});
   if constexpr (kSums == 2) {
 #pragma unroll
     for (int x = 0; x < 2; ++x)
