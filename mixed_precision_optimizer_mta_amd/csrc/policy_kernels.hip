@@ -11,9 +11,12 @@
 //
 // Numerics: exponentials are 2^((z - max) log2 e) in float32, a lane sums at
 // most 64 (a streamed row: vocab / 1024) of them in float32, lanes are joined
-// in float32 within a wave and in float64 across waves.  What follows for a
-// row (its logp, ratio, clip, KL) is a handful of float64 operations of one
-// wave: exp(d) - d - 1 and 1 - p lose every digit of a float32 near 0.
+// in float32 within a wave and in float64 across waves.  The action's own
+// exponential stays out of that sum: where it is 1 and the others are small,
+// 1 - p is their sum, of which a float32 1 + sum keeps little or nothing.
+// What follows for a row (its logp, ratio, clip, KL) is a handful of float64
+// operations of one wave: exp(d) - d - 1 and 1 - p lose every digit of a
+// float32 near 0.
 #include "ops_device.h"
 
 namespace mta {
@@ -62,16 +65,18 @@ __device__ __forceinline__ double exp_less_1(double x) {
   return y;
 }
 
-// ln s in float64 for a normal s > 0: s = m 2^e with m in [1/sqrt 2, sqrt 2),
+// ln(1 + s) in float64 for s >= 0: 1 + s = m 2^e with m in [1/sqrt 2, sqrt 2),
 // ln m = 2 atanh t, t = (m - 1) / (m + 1), |t| < 0.172, its series to t^17.
-__device__ __forceinline__ double ln(double s) {
-  double m = __builtin_amdgcn_frexp_mant(s);
-  int e = __builtin_amdgcn_frexp_exp(s);
+// Where e is 0, m - 1 is s itself, with the digits that 1 + s rounds away.
+__device__ __forceinline__ double ln_plus_1(double s) {
+  double m = __builtin_amdgcn_frexp_mant(1.0 + s);
+  int e = __builtin_amdgcn_frexp_exp(1.0 + s);
   if (m < 0.70710678118654752) {
     m += m;
     --e;
   }
-  const double t = (m - 1.0) / (m + 1.0), u = t * t;
+  const double d = e == 0 ? s : m - 1.0;
+  const double t = d / (2.0 + d), u = t * t;
   double p = 2.0 / 17.0;
   p = __builtin_fma(p, u, 2.0 / 15.0);
   p = __builtin_fma(p, u, 2.0 / 13.0);
@@ -90,12 +95,15 @@ struct RowInputs {
   int64_t action;
 };
 
-// The row's scalars from its maximum and the sum of exp(z - max).
+// The row's scalars from its maximum, the sum of exp(z - max) over all entries
+// but the action's, and the action's own.  Where the action is the maximum its
+// own is exactly 1, so logp = -ln(1 + others) has every digit of `others`.
 __device__ __forceinline__ PolicyRow policy_row(const mta_policy_args &a,
                                                 const RowInputs &in, float za,
-                                                float top, double total) {
+                                                float top, double others,
+                                                float own) {
   PolicyRow r;
-  const double logtotal = ln(total);
+  const double logtotal = ln_plus_1(others + (double{own} - 1.0));
   r.lse = double{top} + logtotal;
   r.logp = (double{za} - double{top}) - logtotal;
   const double adv = in.advantage, w = in.w;
@@ -173,6 +181,20 @@ struct RowShared {
   float gain, chosen;
 };
 
+// A run with element k (the same in every lane) made -infinity.
+template <int D>
+__device__ __forceinline__ Raw8<D> without(Raw8<D> x, uint32_t k) {
+  constexpr int kEach = 8 / Raw8<D>::kWords;
+  const uint32_t bits = k % kEach * 16;
+  const uint32_t clear = kEach == 1 ? 0xFFFFFFFFu : 0xFFFFu << bits;
+#pragma unroll
+  for (int w = 0; w < Raw8<D>::kWords; ++w)
+    x.w[w] = w == static_cast<int>(k / kEach)
+                 ? (x.w[w] & ~clear) | kMinusInf<D> << bits
+                 : x.w[w];
+  return x;
+}
+
 // Runs of a streamed row that a lane has in flight.
 constexpr int kBatch = 4;
 
@@ -243,15 +265,28 @@ __global__ __launch_bounds__(Threads * kRows<Threads>,
       else z[j] = fill8<D>(kMinusInf<D>);
     }
   }
-  const float ze = has_edge ? load_elem<D>(zrow, edge) : -kInf;
   const int64_t action = in.action;
   const bool inside = action >= 0 && action < a.vocab;
   const float za = inside ? load_elem<D>(zrow, action) : __builtin_nanf("");
+  // the action's place: element `chosen_k` of run `chosen_u` (no run: none of
+  // them), or an end; the sum is over the others
+  const uint32_t c = static_cast<uint32_t>(action) - cut.head;
+  const uint32_t chosen_u = inside && c < units * 8 ? c / 8 : ~0u;
+  const uint32_t chosen_k = c % 8;
+  const bool chosen_edge =
+      inside && has_edge && edge == static_cast<uint32_t>(action);
+  float ze = has_edge ? load_elem<D>(zrow, edge) : -kInf;
   if constexpr (Units != 0) {
 #pragma unroll
     for (int j = 0; j < Units; ++j)
 #pragma unroll
       for (int k = 0; k < 8; ++k) top = fmaxf(top, z[j][k]);
+    // (one wave has the action; the others pass by)
+    if (chosen_u != ~0u && chosen_u % Threads == tid) {
+#pragma unroll
+      for (int j = 0; j < Units; ++j)
+        if (chosen_u / Threads == j) z[j] = without<D>(z[j], chosen_k);
+    }
   } else {
     // running maximum and sum; a lane that has seen only -inf has 0
     for (uint32_t u = tid; u < units; u += Threads * kBatch) {
@@ -261,6 +296,9 @@ __global__ __launch_bounds__(Threads * kRows<Threads>,
         if (u + j * Threads < units) x[j] = load(u + j * Threads);
         else x[j] = fill8<D>(kMinusInf<D>);
       }
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j)
+        if (u + j * Threads == chosen_u) x[j] = without<D>(x[j], chosen_k);
       float m = top;
 #pragma unroll
       for (int j = 0; j < kBatch; ++j)
@@ -278,6 +316,8 @@ __global__ __launch_bounds__(Threads * kRows<Threads>,
   }
   const float seen = top;  // what `sum` is relative to (streamed)
   top = fmaxf(top, ze);
+  if constexpr (Units == 0) top = fmaxf(top, za);
+  if (chosen_edge) ze = -kInf;
   // the compiler would keep a 16-bit row widened from here on: pinned, its
   // registers stay half as many
   const auto pin = [&] {
@@ -308,18 +348,19 @@ __global__ __launch_bounds__(Threads * kRows<Threads>,
   top = all;
   sum += __builtin_amdgcn_exp2f((ze - all) * kLog2E);
   sum = wave_sum(sum);
-  double total = sum;
+  double others = sum;
   if constexpr (!kOneWave) {
     if (tid % 64 == 0) sh.sum[wave] = sum;
     __syncthreads();
-    total = 0.0;
+    others = 0.0;
 #pragma unroll
-    for (int i = 0; i < kWaves; ++i) total += sh.sum[i];
+    for (int i = 0; i < kWaves; ++i) others += sh.sum[i];
   }
+  const float own = __builtin_amdgcn_exp2f((za - all) * kLog2E);
 
   float gain = 0.0f, chosen = 0.0f;  // S * coef; the action's gradient
   if (wave == 0) {
-    const PolicyRow r = policy_row(a, in, za, top, total);
+    const PolicyRow r = policy_row(a, in, za, top, others, own);
     gain = r.coef * in.scale;
     chosen = static_cast<float>(-exp_less_1(r.logp)) * gain;
     if (tid == 0) {
@@ -339,7 +380,7 @@ __global__ __launch_bounds__(Threads * kRows<Threads>,
     gain = sh.gain;
     chosen = sh.chosen;
   }
-  gain = -gain / static_cast<float>(total);
+  gain = -gain / static_cast<float>(others + double{own});
   // the exponentials are formed again: the compiler would keep those of the
   // sum, twice the row's registers
   __asm__("" : "+v"(top));
@@ -370,12 +411,8 @@ __global__ __launch_bounds__(Threads * kRows<Threads>,
   }
   if (has_edge) store_elem<D>(grow, edge, grad(ze));
   // the action's own gradient, by the lane that wrote its place
-  if (inside) {
-    const uint32_t c = static_cast<uint32_t>(action) - cut.head;
-    if (c < units * 8 ? tid == c / 8 % Threads
-                      : has_edge && edge == static_cast<uint32_t>(action))
-      store_elem<D>(grow, action, chosen);
-  }
+  if (chosen_edge || (chosen_u != ~0u && tid == chosen_u % Threads))
+    store_elem<D>(grow, action, chosen);
 }
 
 // The rows' sums joined in one fixed order: a workgroup takes a stretch of

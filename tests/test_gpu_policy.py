@@ -220,6 +220,59 @@ def test_not_finite_rows_stay_apart(vocab):
     assert torch.isnan(r.logp[1:]).all() and torch.isnan(r.stats[0])
 
 
+def confident(vocab, dtype, gaps=(12.0, 16.0, 20.0, 25.0)):
+    """One row for each gap by which the action's logit passes the others',
+    which are normal and end in -25, no clipping, no KL term: (inputs, 1 - p,
+    logp, ratio), in float64 from sums without the action's term."""
+    rows = len(gaps)
+    g = gen(vocab)
+    z = torch.randn(rows, vocab, generator=g).clamp(-3, 3)
+    a = torch.randint(vocab, (rows,), generator=g)
+    a[0], a[-1] = 0, vocab - 1           # the ends of a row among them
+    z[torch.arange(rows), a] = torch.tensor(gaps)
+    z = z.to(R.DTYPES[dtype])
+    z64 = R.to64(z)
+    others = np.exp(z64 - z64.max(1, keepdims=True))
+    others[np.arange(rows), a.numpy()] = 0.0
+    rest = others.sum(1)
+    logp = -np.log1p(rest)
+    old = torch.from_numpy(logp).float()
+    adv = torch.tensor([1.0, -2.0, 3.0, -0.5][:rows])
+    d = {"z": z.cuda(), "a": a.cuda(), "old": old.cuda(), "adv": adv.cuda(),
+         "w": torch.full((rows,), 1.0 / rows).cuda(), "ref": None,
+         "kw": dict(clip_low=0.2, clip_high=0.2, kl_coef=0.0)}
+    return d, rest / (1 + rest), logp, np.exp(logp - R.to64(old))
+
+
+# Relative error of a sum of exponentials of arguments to -30: an argument's
+# difference, its product with log2(e) and that constant are roundings of half
+# a step each, 2.5 * 2^-24 * 30, and the sum and 2^x as in sum_error.
+def rest_error(vocab):
+    return sum_error(vocab) + 75 * 2.0 ** -24
+
+
+CONFIDENT = [2, 40, 700, 4096, 9001, 50257, 65537, 131072]
+
+
+@pytest.mark.parametrize("dtype", list(R.DTYPES))
+@pytest.mark.parametrize("vocab", CONFIDENT)
+def test_confident_rows_keep_the_digits_of_the_rest(vocab, dtype):
+    """Where p of the action nears 1, its gradient is -c (1 - p) and logp is
+    ln p: both have as many digits as the sum of the other entries."""
+    d, rest, logp, ratio = confident(vocab, dtype)
+    e = rest_error(vocab)
+    r = call(M.policy_loss_grad, d, grad_scale=torch.full((1,), 64.0).cuda())
+    got = R.to64(r.logp)
+    assert (np.abs(got - logp) <= (e + 2.0 ** -23) * np.abs(logp)).all()
+    want = -64.0 / len(rest) * R.to64(d["adv"]) * ratio * rest
+    g = R.to64(r.dlogits)[np.arange(len(rest)), d["a"].cpu().numpy()]
+    # ratio is off by logp's error (below e), c and its product by roundings
+    bound = (2 * e + 2.0 ** -21 + R.half_step(r.dlogits.dtype)) * np.abs(want)
+    if dtype == "f16":
+        bound = bound + 2.0 ** -25
+    assert (np.abs(g - want) <= bound).all()
+
+
 def test_large_logits_keep_their_differences():
     for dtype in ("f32", "bf16"):
         for base in (1e4, -1e6, 1e30):
