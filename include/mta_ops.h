@@ -127,12 +127,15 @@ int mta_ckpt_wgrad(const mta_ckpt_wgrad_args *args, void *stream);
 int mta_ckpt_wgrad_workspace(int64_t tokens, int64_t fin, int64_t fout,
                              int type, int32_t cus, int64_t *bytes);
 
-/* What the forward keeps of a row for mta_policy_loss_backward. */
+/* What the forward keeps of a row for mta_policy_loss_backward: softmax(z)[j]
+ * is exp(z[j] - top) / total.  (The log of the sum as one number would not do:
+ * beside a top of 2^53 nothing is left of log(total).)  All 0 in a row of
+ * weight 0. */
 typedef struct {
-  double lse;  /* log of the sum of exp(logits) */
-  float coef;  /* d loss / d logp of the row, weight included; 0 in a row of
-                  weight 0 */
-  int32_t on;  /* 1; 0 in a row of weight 0 */
+  float top;   /* the row's largest logit */
+  float total; /* the sum of exp(logits - top) */
+  float coef;  /* d loss / d logp of the row, weight included */
+  int32_t on;  /* 1 */
 } mta_policy_row;
 
 /* Clipped policy loss with a KL term, summed over the rows (tokens) with

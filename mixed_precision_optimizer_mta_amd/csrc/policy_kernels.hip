@@ -32,7 +32,7 @@ constexpr uint32_t kMinusInf =
 
 struct PolicyRow {
   float coef;  // d loss / d logp, weight included
-  double lse, logp;
+  double logp;
   double sums[kPolicySums];
 };
 
@@ -104,7 +104,6 @@ __device__ __forceinline__ PolicyRow policy_row(const mta_policy_args &a,
                                                 float own) {
   PolicyRow r;
   const double logtotal = ln_plus_1(others + (double{own} - 1.0));
-  r.lse = double{top} + logtotal;
   r.logp = (double{za} - double{top}) - logtotal;
   const double adv = in.advantage, w = in.w;
   const double ratio = 1.0 + exp_less_1(r.logp - double{in.old_logp});
@@ -247,7 +246,7 @@ __global__ __launch_bounds__(Threads * kRows<Threads>,
     }
     if (tid == 0) {
       if (a.logp) a.logp[row] = 0.0f;
-      if (a.saved) a.saved[row] = mta_policy_row{0.0, 0.0f, 0};
+      if (a.saved) a.saved[row] = mta_policy_row{0.0f, 0.0f, 0.0f, 0};
 #pragma unroll
       for (int i = 0; i < kPolicySums; ++i) out[i] = 0.0;
     }
@@ -357,6 +356,7 @@ __global__ __launch_bounds__(Threads * kRows<Threads>,
     for (int i = 0; i < kWaves; ++i) others += sh.sum[i];
   }
   const float own = __builtin_amdgcn_exp2f((za - all) * kLog2E);
+  const float total = static_cast<float>(others + double{own});
 
   float gain = 0.0f, chosen = 0.0f;  // S * coef; the action's gradient
   if (wave == 0) {
@@ -365,7 +365,7 @@ __global__ __launch_bounds__(Threads * kRows<Threads>,
     chosen = static_cast<float>(-exp_less_1(r.logp)) * gain;
     if (tid == 0) {
       if (a.logp) a.logp[row] = static_cast<float>(r.logp);
-      if (a.saved) a.saved[row] = mta_policy_row{r.lse, r.coef, 1};
+      if (a.saved) a.saved[row] = mta_policy_row{top, total, r.coef, 1};
       if constexpr (!kOneWave) {
         sh.gain = gain;
         sh.chosen = chosen;
@@ -380,7 +380,7 @@ __global__ __launch_bounds__(Threads * kRows<Threads>,
     gain = sh.gain;
     chosen = sh.chosen;
   }
-  gain = -gain / static_cast<float>(others + double{own});
+  gain = -gain / total;
   // the exponentials are formed again: the compiler would keep those of the
   // sum, twice the row's registers
   __asm__("" : "+v"(top));
@@ -482,16 +482,12 @@ __global__ __launch_bounds__(kBackThreads) void k_policy_backward(
   }
   const float ze = edge < vocab ? load_elem<D>(zrow, edge) : 0.0f;
   const int64_t action = a.actions[row];
-  const float gain = (a.d_grad_scale ? *a.d_grad_scale : 1.0f) * r.coef;
-  // lse as a float32 and the rest of it
-  const float hi = static_cast<float>(r.lse);
-  const float lo = hi - hi == 0.0f
-                       ? static_cast<float>(r.lse - double{hi}) * kLog2E
-                       : 0.0f;
+  const float gain = r.coef * (a.d_grad_scale ? *a.d_grad_scale : 1.0f);
+  // as in the forward, to the bit
+  const float each = -gain / r.total;
   const auto grad = [&](float x, uint32_t at) {
-    const float p =
-        __builtin_amdgcn_exp2f(__builtin_fmaf(x - hi, kLog2E, -lo));
-    return gain * (at == action ? 1.0f - p : -p);
+    const float y = __builtin_amdgcn_exp2f((x - r.top) * kLog2E) * each;
+    return at == action ? gain + y : y;
   };
 #pragma unroll
   for (int j = 0; j < kBackUnroll; ++j) {

@@ -283,6 +283,32 @@ def test_large_logits_keep_their_differences():
             assert abs(r.logp.item() + np.log(5000)) <= sum_error(5000)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("base", [1e4, -1e6, 1e30, -1e38])
+def test_large_logits_reach_the_backward(base, dtype):
+    """Equal logits of any size: p is 1 / vocab for each, in both forms."""
+    n = 5000
+    z = torch.full((2, n), base).to(R.DTYPES[dtype]).cuda()
+    z[1, 7] = -float("inf")
+    a = torch.tensor([0, n - 1]).cuda()
+    one = torch.ones(2).cuda()
+    args = (z, a, -torch.tensor([n, n - 1.0]).log().cuda(), one)
+    f = M.policy_loss_forward(*args)
+    got = M.policy_loss_backward(z, a, f.saved)
+    for g in (got, M.policy_loss_grad(*args).dlogits):
+        g = R.to64(g)
+        for t, m in ((0, n), (1, n - 1)):
+            want = np.full(n, 0.5 / m)
+            want[a[t].item()] = 0.5 / m - 0.5
+            if t == 1:
+                want[7] = 0.0
+            # p is off by its sum's error, the ratio by logp's and old's
+            # rounding (below 2^-21), each product by a rounding
+            bound = np.abs(want) * (2 * sum_error(n) + 2.0 ** -19 +
+                                    R.half_step(z.dtype))
+            assert (np.abs(g[t] - want) <= bound).all()
+
+
 def test_no_kl_term_ignores_the_reference():
     d = case(4, 300, "f32", 6, masked=0.0)
     d["kw"]["kl_coef"] = 0.0
