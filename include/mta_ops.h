@@ -135,7 +135,7 @@ typedef struct {
   float top;   /* the row's largest logit */
   float total; /* the sum of exp(logits - top) */
   float coef;  /* d loss / d logp of the row, weight included */
-  int32_t on;  /* 1 */
+  float rest;  /* 1 - softmax(logits)[action], with all its digits near 0 */
 } mta_policy_row;
 
 /* Clipped policy loss with a KL term, summed over the rows (tokens) with

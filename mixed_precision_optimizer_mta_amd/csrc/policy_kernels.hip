@@ -246,7 +246,7 @@ __global__ __launch_bounds__(Threads * kRows<Threads>,
     }
     if (tid == 0) {
       if (a.logp) a.logp[row] = 0.0f;
-      if (a.saved) a.saved[row] = mta_policy_row{0.0f, 0.0f, 0.0f, 0};
+      if (a.saved) a.saved[row] = mta_policy_row{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int i = 0; i < kPolicySums; ++i) out[i] = 0.0;
     }
@@ -362,10 +362,11 @@ __global__ __launch_bounds__(Threads * kRows<Threads>,
   if (wave == 0) {
     const PolicyRow r = policy_row(a, in, za, top, others, own);
     gain = r.coef * in.scale;
-    chosen = static_cast<float>(-exp_less_1(r.logp)) * gain;
+    const float rest = static_cast<float>(-exp_less_1(r.logp));  // 1 - p
+    chosen = rest * gain;
     if (tid == 0) {
       if (a.logp) a.logp[row] = static_cast<float>(r.logp);
-      if (a.saved) a.saved[row] = mta_policy_row{top, total, r.coef, 1};
+      if (a.saved) a.saved[row] = mta_policy_row{top, total, r.coef, rest};
       if constexpr (!kOneWave) {
         sh.gain = gain;
         sh.chosen = chosen;
@@ -464,7 +465,7 @@ __global__ __launch_bounds__(kBackThreads) void k_policy_backward(
   const uint32_t u0 = part * kBackUnits + tid;
   const uint32_t edge = part == 0 ? cut.edge(tid) : vocab;
   const mta_policy_row r = a.saved[row];
-  if (r.on == 0) {
+  if (r.total == 0.0f) {  // a row of weight 0: others have 1 or more, or NaN
     const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < kBackUnroll; ++j) {
@@ -484,10 +485,10 @@ __global__ __launch_bounds__(kBackThreads) void k_policy_backward(
   const int64_t action = a.actions[row];
   const float gain = r.coef * (a.d_grad_scale ? *a.d_grad_scale : 1.0f);
   // as in the forward, to the bit
-  const float each = -gain / r.total;
+  const float each = -gain / r.total, chosen = r.rest * gain;
   const auto grad = [&](float x, uint32_t at) {
-    const float y = __builtin_amdgcn_exp2f((x - r.top) * kLog2E) * each;
-    return at == action ? gain + y : y;
+    return at == action ? chosen
+                        : __builtin_amdgcn_exp2f((x - r.top) * kLog2E) * each;
   };
 #pragma unroll
   for (int j = 0; j < kBackUnroll; ++j) {

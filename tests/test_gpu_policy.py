@@ -273,6 +273,28 @@ def test_confident_rows_keep_the_digits_of_the_rest(vocab, dtype):
     assert (np.abs(g - want) <= bound).all()
 
 
+@pytest.mark.parametrize("dtype", list(R.DTYPES))
+@pytest.mark.parametrize("vocab", CONFIDENT)
+def test_confident_rows_have_the_same_gradient_in_two_calls(vocab, dtype):
+    d, rest, _, ratio = confident(vocab, dtype)
+    scale = torch.full((1,), 64.0).cuda()
+    f = call(M.policy_loss_forward, d)
+    g = M.policy_loss_backward(d["z"], d["a"], f.saved, grad_scale=scale)
+    at = np.arange(len(rest)), d["a"].cpu().numpy()
+    want = -64.0 / len(rest) * R.to64(d["adv"]) * ratio * rest
+    bound = (2 * rest_error(vocab) + 2.0 ** -21 +
+             R.half_step(g.dtype)) * np.abs(want)
+    if dtype == "f16":
+        bound = bound + 2.0 ** -25
+    assert (np.abs(R.to64(g)[at] - want) <= bound).all()
+    z = d["z"].clone().requires_grad_()
+    loss, _ = M.policy_loss(z, d["a"], d["old"], d["adv"], d["w"])
+    (loss * 64.0).backward()
+    assert torch.equal(z.grad, g)
+    assert torch.equal(g, call(M.policy_loss_grad, d,
+                               grad_scale=scale).dlogits)
+
+
 def test_large_logits_keep_their_differences():
     for dtype in ("f32", "bf16"):
         for base in (1e4, -1e6, 1e30):
