@@ -36,13 +36,16 @@ struct PolicyRow {
   double sums[kPolicySums];
 };
 
-// e^x - 1 in float64: x = k ln 2 + r with |r| <= ln(2) / 2, the Taylor series
-// of e^r - 1 to r^12 (the next term is below 2^-50 of it), times 2^k.  A row
-// needs three of these and a logarithm from one wave that the others wait
-// for; the library's, which round to the last bit, take twice the time and
-// (their tables of constants kept over the loop of rows) three times the
-// registers.
-__device__ __forceinline__ double exp_less_1(double x) {
+// e^x in float64 is 2^k (1 + p): x = k ln 2 + r with |r| <= ln(2) / 2, p the
+// Taylor series of e^r - 1 to r^12 (the next term is below 2^-50 of it).  A row
+// needs four of these and a logarithm from one wave that the others wait for;
+// the library's, which round to the last bit, take twice the time and (their
+// tables of constants kept over the loop of rows) three times the registers.
+struct Exp {
+  double p, k;
+};
+
+__device__ __forceinline__ Exp exp_parts(double x) {
   const double k = __builtin_rint(x * 1.4426950408889634);
   double r = __builtin_fma(-k, 0x1.62e42fefa39efp-1, x);
   r = __builtin_fma(-k, 0x1.abc9e3b39803fp-56, r);
@@ -58,10 +61,25 @@ __device__ __forceinline__ double exp_less_1(double x) {
   p = __builtin_fma(p, r, 1.0 / 6.0);
   p = __builtin_fma(p, r, 0.5);
   p = __builtin_fma(p * r, r, r);
-  const double s = __builtin_ldexp(1.0, static_cast<int>(k));
-  double y = __builtin_fma(s, p, s - 1.0);
+  return Exp{p, k};
+}
+
+// e^x - 1, which has the digits of x near 0 and none of e^x far below it.
+__device__ __forceinline__ double exp_less_1(double x) {
+  const Exp e = exp_parts(x);
+  const double s = __builtin_ldexp(1.0, static_cast<int>(e.k));
+  double y = __builtin_fma(s, e.p, s - 1.0);
   if (x > 709.0) y = __builtin_inf();
   if (x < -100.0) y = -1.0;
+  return y;
+}
+
+// e^x, which has them.
+__device__ __forceinline__ double exp_full(double x) {
+  const Exp e = exp_parts(x);
+  double y = __builtin_ldexp(1.0 + e.p, static_cast<int>(e.k));
+  if (x > 709.0) y = __builtin_inf();
+  if (x < -745.0) y = 0.0;
   return y;
 }
 
@@ -106,7 +124,7 @@ __device__ __forceinline__ PolicyRow policy_row(const mta_policy_args &a,
   const double logtotal = ln_plus_1(others + (double{own} - 1.0));
   r.logp = (double{za} - double{top}) - logtotal;
   const double adv = in.advantage, w = in.w;
-  const double ratio = 1.0 + exp_less_1(r.logp - double{in.old_logp});
+  const double ratio = exp_full(r.logp - double{in.old_logp});
   const double lo = 1.0 - a.clip_low, hi = 1.0 + a.clip_high;
   // comparisons that keep a NaN ratio
   const double cut = ratio < lo ? lo : ratio > hi ? hi : ratio;

@@ -295,6 +295,38 @@ def test_confident_rows_have_the_same_gradient_in_two_calls(vocab, dtype):
                                grad_scale=scale).dlogits)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_small_ratios_keep_their_digits(dtype):
+    """A token of which the old policy was far surer: r = exp(logp - old) down
+    to 1e-35, unclipped for a positive advantage, in the loss (one row a call)
+    and in its gradient."""
+    vocab = 300
+    for k, gap in enumerate((5.0, 20.0, 25.0, 30.0, 40.0, 60.0, 80.0)):
+        d = case(1, vocab, dtype, k, masked=0.0, kl=False)
+        z = R.to64(d["z"])
+        a = d["a"].item()
+        top = z.max()
+        logp = z[0, a] - top - np.log(np.exp(z - top).sum())
+        d["old"] = torch.full((1,), logp + gap).cuda()
+        d["w"], d["adv"] = torch.ones(1).cuda(), torch.full((1,), 1.5).cuda()
+        ratio = np.exp(logp - R.to64(d["old"])[0])
+        r = call(M.policy_loss_grad, d)
+        e = 2 * sum_error(vocab) + 2.0 ** -20
+        assert abs(r.stats[0].item() + 1.5 * ratio) <= e * 1.5 * ratio
+        p = np.exp(z[0] - top) / np.exp(z[0] - top).sum()
+        one = np.zeros(vocab)
+        one[a] = 1.0
+        want = -1.5 * ratio * (one - p)
+        # 2^-126: below it a result has fewer digits than float32's 24
+        assert (np.abs(R.to64(r.dlogits)[0] - want) <=
+                (2 * e + R.half_step(d["z"].dtype)) * np.abs(want) +
+                2.0 ** -133).all()
+    for gap, r0 in ((740.0, 0.0), (800.0, 0.0), (float("inf"), 0.0)):
+        d["old"] = torch.full((1,), logp + gap).cuda()
+        r = call(M.policy_loss_grad, d)
+        assert r.stats[0] == r0 and (r.dlogits == 0).all()
+
+
 def test_large_logits_keep_their_differences():
     for dtype in ("f32", "bf16"):
         for base in (1e4, -1e6, 1e30):
