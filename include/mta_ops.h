@@ -80,7 +80,9 @@ typedef struct {
  * and scale, padding codes included.  act != MTA_ACT_NONE also writes
  * y = act(x), computed from x itself in float32 and rounded once to `type`; y
  * is then required and may be x itself (with ldy == ldx).  Otherwise y is
- * not looked at.  One launch per 32 tensors. */
+ * not looked at.  One launch per 32 tensors.  (A 16-bit result's exponentials
+ * are the hardware's, off by |u| 2^-24 of themselves.  gelu's 1 + erf is off
+ * by 2^-24 of 1: its values for x far below 0 have fewer digits.) */
 int mta_ckpt_pack(const mta_ckpt_tensor *tensors, int64_t count, int type,
                   int act, void *stream);
 

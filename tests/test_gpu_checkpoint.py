@@ -187,6 +187,45 @@ def test_activation_backward(act, dtype):
     assert (np.abs(got - want)[fine] <= bound[fine]).all()
 
 
+# float32 activations have the digits of a float32.  With steps of 2^-24:
+# e^-|u| is off by two, 1 + e, a quotient and a product by one each, so a
+# sigmoid by four of itself and 1 - s too, s (1 - s) by nine.  gelu_tanh's u is
+# off by six of itself (its constants and three operations), which its
+# exponential multiplies with |u|; below 2^-126 an exponential has steps of
+# 2^-149.
+def test_float32_activations_keep_a_float32s_digits():
+    x = torch.cat([torch.linspace(-86, 86, 4001), torch.linspace(-3, 3, 999),
+                   torch.tensor([-90.0, -100.0, -104.0, 120.0])]).cuda()
+    x64 = R.to64(x)
+    u64 = 2 * np.sqrt(2 / np.pi) * (x64 + 0.044715 * x64 ** 3)
+    for act, u, steps in (("silu", x64, 0.0), ("gelu_tanh", u64, 6.0)):
+        y, ck = M.ckpt_act(x, act)
+        with np.errstate(over="ignore"):
+            e = np.exp(-np.abs(u))
+            s = np.where(u < 0, e, 1.0) / (1 + e)
+        err = (steps * np.minimum(np.abs(u), 110) + 8) * 2.0 ** -24
+        bound = err * np.abs(x64 * s) + (np.abs(x64) + 1) * 2.0 ** -148
+        assert (np.abs(R.to64(y) - x64 * s) <= bound).all(), act
+    # the slopes, at values that are kept as they are
+    k = torch.tensor([m * 2.0 ** p for p in range(-6, 7) for m in range(8, 16)])
+    k = torch.cat([k, -k]).div_(8).reshape(-1, 1).cuda()
+    k64 = R.to64(k)[:, 0]
+    u64 = 2 * np.sqrt(2 / np.pi) * (k64 + 0.044715 * k64 ** 3)
+    du64 = 2 * np.sqrt(2 / np.pi) * (1 + 3 * 0.044715 * k64 ** 2)
+    for act, u, du, steps in (("silu", k64, 1.0, 0.0),
+                              ("gelu_tanh", u64, du64, 6.0)):
+        ck = M.ckpt_pack(k)
+        assert np.array_equal(R.to64(ck.unpack())[:, 0], k64)
+        got = R.to64(M.ckpt_act_backward(ck, torch.ones_like(k), act))[:, 0]
+        with np.errstate(over="ignore"):
+            e = np.exp(-np.abs(u))
+        s, t = np.where(u < 0, e, 1.0) / (1 + e), e / (1 + e) ** 2
+        err = (2 * steps * np.minimum(np.abs(u), 110) + 16) * 2.0 ** -24
+        bound = err * (s + np.abs(k64 * t * du)) + \
+            (1 + np.abs(k64 * du)) * 2.0 ** -147
+        assert (np.abs(got - (s + k64 * t * du)) <= bound).all(), act
+
+
 @pytest.mark.parametrize("act", ACTS)
 def test_slope_is_the_values_difference(act):
     # away from relu's corner: central differences of the float64 value over
