@@ -54,7 +54,21 @@ hipError_t launch_ckpt(int mode, int type, int act, const CkptList &list,
 
 constexpr int kWgradTile = 128;  // outputs of a workgroup, each way
 constexpr int kWgradStep = 32;   // tokens it takes at a time
-constexpr int kWgradRanges = 256;  // answers about the scales' range, at most
+constexpr int kWgradRanges = 256;  // answers about the values' range, at most
+
+// Whether kept values of one scale are the same in float16: multiples of 2^-24
+// of at most 65504 (their four significant bits always fit).  `steps` are their
+// magnitudes in units of the scale's smallest code, 2^(scale - 127 - 9), or'ed:
+// the lowest bit is the lowest of any, the highest the highest.
+__host__ __device__ inline bool float16_holds(uint32_t scale, uint32_t steps) {
+  if (steps == 0) return true;
+  const int unit = static_cast<int>(scale) - 127 - 9;
+  return unit + __builtin_ctz(steps) >= -24 &&
+         unit + 31 - __builtin_clz(steps) <= 15;
+}
+// Scales with which it holds for every code: the smallest code is then 2^-24
+// or more, the largest 57344 or less.
+constexpr uint32_t kFloat16Scales[2] = {112, 134};
 
 // The workgroups of a launch: `whole` tiles of the output over all tokens,
 // then `cut` tiles in `parts` parts of `part_tokens` each.
@@ -63,7 +77,7 @@ struct WgradGrid {
   int64_t whole, cut;
   int64_t part_tokens;
   int parts;
-  int ranges;  // workgroups that look at the scales (float16 dy)
+  int ranges;  // workgroups that look at the kept values (float16 dy)
   int grouped;  // workgroups of as many waves as a CU holds
 };
 

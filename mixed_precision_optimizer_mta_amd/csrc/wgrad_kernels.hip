@@ -8,8 +8,8 @@
 // that of its float32 sums, and the checkpoint is read at one byte a value.
 // A float16 dY is multiplied on the float16 instructions where every kept
 // value is exact in float16 too, as those of float16 activations are; a
-// kernel looks at the scales first.  Otherwise a float16 (float32) dY is split
-// into the two (three) bfloat16 values whose sum it is, one product each.
+// kernel looks at the checkpoint first.  Otherwise a float16 (float32) dY is
+// split into the two (three) bfloat16 values whose sum it is, one product each.
 //
 // Both operands lie with the contracted index t as their rows, while a matrix
 // instruction wants eight consecutive t of one column in a lane.  They are
@@ -98,6 +98,11 @@ __device__ __forceinline__ void kept4(uint32_t code, float scale,
   }
 }
 
+// The magnitude of a whole number below 2^32; 0 of a NaN.
+__device__ __forceinline__ uint32_t whole(float x) {
+  return x == x ? static_cast<uint32_t>(__builtin_fabsf(x)) : 0u;
+}
+
 // The run `n` elements (0 to 7) further on; its last n are anything.
 template <int D>
 __device__ __forceinline__ Raw8<D> slide(Raw8<D> x, int n) {
@@ -181,23 +186,48 @@ __device__ __forceinline__ int64_t neighbours(int64_t w, int64_t n) {
   return x * each + min(x, more) + w / 8;
 }
 
-// Whether every kept value is exact in float16: a scale in [2^-15, 2^7] makes
-// the smallest code 2^-24 and the largest 57344; the smallest scale marks a
-// block that may be all zeros.  A workgroup answers for a stretch of blocks.
+// Whether every kept value is exact in float16, as those of a float16 tensor
+// are.  Most blocks' scales say so; the others' codes are looked at (a block of
+// small values, such as the single column behind whole blocks often is, or of
+// zeros).  A workgroup answers for a stretch of blocks.
 __global__ __launch_bounds__(256) void k_wgrad_range(const WgradArgs a,
                                                      int64_t blocks) {
+  constexpr int kEach = 4;  // blocks a lane has in flight
+  const int64_t stride = int64_t{gridDim.x} * 256;
   int fine = 1;
   for (int64_t e = int64_t{blockIdx.x} * 256 + threadIdx.x; e < blocks;
-       e += int64_t{gridDim.x} * 256) {
-    const uint32_t s = ((const MTA_GLOBAL uint8_t *)a.scale)[e];
-    if (s >= 112 && s <= 134) continue;
-    uint32_t any = s == 10 ? 0 : 1;
-    if (!any) {
-      const auto *q = (const MTA_GLOBAL u32x4 *)a.q + e * 2;
+       e += stride * kEach) {
+    uint32_t s[kEach];
+    u32x4 q[kEach][2];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) any |= (q[0][k] | q[1][k]) & 0x7F7F7F7Fu;
-    }
-    if (any) fine = 0;
+    for (int j = 0; j < kEach; ++j)
+      s[j] = e + j * stride < blocks
+                 ? ((const MTA_GLOBAL uint8_t *)a.scale)[e + j * stride]
+                 : kFloat16Scales[0];
+#pragma unroll
+    for (int j = 0; j < kEach; ++j)
+      if (s[j] < kFloat16Scales[0] || s[j] > kFloat16Scales[1]) {
+        const auto *at = (const MTA_GLOBAL u32x4 *)a.q + (e + j * stride) * 2;
+        q[j][0] = at[0];
+        q[j][1] = at[1];
+      }
+#pragma unroll
+    for (int j = 0; j < kEach; ++j)
+      if (s[j] < kFloat16Scales[0] || s[j] > kFloat16Scales[1]) {
+        // a code times 2^9 is its number of steps; a NaN becomes 0
+        uint32_t steps = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int c = static_cast<int>(q[j][k / 4][k % 4]);
+            const f32x2 v =
+                h ? __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c, 512.0f, true)
+                  : __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(c, 512.0f, false);
+            steps |= whole(v[0]) | whole(v[1]);
+          }
+        if (!float16_holds(s[j], steps)) fine = 0;
+      }
   }
   fine = __syncthreads_and(fine);
   if (threadIdx.x == 0) a.range[blockIdx.x] = fine;

@@ -485,6 +485,66 @@ def test_zero_blocks_do_not_cost_float16_its_products():
         check_wgrad(dw, db, dy, R.to64(ck.unpack()))
 
 
+def takes_float16_products(ck, dy):
+    """Whether a float16 dy's product found every kept value exact in float16:
+    the answers stand at the end of the workspace."""
+    tokens, fin, fout = ck.rows, ck.shape[-1], dy.shape[1]
+    need = B.mta_ckpt_wgrad_workspace(tokens, fin, fout, 2)
+    ws = torch.full((need,), 255, dtype=torch.uint8).cuda()
+    dw = torch.empty(fout, fin).cuda()
+    B.mta_ckpt_wgrad(B.mta_ckpt_wgrad_args(
+        *ck.pointers(), dy.data_ptr(), dw.data_ptr(), None, ws.data_ptr(),
+        need, tokens, fin, fout, fout, fin, 2, 0, 0, 0))
+    n = min(-(-tokens * ck.blocks // 1024), 256)
+    flags = ws[need - -(-4 * n // 16) * 16:][:4 * n].view(torch.int32).tolist()
+    assert set(flags) <= {0, 1}
+    check_wgrad(dw, None, dy, R.to64(ck.unpack(torch.float32)))
+    return all(flags)
+
+
+@pytest.mark.parametrize("fin", [1, 33, 768, 769, 1601])
+def test_kept_float16_values_are_exact_in_float16(fin):
+    dy = torch.randn(2047, 40, generator=gen(4)).half().cuda()
+    for scale in (1.0, 1e-3, 1e-5, 3e-7, 3e4):
+        x = torch.randn(2047, fin, generator=gen(fin)) * scale
+        x.clamp_(-65504, 65504)
+        x[::3] = 0.0
+        ck = M.ckpt_pack(x.half().cuda())
+        assert takes_float16_products(ck, dy), scale
+    # one value of another type that float16 does not hold
+    for tiny in (2.0 ** -25, 65536.0, 1.5 * 2.0 ** -24):
+        y = torch.randn(2047, fin, generator=gen(fin))
+        y[1023, fin - 1] = 0.0
+        ck = M.ckpt_pack(y.half().float().cuda())
+        assert takes_float16_products(ck, dy)
+        y[1023, max(0, fin - 32):] = 0.0
+        y[1023, fin - 1] = tiny
+        ck = M.ckpt_pack(y.cuda())
+        assert not takes_float16_products(ck, dy), tiny
+
+
+def test_float16_products_at_every_scale_are_exact():
+    # one token; blocks of scale 2^k with four-bit values that float16 holds,
+    # most of them subnormal there, against every magnitude of dy
+    dy = torch.tensor([[1.5 * 2.0 ** e for e in range(-23, 16)] +
+                       [2.0 ** -24, 0.0, 2.0 ** -14 - 2.0 ** -24]],
+                      dtype=torch.float64).half().cuda()
+    ks = range(-32, -8)
+    x = torch.zeros(1, 32 * len(ks))
+    for j, k in enumerate(ks):
+        v = [f * 2.0 ** (k + 8 - i) for f in (1.75, 1.125) for i in range(16)]
+        x[0, 32 * j:32 * j + 32] = torch.tensor(
+            [y if y * 2.0 ** 24 % 1 == 0 else 0.0 for y in v])
+    ck = M.ckpt_pack(x.cuda())
+    kept = R.to64(ck.unpack())
+    assert (kept * 2.0 ** 24 % 1 == 0).all() and (kept[0, 32:] != 0).any()
+    assert takes_float16_products(ck, dy)
+    dw, _ = M.ckpt_wgrad(ck, dy, bias=False)
+    # each result is one product of 4 and 11 significant bits, not below
+    # float32's smallest normal: exact
+    assert np.array_equal(R.to64(dw), R.to64(dy).T @ kept)
+
+
 def test_wgrad_offsets_past_32_bits():
     # rows of dy 131,072 apart: the last start past 2^32 elements
     tokens, fin, fout, ld = 33000, 33, 24, 131072
