@@ -101,9 +101,13 @@ int mta_ckpt_act_backward(const mta_ckpt_tensor *tensors, int64_t count,
 /* The weight gradient of y = x W^T + b from x's checkpoint:
  *   dw[o][i] (+)= sum over tokens t of dy[t][o] * kept[t][i]
  *   db[o]    (+)= sum over tokens t of dy[t][o]
- * Products of bfloat16 dy are exact and summed in float32; a float16 (float32)
- * dy is taken as the exact sum of two (three) bfloat16 values, at two (three)
- * times the matrix work.  The sum, and with `accumulate` the old value, are
+ * Products of bfloat16 dy are exact and summed in float32, and so are those of
+ * float16 dy where every kept value is a float16 value, as those of a float16
+ * tensor are.  With any kept value that is not (it is smaller or larger than
+ * float16 holds) a float16 dy is taken as the exact sum of two bfloat16 values,
+ * at twice the matrix work: the time depends on the checkpoint's contents.  A
+ * float32 dy is taken as the sum of three, at three times the work: exact for
+ * |dy| >= 2^-117, less by below 2^-133 under that.  The sum, and with `accumulate` the old value, are
  * added in float32 and rounded once to gtype. */
 typedef struct {
   const uint8_t *q;     /* codes of x[tokens, fin] */
