@@ -8,6 +8,7 @@ rounded and the optimizer's step divides the scale out again.
 ``policy_loss_forward`` and ``policy_loss_backward`` are the two halves, and
 ``policy_loss`` is both as an autograd function.
 """
+import math
 from collections import namedtuple
 
 import torch
@@ -22,13 +23,23 @@ from .torch_list import _G
 PolicyLoss = namedtuple("PolicyLoss", "stats logp saved dlogits")
 
 
-def _vector(t, dtype, n, dev, what):
+def _one_a_row(shape, rows):
+    """Whether a shape is that of the rows, dimensions of one aside, or flat in
+    their order."""
+    shape = [n for n in shape if n != 1]
+    return shape == [n for n in rows if n != 1] or \
+        shape == [n for n in (math.prod(rows),) if n != 1]
+
+
+def _vector(t, dtype, rows, dev, what):
+    """The address of one value a row, for logits of shape [*rows, vocab]."""
     if t is None:
         return None
-    if t.dtype != dtype or t.numel() != n or t.device != dev or \
-            not t.is_contiguous():
-        raise ValueError(f"{what} is a contiguous {dtype} tensor of {n} "
-                         "values on the logits' device")
+    if t.dtype != dtype or t.device != dev or not t.is_contiguous() or (
+            t.shape != rows and not _one_a_row(t.shape, rows)):
+        raise ValueError(f"{what} is a contiguous {dtype} tensor of shape "
+                         f"{list(rows)}, one value a row, on the logits' "
+                         f"device, not {t.dtype} {list(t.shape)}")
     return t.data_ptr()
 
 
@@ -47,7 +58,7 @@ def _run(logits, actions, old_logp, advantages, weights, ref_logp, clip_low,
     rows, vocab, ld = _as_rows(logits, "logits")
     if vocab < 1:
         raise ValueError("logits needs a last dimension of at least 1")
-    dev = logits.device
+    dev, lead = logits.device, logits.shape[:-1]
     f32 = torch.float32
     dlogits, ldd = None, vocab
     if grad:
@@ -66,11 +77,11 @@ def _run(logits, actions, old_logp, advantages, weights, ref_logp, clip_low,
     saved = torch.empty(4 * rows, dtype=f32, device=dev) if save else None
     base = buf.data_ptr()
     args = B.mta_policy_args(
-        logits.data_ptr(), _vector(actions, torch.int64, rows, dev, "actions"),
-        _vector(old_logp, f32, rows, dev, "old_logp"),
-        _vector(advantages, f32, rows, dev, "advantages"),
-        _vector(weights, f32, rows, dev, "weights"),
-        _vector(ref_logp, f32, rows, dev, "ref_logp"),
+        logits.data_ptr(), _vector(actions, torch.int64, lead, dev, "actions"),
+        _vector(old_logp, f32, lead, dev, "old_logp"),
+        _vector(advantages, f32, lead, dev, "advantages"),
+        _vector(weights, f32, lead, dev, "weights"),
+        _vector(ref_logp, f32, lead, dev, "ref_logp"),
         _scalar(grad_scale, dev),
         None if dlogits is None else dlogits.data_ptr(),
         saved.data_ptr() if save else None, logp.data_ptr(), base + need, base,
@@ -89,9 +100,10 @@ def policy_loss_grad(logits, actions, old_logp, advantages, weights=None,
     logits' dtype, in `out` (which may be the logits themselves) or a new
     tensor.
 
-    actions: int64, one a row; old_logp, advantages: float32, one a row;
-    weights: float32 (default 1 / rows each; a row of weight 0 is not read and
-    has gradient 0); ref_logp: float32, needed for kl_coef > 0."""
+    actions: int64; old_logp, advantages: float32; weights: float32 (default
+    1 / rows each; a row of weight 0 is not read and has gradient 0); ref_logp:
+    float32, needed for kl_coef > 0.  Each has one value a row, in the logits'
+    shape [...] or flat in the rows' order."""
     return _run(logits, actions, old_logp, advantages, weights, ref_logp,
                 clip_low, clip_high, kl_coef, True, False, grad_scale, out)
 
@@ -109,7 +121,7 @@ def policy_loss_backward(logits, actions, saved, grad_scale=None, out=None):
     what policy_loss_forward saved for the same logits and actions."""
     _check_type(logits, "logits")
     rows, vocab, ld = _as_rows(logits, "logits")
-    dev = logits.device
+    dev, lead = logits.device, logits.shape[:-1]
     if saved.numel() != 4 * rows or saved.dtype != torch.float32 or \
             saved.device != dev or not saved.is_contiguous():
         raise ValueError("saved is that of a forward over the same rows")
@@ -121,7 +133,7 @@ def policy_loss_backward(logits, actions, saved, grad_scale=None, out=None):
     _same_device(dev, out)
     args = B.mta_policy_args(
         logits=logits.data_ptr(),
-        actions=_vector(actions, torch.int64, rows, dev, "actions"),
+        actions=_vector(actions, torch.int64, lead, dev, "actions"),
         d_grad_scale=_scalar(grad_scale, dev), dlogits=out.data_ptr(),
         saved=saved.data_ptr(), rows=rows, vocab=vocab, ld=ld,
         ldd=_as_rows(out, "out")[2], type=_G[logits.dtype])

@@ -481,6 +481,24 @@ def test_refusals_of_tensors():
         M.policy_loss_backward(d["z"][:2], d["a"][:2], f.saved)
 
 
+def test_values_of_another_order_of_rows_are_refused():
+    d = case(15, 100, "bf16")
+    want = call(M.policy_loss_grad, d)
+    d["z"] = d["z"].reshape(3, 5, 100)
+    for k in ("old", "adv", "w", "ref"):
+        d[k] = d[k].reshape(3, 5)
+    got = call(M.policy_loss_grad, {**d, "w": d["w"].reshape(15)})
+    assert torch.equal(got.dlogits.reshape(15, 100), want.dlogits)
+    f = call(M.policy_loss_forward, d)
+    for k in ("a", "old", "adv", "w", "ref"):
+        bad = {**d, k: d[k].reshape(5, 3)}
+        for fn in (M.policy_loss_grad, M.policy_loss_forward):
+            with pytest.raises(ValueError):
+                call(fn, bad)
+    with pytest.raises(ValueError):
+        M.policy_loss_backward(d["z"], d["a"].reshape(5, 3), f.saved)
+
+
 def test_captured_calls_replay_on_new_inputs():
     d = case(50, 5003, "bf16")
     scale = torch.full((1,), 4.0).cuda()

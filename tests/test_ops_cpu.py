@@ -235,6 +235,33 @@ def test_tensors_off_the_gpu_are_refused():
     assert M.ckpt_pack([]) == [] and M.ckpt_unpack([]) == []
 
 
+def test_one_value_a_row_has_the_rows_shape():
+    from mixed_precision_optimizer_mta_amd.policy import _vector
+
+    def fits(shape, rows):
+        t = torch.zeros(shape)
+        try:
+            assert _vector(t, torch.float32, rows, t.device, "x") is not None
+            return True
+        except ValueError as e:
+            assert "one value a row" in str(e)
+            return False
+
+    for rows in ((3, 5), (1, 3, 5), (3, 1, 5)):
+        for good in ((3, 5), (15,), (3, 5, 1), (1, 15)):
+            assert fits(good, rows)
+        for bad in ((5, 3), (3, 4), (14,), (15, 2), ()):
+            assert not fits(bad, rows)
+    assert fits((), ()) and fits((1,), ()) and fits((), (1,))
+    assert fits((0,), (0, 5)) and fits((0, 5), (0, 5))
+    assert not fits((2,), ()) and not fits((1,), (0,))
+    t = torch.zeros(3, 5)
+    for bad in (t.double(), torch.zeros(5, 3).t()):
+        with pytest.raises(ValueError):
+            _vector(bad, torch.float32, (3, 5), t.device, "x")
+    assert _vector(None, torch.float32, (3, 5), t.device, "x") is None
+
+
 def test_rows_of_a_view():
     from mixed_precision_optimizer_mta_amd.checkpoint import _as_rows
     x = torch.zeros(4, 6, 10)
