@@ -14,7 +14,8 @@ from collections import namedtuple
 import torch
 
 from . import _binding as B
-from .checkpoint import _as_rows, _check_type, _on_stream, _same_device, _written
+from .checkpoint import (_as_rows, _check_type, _on_stream, _rows_or_copy,
+                         _same_device, _written)
 from .torch_list import _G
 
 #: stats: float32 [3] on the device, (loss, sum w kl, sum of the weights of
@@ -163,6 +164,12 @@ class _Policy(torch.autograd.Function):
 def policy_loss(logits, actions, old_logp, advantages, weights=None,
                 ref_logp=None, clip_low=0.2, clip_high=0.2, kl_coef=0.0):
     """(loss, logp) with the loss differentiable with respect to the logits;
-    the gradient of a scaled loss is scaled before it is rounded."""
-    return _Policy.apply(logits, actions, old_logp, advantages, weights,
-                         ref_logp, clip_low, clip_high, kl_coef)
+    the gradient of a scaled loss is scaled before it is rounded.  Tensors of
+    any strides are taken: logits whose rows are not equally spaced, such as
+    the logits[:, :-1] of a batch, are copied first."""
+    def flat(t):
+        return None if t is None else t.contiguous()
+
+    return _Policy.apply(_rows_or_copy(logits), flat(actions), flat(old_logp),
+                         flat(advantages), flat(weights), flat(ref_logp),
+                         clip_low, clip_high, kl_coef)

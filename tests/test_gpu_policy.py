@@ -540,6 +540,38 @@ def test_autograd():
                           z.grad), 1024.0)
 
 
+@pytest.mark.parametrize("dtype", list(R.DTYPES))
+def test_autograd_takes_the_shifted_logits_of_a_batch(dtype):
+    """logits[:, :-1] against tokens[:, 1:], and logits of [vocab, ...] order:
+    the gradients of contiguous copies, in their places."""
+    z = (torch.randn(3, 9, 300, generator=gen(1)) * 2).to(
+        R.DTYPES[dtype]).cuda()
+    tokens = torch.randint(300, (3, 9), generator=gen(2)).cuda()
+    v = [torch.randn(3, 9, generator=gen(3 + k)).cuda() for k in range(3)]
+    v[0] -= 6.0                            # (old log-probabilities)
+    v[2] -= 6.0
+    w = torch.rand(3, 9, generator=gen(9)).cuda()
+
+    def loss(t, *args):
+        out, logp = M.policy_loss(t, *args, 0.2, 0.3, 0.1)
+        assert logp.shape == (3, 8)
+        (out * 32.0).backward()
+        return out.detach(), logp
+
+    args = [t[:, 1:] for t in (tokens, v[0], v[1], w, v[2])]
+    flat = [t.contiguous() for t in args]
+    x = z[:, :-1].contiguous().requires_grad_()
+    want = loss(x, *flat)
+    y = z.clone().requires_grad_()
+    got = loss(y[:, :-1], *args)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert torch.equal(y.grad[:, :-1], x.grad) and (y.grad[:, -1] == 0).all()
+    t = z[:, :-1].permute(2, 0, 1).contiguous().requires_grad_()
+    got = loss(t.permute(1, 2, 0), *args)
+    assert torch.equal(got[0], want[0])
+    assert torch.equal(t.grad.permute(1, 2, 0), x.grad)
+
+
 def test_a_graph_refuses_logits_overwritten_since():
     d = case(6, 700, "bf16", 6)
     z = d["z"].clone().requires_grad_()
