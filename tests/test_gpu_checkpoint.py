@@ -355,6 +355,33 @@ def test_wgrad_of_many_tokens_and_few_outputs(tokens, fin, fout, dtype):
     assert torch.equal(old[0], dw + 3.0) and torch.equal(old[1], db - 2.0)
 
 
+@pytest.mark.parametrize("dtype", list(R.DTYPES))
+@pytest.mark.parametrize("tokens,fin,fout", [
+    (1, 40, 24), (31, 130, 9), (33, 7, 130), (1000, 130, 260), (1024, 768, 640),
+    (2051, 1601, 1602), (2051, 1600, 1504), (4099, 65, 33), (8193, 260, 1000),
+    (9001, 520, 260), (20000, 40, 8), (20011, 129, 200), (33000, 33, 24)])
+def test_wgrad_takes_every_token_once(tokens, fin, fout, dtype):
+    """Sums of whole numbers below 2^24, exact in float32 in any order: a token
+    that is left out, taken twice or paired with another's dy shows.  x has
+    four significant bits, which its checkpoint keeps; dy as many as the sums
+    leave room for, so that its second bfloat16 value is there where it can
+    be.  x is taken at its size and at 2^-30 of it, where float16 holds none
+    of it."""
+    most = min(255 if dtype == "bf16" else 511, (1 << 24) // (15 * tokens) - 1)
+    x = torch.randint(-15, 16, (tokens, fin), generator=gen(tokens)).float()
+    dy = torch.randint(-most, most + 1, (tokens, fout), generator=gen(fin))
+    dy = dy.to(R.DTYPES[dtype]).cuda()
+    d = dy.double().cpu().numpy()
+    want = torch.from_numpy(d.T @ x.double().numpy()).float().cuda()
+    bias = torch.from_numpy(d.sum(0)).float().cuda()
+    for scale in (1.0, 2.0 ** -30):
+        ck = M.ckpt_pack((x * scale).cuda())
+        dw, db = M.ckpt_wgrad(ck, dy)
+        assert torch.equal(dw, want * scale) and torch.equal(db, bias)
+        M.ckpt_wgrad(ck, dy, out=dw, out_bias=db, accumulate=True)
+        assert torch.equal(dw, 2 * want * scale) and torch.equal(db, 2 * bias)
+
+
 @pytest.mark.parametrize("gtype", list(R.DTYPES))
 @pytest.mark.parametrize("dtype", list(R.DTYPES))
 @pytest.mark.parametrize("tokens", [70, 3000])
@@ -684,6 +711,26 @@ def test_checkpointed_layers_have_the_formulas_gradients(wdtype):
     x2 = x.detach().requires_grad_()
     M.checkpointed_act(M.checkpointed_linear(x2, w, b), "relu").sum().backward()
     assert torch.isfinite(x2.grad).all()
+
+
+@pytest.mark.parametrize("wdtype", list(R.DTYPES))
+@pytest.mark.parametrize("xdtype", list(R.DTYPES))
+def test_a_layers_input_gradient_is_the_product(xdtype, wdtype):
+    xt, wt = R.DTYPES[xdtype], R.DTYPES[wdtype]
+    x = activations((6, 20, 64), xt).requires_grad_()
+    w = (torch.randn(48, 64, generator=gen(3)) * 0.1).to(wt).cuda()
+    dy = torch.randn(6, 20, 48, generator=gen(4)).to(xt).cuda()
+    y = M.checkpointed_linear(x, w.requires_grad_())
+    y.backward(dy)
+    w64, d64 = R.to64(w.detach().to(xt)), R.to64(dy)
+    # 48 products, each addition off by half a step of the magnitudes' sum,
+    # rounded once
+    want, mass = d64 @ w64, np.abs(d64) @ np.abs(w64)
+    bound = R.half_step(xt) * np.abs(want) + 50 * 2.0 ** -24 * mass
+    if xt == torch.float16:
+        bound = bound + 2.0 ** -25
+    assert x.grad.dtype == xt
+    assert (np.abs(R.to64(x.grad) - want) <= bound).all()
 
 
 def test_layers_take_any_strides_and_parameter_types():

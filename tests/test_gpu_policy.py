@@ -392,6 +392,32 @@ def test_default_weights_and_the_border():
     assert act in (0.0, 0.25, 0.5, 0.75)
 
 
+@pytest.mark.parametrize("dtype", list(R.DTYPES))
+def test_a_ratio_on_the_border_is_not_clipped(dtype):
+    """vocab 1: logp is 0, so with old_logp 0 the ratio is exactly 1, which
+    with no room to either side is both borders.  The slope is then that of
+    the unclipped term, for either sign of the advantage."""
+    z = torch.tensor([[3.0], [-2.0], [0.0], [1e4]]).to(R.DTYPES[dtype]).cuda()
+    zero = torch.zeros(4).cuda()
+    adv = torch.tensor([1.0, -1.0, 0.5, -2.0]).cuda()
+    w = torch.tensor([1.0, 2.0, 4.0, 8.0]).cuda()
+    r = M.policy_loss_forward(z, zero.long(), zero, adv, weights=w,
+                              clip_low=0.0, clip_high=0.0)
+    assert (r.logp == 0).all()
+    assert r.stats.tolist() == [-(adv * w).sum().item(), 0.0, 0.0]
+    coef = r.saved.view(4, 4)[:, 2]
+    assert torch.equal(coef, -adv * w)
+    # a step past the border on the side that the sign clips
+    old = torch.tensor([-1.0, 1.0, -1.0, 1.0]).cuda() * 2.0 ** -20
+    r = M.policy_loss_forward(z, zero.long(), old, adv, weights=w,
+                              clip_low=0.0, clip_high=0.0)
+    assert r.stats[2] == w.sum() and (r.saved.view(4, 4)[:, 2] == 0).all()
+    # and on the other
+    r = M.policy_loss_forward(z, zero.long(), -old, adv, weights=w,
+                              clip_low=0.0, clip_high=0.0)
+    assert r.stats[2] == 0 and (r.saved.view(4, 4)[:, 2] != 0).all()
+
+
 def test_gradient_is_the_losses_difference():
     d = case(3, 40, "f32", 11, masked=0.0)
     g = R.to64(call(M.policy_loss_grad, d).dlogits)
