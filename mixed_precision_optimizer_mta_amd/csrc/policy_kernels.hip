@@ -149,6 +149,19 @@ __device__ __forceinline__ PolicyRow policy_row(const mta_policy_args &a,
   return r;
 }
 
+// A value that every lane has, in scalar registers: the row needs the others.
+__device__ __forceinline__ float uniform(float x) {
+  return __int_as_float(__builtin_amdgcn_readfirstlane(__float_as_int(x)));
+}
+__device__ __forceinline__ double uniform(double x) {
+  const uint64_t u = __double_as_longlong(x);
+  const uint64_t lo = static_cast<uint32_t>(
+      __builtin_amdgcn_readfirstlane(static_cast<int>(u)));
+  const uint64_t hi = static_cast<uint32_t>(
+      __builtin_amdgcn_readfirstlane(static_cast<int>(u >> 32)));
+  return __longlong_as_double(static_cast<long long>(hi << 32 | lo));
+}
+
 // Maximum or sum over the 64 lanes of a wave, in every lane.
 __device__ __forceinline__ float wave_max(float x) {
 #pragma unroll
@@ -201,14 +214,14 @@ struct RowShared {
 // A run with element k (the same in every lane) made -infinity.
 template <int D>
 __device__ __forceinline__ Raw8<D> without(Raw8<D> x, uint32_t k) {
-  constexpr int kEach = 8 / Raw8<D>::kWords;
-  const uint32_t bits = k % kEach * 16;
-  const uint32_t clear = kEach == 1 ? 0xFFFFFFFFu : 0xFFFFu << bits;
+  constexpr int kWords = Raw8<D>::kWords, kEach = 8 / kWords;
+  const uint32_t inf = kEach == 1 ? kMinusInf<D> : kMinusInf<D> * 0x10001u;
+  const uint32_t bits = kEach == 1 ? ~0u : 0xFFFFu << (k % kEach * 16);
 #pragma unroll
-  for (int w = 0; w < Raw8<D>::kWords; ++w)
-    x.w[w] = w == static_cast<int>(k / kEach)
-                 ? (x.w[w] & ~clear) | kMinusInf<D> << bits
-                 : x.w[w];
+  for (int w = 0; w < kWords; ++w) {
+    const uint32_t m = k / kEach == static_cast<uint32_t>(w) ? bits : 0u;
+    x.w[w] = (x.w[w] & ~m) | (inf & m);
+  }
   return x;
 }
 
@@ -284,7 +297,7 @@ __global__ __launch_bounds__(Threads * kRows<Threads>,
   }
   const int64_t action = in.action;
   const bool inside = action >= 0 && action < a.vocab;
-  const float za = inside ? load_elem<D>(zrow, action) : __builtin_nanf("");
+  float za = inside ? load_elem<D>(zrow, action) : __builtin_nanf("");
   // the action's place: element `chosen_k` of run `chosen_u` (no run: none of
   // them), or an end; the sum is over the others
   const uint32_t c = static_cast<uint32_t>(action) - cut.head;
@@ -298,12 +311,16 @@ __global__ __launch_bounds__(Threads * kRows<Threads>,
     for (int j = 0; j < Units; ++j)
 #pragma unroll
       for (int k = 0; k < 8; ++k) top = fmaxf(top, z[j][k]);
-    // (one wave has the action; the others pass by)
-    if (chosen_u != ~0u && chosen_u % Threads == tid) {
+    // (the maximum before the change: the compiler would keep two rows, and
+    // the loss alone of 7934 x 16384 bfloat16 take 73 us, not 58)
 #pragma unroll
-      for (int j = 0; j < Units; ++j)
-        if (chosen_u / Threads == j) z[j] = without<D>(z[j], chosen_k);
-    }
+    for (int j = 0; j < Units; ++j)
+#pragma unroll
+      for (int k = 0; k < Raw8<D>::kWords; ++k)
+        __asm__("" : "+v"(z[j].w[k]) : "v"(top));
+#pragma unroll
+    for (int j = 0; j < Units; ++j)
+      if (tid + j * Threads == chosen_u) z[j] = without<D>(z[j], chosen_k);
   } else {
     // running maximum and sum; a lane that has seen only -inf has 0
     for (uint32_t u = tid; u < units; u += Threads * kBatch) {
@@ -353,6 +370,8 @@ __global__ __launch_bounds__(Threads * kRows<Threads>,
 #pragma unroll
     for (int i = 0; i < kWaves; ++i) all = fmaxf(all, sh.top[i]);
   }
+  all = uniform(all);
+  za = uniform(za);
   if constexpr (Units != 0) {
 #pragma unroll
     for (int j = 0; j < Units; ++j)
@@ -373,14 +392,16 @@ __global__ __launch_bounds__(Threads * kRows<Threads>,
 #pragma unroll
     for (int i = 0; i < kWaves; ++i) others += sh.sum[i];
   }
-  const float own = __builtin_amdgcn_exp2f((za - all) * kLog2E);
-  const float total = static_cast<float>(others + double{own});
+  others = uniform(others);
+  const float own = uniform(__builtin_amdgcn_exp2f((za - all) * kLog2E));
+  const float total = uniform(static_cast<float>(others + double{own}));
 
   float gain = 0.0f, chosen = 0.0f;  // S * coef; the action's gradient
   if (wave == 0) {
     const PolicyRow r = policy_row(a, in, za, top, others, own);
     gain = r.coef * in.scale;
-    const float rest = static_cast<float>(-exp_less_1(r.logp));  // 1 - p
+    const float rest =  // 1 - p
+        static_cast<float>(others) * __builtin_amdgcn_rcpf(total);
     chosen = rest * gain;
     if (tid == 0) {
       if (a.logp) a.logp[row] = static_cast<float>(r.logp);
@@ -396,13 +417,13 @@ __global__ __launch_bounds__(Threads * kRows<Threads>,
   if (!grow) return;
   if constexpr (!kOneWave) {
     __syncthreads();
-    gain = sh.gain;
-    chosen = sh.chosen;
+    gain = uniform(sh.gain);
+    chosen = uniform(sh.chosen);
   }
-  gain = -gain / total;
+  gain = uniform(-gain / total);
   // the exponentials are formed again: the compiler would keep those of the
   // sum, twice the row's registers
-  __asm__("" : "+v"(top));
+  __asm__("" : "+s"(top));
   pin();
   const auto grad = [&](float x) {
     return __builtin_amdgcn_exp2f((x - top) * kLog2E) * gain;
