@@ -133,8 +133,9 @@ int mta_ckpt_wgrad(const mta_ckpt_wgrad_args *args, void *stream);
 int mta_ckpt_wgrad_workspace(int64_t tokens, int64_t fin, int64_t fout,
                              int type, int32_t cus, int64_t *bytes);
 
-/* What the forward keeps of a row for mta_policy_loss_backward: softmax(z)[j]
- * is exp(z[j] - top) / total.  (The log of the sum as one number would not do:
+/* What the forward keeps of a row for mta_policy_loss_backward of the same
+ * library, which alone needs to know its fields: softmax(z)[j] is
+ * exp(z[j] - top) / total.  (The log of the sum as one number would not do:
  * beside a top of 2^53 nothing is left of log(total).)  All 0 in a row of
  * weight 0. */
 typedef struct {

@@ -393,6 +393,7 @@ def checkpointed_linear(x, weight, bias=None):
 
 
 def checkpointed_act(x, act):
-    """act(x) whose backward keeps x in 8 bits."""
+    """act(x) whose backward keeps x in 8 bits (where gradients are off, the
+    checkpoint is made and dropped)."""
     _act_code(act)
     return _Act.apply(x, act)

@@ -383,10 +383,10 @@ int run_policy(const mta_policy_args *a, bool backward, void *stream,
 // of a tile 0.37 of a CU that holds one workgroup, 0.285 with two, 0.27 with
 // more and 0.265 with groups (float32 dY: 1.1, 0.85, 0.85 and 0.75); 5 for the
 // second kernel and 0.015 a part for its bytes.  Against whole tiles by single
-// groups, in bfloat16: 423 us instead of 479 for 1600 x 6400 outputs (2.5
-// rounds) over 16384 tokens, 71 instead of 102 for 1600 x 1600 over 8192, 59
-// instead of 385 for 768 x 768 over 32768 (66 with parts alone), and 31
-// instead of 42 for 768 x 2304 over 1024 tokens of float32 dY.
+// groups, in bfloat16: 404 us instead of 423 for 1600 x 6400 outputs (2.5
+// rounds) over 16384 tokens, 68 instead of 91 for 1600 x 1600 over 8192, 56
+// instead of 338 for 768 x 768 over 32768 (58 with parts alone), and 28
+// instead of 40 for 768 x 2304 over 1024 tokens of float32 dY (32).
 mta::WgradGrid mta::wgrad_grid(int64_t tokens, int64_t fin, int64_t fout,
                                int type, int cus) {
   static constexpr double kStepUs[2][4] = {{0.37, 0.285, 0.27, 0.265},

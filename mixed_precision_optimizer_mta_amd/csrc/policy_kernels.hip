@@ -6,7 +6,7 @@
 // least twice.  Here a row stays in the registers of the workgroup that reads
 // it (65536 logits are 32 registers a lane of 1024 in 16 bits), so one call
 // reads every logit once and writes every gradient once: bound by HBM (8192
-// rows of 50257 bfloat16 logits, a fifth of them masked, at 5.6 TB/s).  Longer
+// rows of 50257 bfloat16 logits, a fifth of them masked, at 5.5 TB/s).  Longer
 // rows are read twice, the second time mostly from the memory-side cache.
 //
 // Numerics: exponentials are 2^((z - max) log2 e) in float32, a lane sums at
@@ -38,7 +38,7 @@ struct PolicyRow {
 
 // e^x in float64 is 2^k (1 + p): x = k ln 2 + r with |r| <= ln(2) / 2, p the
 // Taylor series of e^r - 1 to r^12 (the next term is below 2^-50 of it).  A row
-// needs four of these and a logarithm from one wave that the others wait for;
+// needs two of these and a logarithm from one wave that the others wait for;
 // the library's, which round to the last bit, take twice the time and (their
 // tables of constants kept over the loop of rows) three times the registers.
 struct Exp {
@@ -178,7 +178,7 @@ __device__ __forceinline__ float wave_sum(float x) {
 // multiple of Align, and up to Align / size + 7 single logits at its two ends,
 // one to each of the first lanes.  Rows of an odd length start anywhere: with
 // runs from each row's first element the same batch of 50257 columns took 352
-// us instead of 265.
+// us (271 now).
 struct Cut {
   uint32_t head, units, vocab;
   // The end of the row that lane i holds; `vocab` or more: none.
@@ -231,7 +231,10 @@ constexpr int kBatch = 4;
 // Units > 0: that many runs of eight logits to a lane, kept in registers.
 // Units == 0: the row is streamed, twice.  A row is one workgroup's (or one
 // wave's) and there is no loop over rows: over such a loop the compiler keeps
-// the scalars' float64 constants in 60 registers.
+// the scalars' float64 constants in 60 registers.  A 16-bit row has 64 registers
+// a lane, for two groups of sixteen waves on a CU: of seven runs six words are
+// spilled around the scalars, of eight 13 (by one wave a row three from six runs
+// on, and 15), 15 of the 840 MB that 8192 x 50304 bfloat16 write.
 template <int D, int Threads, int Units>
 __global__ __launch_bounds__(Threads * kRows<Threads>,
                              (D == MTA_F32 ? 4 : 8)) void k_policy(
@@ -590,8 +593,8 @@ hipError_t launch_policy(const mta_policy_args &a, hipStream_t stream) {
     // group waits less at its joins.  A float32 row of sixteen waves leaves
     // room for one group on a CU, whose loads, sums and stores then take
     // turns: streamed, two groups overlap theirs and the second reading comes
-    // from the memory-side cache (2047 rows of 50257 with their gradient 200
-    // us against 212, the loss alone 67 us against 98).
+    // from the memory-side cache (2047 rows of 50257 with their gradient 205
+    // us, 212 when kept; the loss alone 67 us, 98 when kept).
     if (a.vocab <= 64 * 64) return start_units<D, 64, 1>(a, stream);
     if (a.vocab <= 256 * 64) return start_units<D, 256, 3>(a, stream);
     if constexpr (D != MTA_F32)

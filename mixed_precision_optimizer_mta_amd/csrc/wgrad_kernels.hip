@@ -17,17 +17,19 @@
 // with the transposing LDS load: 16 lanes read four rows of 16 columns and
 // each gets four rows of one column.
 //
-// Bound by the LDS and the matrix pipes together: a step of a workgroup, 32
-// tokens, is 32 KiB of transposing reads (which reach 128 bytes a clock here),
-// 16 KiB of writes (64 to 77), 16 loads of a wave and 32 matrix instructions.
-// A workgroup of four waves takes a tile of 128 x 128, and three share a CU, so
-// that one's reads run under another's products: 8192 tokens of 4096 x 4096 in
-// bfloat16 at 850 to 890 TFLOP/s, against 820 to 880 for one workgroup of 256^2
-// with the same inner loop, whose eight waves keep step, and 800 without the
-// order that sched_group_barrier asks for.  A tile's sums are written with all
-// tests of types outside and, when added to the gradient, with 32 old values
-// on their way at once: one after the other they cost 8 us a workgroup (4
-// steps of tokens 16.3 us, now 8.5; 1024 tokens, 768 -> 2304, 27.0, now 19.4).
+// Bound by the LDS and the matrix pipes, which take turns: a step of a
+// workgroup, 32 tokens, is 32 KiB of transposing reads (which reach 128 bytes a
+// clock here), 16 KiB of writes (64 to 77), 16 loads of a wave and 32 matrix
+// instructions, and the counters have the LDS busy for 51% of the time and the
+// matrix pipes for 41%.  A workgroup of four waves takes a tile of 128 x 128,
+// and three share a CU, so that one's reads run under another's products: 8192
+// tokens of 4096 x 4096 in bfloat16 in 294 to 310 us (890 to 935 TFLOP/s),
+// 308 without the order that sched_group_barrier asks for where it is 294 with
+// it; one workgroup of 256^2 with the same inner loop, whose eight waves keep
+// step, was 1 to 3% slower.  A tile's sums are written with all tests of types
+// outside and, when added to the gradient, with 32 old values on their way at
+// once: one after the other they cost 8 us a workgroup (4 steps of tokens 16.3
+// us, now 8.6; 1024 tokens, 768 -> 2304, 27.0, now 16 to 18).
 #include "ops_device.h"
 
 namespace mta {
@@ -285,7 +287,7 @@ __global__ __launch_bounds__(kThreads * Groups)
   // Columns past the last whole run are the last one's again: what comes of
   // them is not written.  A run that the last column ends inside is moved to
   // its place when it is staged (loaded by elements instead, the last tiles
-  // of 1601 outputs made 8192 tokens of 1600 features take 120 us, not 80).
+  // of 1601 outputs made 8192 tokens of 1600 features take 120 us, not 76).
   const int64_t col_o = min(o0 + co, max(int64_t{0}, a.fout - 8));
   const int64_t col_i = min(i0 + ci, max(int64_t{0}, a.ldq - 16));
   const int64_t lane_o = (col_o - o0 + row_o * a.lddy) * int64_t{sizeof(elem<D>)};
