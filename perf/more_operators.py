@@ -1,0 +1,327 @@
+"""The measured cases of the operators for a training step's matrices and its
+vocabulary: the orthogonalised update of the Muon rule (with and without its
+momentum) and the cross entropy of a linear output layer, with its gradients
+and without keeping the logits.
+
+Sizes are those of the GPT-2-shaped workloads of this repository (widths 768,
+1600, 2304, 4800 and 6400, vocabulary 50257), adapters of a low rank beside
+them, and odd ones.
+"""
+import math
+
+import torch
+
+own = False
+
+_DT = {"f32": torch.float32, "bf16": torch.bfloat16, "f16": torch.float16}
+_SIZE = {"f32": 4, "bf16": 2, "f16": 2}
+COEF = (3.4445, -4.7750, 2.0315)
+STEPS = 5
+EPS = 1e-7
+IGNORE = -100
+
+
+# --------------------------------------------------------------------------
+# cases
+# --------------------------------------------------------------------------
+
+def listed():
+    return [
+        # one low-rank adapter's matrix: what the calls' launches cost
+        dict(name="ortho adapter", op="ortho", dtype="bf16",
+             shapes="16x768", pad=0),
+        # a narrow model's twelve attention projections in one call
+        dict(name="ortho narrow", op="ortho", dtype="bf16",
+             shapes="768x768*12", pad=0),
+        # float32 gradients of odd shapes, tall and wide, in wider rows
+        dict(name="ortho odd f32", op="ortho", dtype="f32",
+             shapes="517x1601,1601x517,1023x1025", pad=3),
+        # the feed-forward matrices of four wide blocks
+        dict(name="ortho wide", op="ortho", dtype="bf16",
+             shapes="6400x1600*4,1600x6400*4", pad=0),
+        # an optimizer step's updates of a narrow model's joint projections
+        dict(name="muon narrow", op="muon", dtype="bf16",
+             shapes="2304x768*12", nesterov=True),
+        # float16 gradients, odd shapes, heavy-ball momentum
+        dict(name="muon odd f16", op="muon", dtype="f16",
+             shapes="769x1203*3,1600x333", nesterov=False),
+        # every matrix of two wide blocks, float32 momenta
+        dict(name="muon wide", op="muon", dtype="bf16",
+             shapes="4800x1600*2,1600x1600*2,6400x1600*2,1600x6400*2",
+             nesterov=True),
+        # the loss of a few sampled tokens
+        dict(name="loss few tokens", op="loss", dtype="bf16", tokens=8,
+             width=768, vocab=50257, mode="eval", masked=0.0),
+        # an evaluation batch of the narrow model
+        dict(name="loss eval", op="loss", dtype="bf16", tokens=16384,
+             width=768, vocab=50257, mode="eval", masked=0.1),
+        # a training batch of the wide model with padding
+        dict(name="loss train", op="loss", dtype="bf16", tokens=8192,
+             width=1600, vocab=50257, mode="train", masked=0.2),
+        # float32 throughout, through forward and backward apart
+        dict(name="loss f32 two calls", op="loss", dtype="f32", tokens=1023,
+             width=768, vocab=50257, mode="two", masked=0.1),
+        # float16 with a loss scale, odd width
+        dict(name="loss odd f16", op="loss", dtype="f16", tokens=2047,
+             width=1601, vocab=50257, mode="train", masked=0.3),
+    ]
+
+
+def _log(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(
+        rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(["ortho", "muon", "loss"])
+    dtype = rng.choice(["bf16", "bf16", "f16", "f32"])
+    if op != "loss":
+        rows, cols = _log(rng, 1, 6400), _log(rng, 1, 6400)
+        small, large = min(rows, cols), max(rows, cols)
+        each = STEPS * (4 * small * small * large + 2 * small ** 3)
+        # the plain form of float32 results runs in 64 bits
+        most = 4e12 if dtype != "f32" else 1e12
+        count = rng.choice([1, 1, 2, 3, 12])
+        count = max(1, min(count, int(most / each)))
+        shapes = "%dx%d*%d" % (rows, cols, count)
+        if op == "ortho":
+            return dict(op=op, dtype=dtype, shapes=shapes,
+                        pad=rng.choice([0, 0, 1, 16]))
+        return dict(op=op, dtype=dtype, shapes=shapes,
+                    nesterov=rng.random() < 0.6)
+    width, vocab = _log(rng, 8, 2400), _log(rng, 2, 160000)
+    most = max(1, min(32768, int(6e11 / width / vocab), int(7e8 / vocab)))
+    return dict(op=op, dtype=dtype, tokens=_log(rng, 1, most), width=width,
+                vocab=vocab, mode=rng.choice(["train", "train", "two",
+                                              "eval"]),
+                masked=rng.choice([0.0, 0.2, 0.6]))
+
+
+def _shapes(case):
+    out = []
+    for part in case["shapes"].split(","):
+        size, _, count = part.partition("*")
+        rows, cols = size.split("x")
+        out += [(int(rows), int(cols))] * int(count or 1)
+    return out
+
+
+# --------------------------------------------------------------------------
+# inputs
+# --------------------------------------------------------------------------
+
+def _gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def _randn(g, *shape):
+    return torch.randn(*shape, generator=g, device="cuda")
+
+
+def _gradient(g, rows, cols, pad=0):
+    """A weight's gradient: a few directions that stand out of the noise of
+    the batch, rows and columns of unequal size."""
+    x = _randn(g, rows, cols + pad)
+    few = min(4, rows, cols)
+    x += (_randn(g, rows, few) @ _randn(g, few, cols + pad)) * (
+        3 / math.sqrt(min(rows, cols)))
+    x *= torch.exp(0.3 * _randn(g, rows, 1))
+    x *= torch.exp(0.3 * _randn(g, 1, cols + pad))
+    return x * 1e-3
+
+
+def prepare(case, seed):
+    g = _gen(seed)
+    dt = _DT[case["dtype"]]
+    st = dict(case)
+    if case["op"] == "ortho":
+        st["x"] = [_gradient(g, r, c, case["pad"]).to(dt)[:, :c]
+                   for r, c in _shapes(case)]
+    elif case["op"] == "muon":
+        st["g"] = [_gradient(g, r, c).to(dt) for r, c in _shapes(case)]
+        st["m"] = [4 * _gradient(g, r, c) for r, c in _shapes(case)]
+    else:
+        t, d, v = case["tokens"], case["width"], case["vocab"]
+        w = (_randn(g, v, d) * 0.02).to(dt)
+        a = torch.randint(v, (t,), generator=g, device="cuda")
+        h = _randn(g, t, d)
+        # a model that has learnt something: the target's logit is raised by
+        # 0 to 12
+        at = w[a].float()
+        h += at * (12 * torch.rand(t, 1, generator=g, device="cuda") /
+                   at.square().sum(1, keepdim=True).clamp_min(0.02 ** 2))
+        st["h"], st["w"] = h.to(dt), w
+        off = torch.rand(t, generator=g, device="cuda") < case["masked"]
+        off[0] = False
+        st["targets"] = torch.where(off, IGNORE, a)
+        st["loss_scale"] = torch.full((1,), 1024.0, device="cuda")
+    return st
+
+
+# --------------------------------------------------------------------------
+# one pass
+# --------------------------------------------------------------------------
+
+def run(st):
+    return {"ortho": _run_ortho, "muon": _run_muon, "loss": _run_loss}[
+        st["op"]](st)
+
+
+def _run_ortho(st):
+    """Every matrix of the list orthogonalised, in its own type."""
+    if own:
+        from mixed_precision_optimizer_mta_amd import orthogonalize
+        return orthogonalize(st["x"], steps=STEPS, coefficients=COEF, eps=EPS)
+    return [_newton_schulz(x).to(x.dtype) for x in st["x"]]
+
+
+def _run_muon(st):
+    """The momenta take the gradients in, in place, and the updates come back
+    orthogonalised, in the gradients' type."""
+    if own:
+        from mixed_precision_optimizer_mta_amd import muon_update
+        out = muon_update(st["g"], st["m"], momentum=0.95,
+                          nesterov=st["nesterov"], steps=STEPS,
+                          coefficients=COEF, eps=EPS)
+        return {"update": out, "momentum": st["m"]}
+    out = []
+    for g, m in zip(st["g"], st["m"]):
+        x = g.float()
+        m.mul_(0.95).add_(x)
+        u = x + 0.95 * m if st["nesterov"] else m
+        out.append(_newton_schulz(u, g.dtype).to(g.dtype))
+    return {"update": out, "momentum": st["m"]}
+
+
+def _newton_schulz(x, dtype=None):
+    # 64 bits where the result is to have the digits of 32
+    wide = torch.float64 if (dtype or x.dtype) == torch.float32 else \
+        torch.float32
+    a, b, c = COEF
+    x = x.to(wide)
+    tall = x.shape[0] > x.shape[1]
+    if tall:
+        x = x.t()
+    x = x / (x.double().square().sum().sqrt() + EPS).to(wide)
+    for _ in range(STEPS):
+        s = x @ x.t()
+        x = a * x + (b * s + c * (s @ s)) @ x
+    return x.t() if tall else x
+
+
+def _run_loss(st):
+    """The mean cross entropy over the tokens that have a target, with the
+    loss scale times its gradients ("train": one call; "two": the forward,
+    then the backward from what it saved), or the loss alone ("eval")."""
+    if own:
+        from mixed_precision_optimizer_mta_amd import (
+            linear_cross_entropy_backward, linear_cross_entropy_forward,
+            linear_cross_entropy_grad)
+        args = st["h"], st["w"], st["targets"]
+        if st["mode"] == "train":
+            r = linear_cross_entropy_grad(*args, grad_scale=st["loss_scale"])
+            return {"loss": r.loss, "logp": r.logp, "dh": r.dhidden,
+                    "dw": r.dweight}
+        r = linear_cross_entropy_forward(*args)
+        out = {"loss": r.loss, "logp": r.logp}
+        if st["mode"] == "two":
+            out["dh"], out["dw"] = linear_cross_entropy_backward(
+                *args, r.saved, grad_scale=st["loss_scale"])
+        return out
+    h, w = st["h"].float(), st["w"].float()
+    on = st["targets"] != IGNORE
+    a = torch.where(on, st["targets"], 0)[:, None]
+    z = h @ w.t()
+    top = z.amax(1, keepdim=True)
+    zt = z.gather(1, a) - top
+    z.sub_(top).exp_()
+    total = z.sum(1, keepdim=True)
+    # a token's few values next to probability 1, in 64 bits
+    logp = torch.where(on, (zt.double() - total.double().log())[:, 0], 0.0)
+    weight = on.double() / on.sum()
+    out = {"loss": -(weight * logp).sum().float(), "logp": logp.float()}
+    if st["mode"] == "eval":
+        return out
+    z.div_(total)
+    rest = torch.expm1(logp).float()[:, None]
+    z.scatter_(1, a, rest)
+    z.mul_((weight * st["loss_scale"].double()).float()[:, None])
+    out["dh"] = (z @ w).to(st["h"].dtype)
+    out["dw"] = (z.t() @ h).to(st["w"].dtype)
+    return out
+
+
+# --------------------------------------------------------------------------
+# work and exact values
+# --------------------------------------------------------------------------
+
+def work(case):
+    sz = _SIZE[case["dtype"]]
+    if case["op"] != "loss":
+        n = flops = 0
+        for r, c in _shapes(case):
+            small, large = min(r, c), max(r, c)
+            n += r * c
+            # of the symmetric products X X^T and its square, one half
+            flops += STEPS * (3 * small * small * large + small ** 3)
+        return {"bytes": n * (2 * sz + (8 if case["op"] == "muon" else 0)),
+                "flops": flops}
+    t, d, v = case["tokens"], case["width"], case["vocab"]
+    kept = 1 + (t - 1) * (1 - case["masked"])
+    grads = 0 if case["mode"] == "eval" else 1
+    return {"bytes": (kept * d + v * d) * sz + grads * (t * d + v * d) * sz +
+            12 * t, "flops": (6 if grads else 2) * kept * d * v}
+
+
+def _exact_ortho(x):
+    """The steps' polynomial applied to the singular values' side: the
+    product of the steps' symmetric factors times the scaled matrix."""
+    x = x.double()
+    flip = x.shape[0] > x.shape[1]
+    x = x.mT.contiguous() if flip else x.contiguous()
+    y = x / (torch.linalg.vector_norm(x) + EPS)
+    one = torch.eye(len(y), dtype=torch.float64, device=y.device)
+    for _ in range(STEPS):
+        gram = torch.mm(y, y.mT.contiguous())
+        factor = torch.addmm(one, gram, torch.addmm(
+            one, gram, one, beta=COEF[1], alpha=COEF[2]), beta=COEF[0])
+        y = torch.mm(factor, y)
+    return y.mT if flip else y
+
+
+def exact(case, seed):
+    st = prepare(case, seed)
+    if case["op"] == "ortho":
+        return [_exact_ortho(x) for x in st["x"]]
+    if case["op"] == "muon":
+        new = [m.double() * 0.95 + g.double()
+               for g, m in zip(st["g"], st["m"])]
+        look = [g.double() + 0.95 * m if case["nesterov"] else m
+                for g, m in zip(st["g"], new)]
+        return {"update": [_exact_ortho(u) for u in look], "momentum": new}
+    on = st["targets"] != IGNORE
+    count = on.sum().double()
+    w = st["w"].double()
+    grads = case["mode"] != "eval"
+    loss = torch.zeros((), dtype=torch.float64, device="cuda")
+    logp, dh, dw = [], [], torch.zeros_like(w) if grads else None
+    wt = w.mT.contiguous()
+    for lo in range(0, case["tokens"], 2048):
+        keep = on[lo:lo + 2048]
+        h = st["h"][lo:lo + 2048].double()
+        a = st["targets"][lo:lo + 2048].clamp_min(0)[:, None]
+        lp = torch.log_softmax(torch.mm(h, wt), 1)
+        mine = lp.gather(1, a)
+        logp.append(torch.where(keep, mine[:, 0], 0.0))
+        loss -= logp[-1].sum() / count
+        if grads:
+            p = lp.exp()
+            p.scatter_(1, a, torch.expm1(mine))
+            p *= torch.where(keep, st["loss_scale"].double() / count,
+                             0.0)[:, None]
+            dh.append(torch.mm(p, w))
+            dw += torch.mm(p.mT.contiguous(), h)
+    out = {"loss": loss, "logp": torch.cat(logp)}
+    if grads:
+        out["dh"], out["dw"] = torch.cat(dh), dw
+    return out
