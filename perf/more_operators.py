@@ -79,10 +79,8 @@ def draw(rng):
         rows, cols = _log(rng, 1, 6400), _log(rng, 1, 6400)
         small, large = min(rows, cols), max(rows, cols)
         each = STEPS * (4 * small * small * large + 2 * small ** 3)
-        # the plain form of float32 results runs in 64 bits
-        most = 4e12 if dtype != "f32" else 1e12
         count = rng.choice([1, 1, 2, 3, 12])
-        count = max(1, min(count, int(most / each)))
+        count = max(1, min(count, int(4e12 / each)))
         shapes = "%dx%d*%d" % (rows, cols, count)
         if op == "ortho":
             return dict(op=op, dtype=dtype, shapes=shapes,
@@ -189,20 +187,17 @@ def _run_muon(st):
         x = g.float()
         m.mul_(0.95).add_(x)
         u = x + 0.95 * m if st["nesterov"] else m
-        out.append(_newton_schulz(u, g.dtype).to(g.dtype))
+        out.append(_newton_schulz(u).to(g.dtype))
     return {"update": out, "momentum": st["m"]}
 
 
-def _newton_schulz(x, dtype=None):
-    # 64 bits where the result is to have the digits of 32
-    wide = torch.float64 if (dtype or x.dtype) == torch.float32 else \
-        torch.float32
+def _newton_schulz(x):
     a, b, c = COEF
-    x = x.to(wide)
+    x = x.float()
     tall = x.shape[0] > x.shape[1]
     if tall:
         x = x.t()
-    x = x / (x.double().square().sum().sqrt() + EPS).to(wide)
+    x = x / (x.double().square().sum().sqrt() + EPS).float()
     for _ in range(STEPS):
         s = x @ x.t()
         x = a * x + (b * s + c * (s @ s)) @ x
