@@ -1,8 +1,10 @@
 """Fused mixed-precision gradient clip + multi-tensor AdamW for MI355X.
 
 The work runs in libmta.so (HIP, gfx950) behind the C ABI of include/mta.h
-(the optimizer step) and include/mta_ops.h (what makes its gradients: 8-bit
-activation checkpoints with their backward, and a clipped policy loss).
+(the optimizer step), include/mta_ops.h (what makes its gradients: 8-bit
+activation checkpoints with their backward, and a clipped policy loss) and
+include/mta_matrix.h (operators whose work is matrix products: orthogonalised
+updates).
 ``_binding`` mirrors that ABI name for name; ``MtaList`` marshals PyTorch
 tensors and the current HIP stream into it.  Nothing here computes any part
 of the step, and nothing falls back to another implementation: if
@@ -28,3 +30,5 @@ from .checkpoint import (Checkpoint8, checkpointed_act,  # noqa: F401
 from .policy import (PolicyLoss, policy_loss,  # noqa: F401
                      policy_loss_backward, policy_loss_forward,
                      policy_loss_grad)
+from ._binding import MATRIX_EXPORTS, mta_matrix_version  # noqa: F401
+from .muon import muon_update, orthogonalize  # noqa: F401

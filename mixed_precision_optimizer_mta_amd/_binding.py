@@ -1,5 +1,5 @@
-"""ctypes binding of libmta.so: the C ABI of include/mta.h and
-include/mta_ops.h, same names.
+"""ctypes binding of libmta.so: the C ABI of include/mta.h, include/mta_ops.h
+and include/mta_matrix.h, same names.
 
 Argument marshalling only: every step of the optimizer runs in the HIP
 library.  If the library is not built, loading fails loudly; there is no
@@ -33,6 +33,10 @@ ABI_VERSION = 5
 # MTA_OPS_VERSION of include/mta_ops.h
 OPS_VERSION = 1
 
+# MTA_MATRIX_VERSION of include/mta_matrix.h
+MATRIX_VERSION = 1
+MTA_ORTHO_STEPS = 16
+
 # every symbol include/mta.h declares
 EXPORTS = ("mta_list_create", "mta_list_destroy", "mta_scale",
            "mta_clip_norm", "mta_adamw_step", "mta_list_set_weight_copies",
@@ -49,6 +53,10 @@ OPS_EXPORTS = ("mta_ckpt_pack", "mta_ckpt_unpack", "mta_ckpt_act_backward",
                "mta_ckpt_wgrad", "mta_ckpt_wgrad_workspace",
                "mta_policy_loss", "mta_policy_loss_backward",
                "mta_policy_loss_workspace", "mta_ops_version")
+
+# every symbol include/mta_matrix.h declares
+MATRIX_EXPORTS = ("mta_orthogonalize", "mta_orthogonalize_workspace",
+                  "mta_matrix_version")
 
 
 class mta_tensor(ctypes.Structure):
@@ -126,6 +134,27 @@ class mta_policy_args(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
+class mta_ortho_matrix(ctypes.Structure):
+    _fields_ = [("g", ctypes.c_void_p), ("m", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("w", ctypes.c_void_p),
+                ("w16", ctypes.c_void_p), ("rows", ctypes.c_int64),
+                ("cols", ctypes.c_int64), ("ldg", ctypes.c_int64),
+                ("ldout", ctypes.c_int64), ("scale", ctypes.c_double)]
+
+
+class mta_ortho_args(ctypes.Structure):
+    _fields_ = [("matrices", ctypes.POINTER(mta_ortho_matrix)),
+                ("count", ctypes.c_int64), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_int64),
+                ("coefficients", ctypes.POINTER(ctypes.c_double)),
+                ("d_coef", ctypes.c_void_p), ("d_amp", ctypes.c_void_p),
+                ("eps", ctypes.c_double), ("momentum", ctypes.c_double),
+                ("lr", ctypes.c_double), ("weight_decay", ctypes.c_double),
+                ("steps", ctypes.c_int32), ("type", ctypes.c_int32),
+                ("out_type", ctypes.c_int32), ("copy_type", ctypes.c_int32),
+                ("nesterov", ctypes.c_int32), ("precise", ctypes.c_int32)]
+
+
 class MtaError(RuntimeError):
     """A libmta call returned a negative mta_status."""
 
@@ -198,7 +227,11 @@ def lib():
             fn.argtypes = [ctypes.POINTER(mta_policy_args), vp]
         L.mta_policy_loss_workspace.argtypes = [i64, ctypes.POINTER(i64)]
         L.mta_ops_version.argtypes = []
-        for name in EXPORTS + OPS_EXPORTS:
+        L.mta_orthogonalize.argtypes = [ctypes.POINTER(mta_ortho_args), vp]
+        L.mta_orthogonalize_workspace.argtypes = [
+            ctypes.POINTER(mta_ortho_args), ctypes.POINTER(i64)]
+        L.mta_matrix_version.argtypes = []
+        for name in EXPORTS + OPS_EXPORTS + MATRIX_EXPORTS:
             if name != "mta_last_error":
                 getattr(L, name).restype = ctypes.c_int
         if L.mta_abi_version() != ABI_VERSION:
@@ -209,6 +242,11 @@ def lib():
             raise RuntimeError(
                 f"{LIB_PATH} has operators version {L.mta_ops_version()}, "
                 f"this binding speaks {OPS_VERSION}: rebuild the library")
+        if L.mta_matrix_version() != MATRIX_VERSION:
+            raise RuntimeError(
+                f"{LIB_PATH} has matrix operators version "
+                f"{L.mta_matrix_version()}, this binding speaks "
+                f"{MATRIX_VERSION}: rebuild the library")
         _lib = L
     return _lib
 
@@ -467,3 +505,23 @@ def mta_policy_loss_backward(args, stream=0):
 
 def mta_ops_version():
     return lib().mta_ops_version()
+
+
+def mta_orthogonalize_workspace(args):
+    """args: an mta_ortho_args, of which the matrices' sizes and `precise`
+    count."""
+    out = ctypes.c_int64()
+    _check(lib().mta_orthogonalize_workspace(ctypes.byref(args),
+                                             ctypes.byref(out)),
+           "mta_orthogonalize_workspace")
+    return out.value
+
+
+def mta_orthogonalize(args, stream=0):
+    """args: an mta_ortho_args."""
+    _check(lib().mta_orthogonalize(ctypes.byref(args), stream),
+           "mta_orthogonalize")
+
+
+def mta_matrix_version():
+    return lib().mta_matrix_version()

@@ -1,0 +1,119 @@
+// matrix_internal.h -- types shared by the host side and the gfx950 kernels of
+// the operators of include/mta_matrix.h.  Not part of the public C ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/mta_matrix.h"
+#include "mta_internal.h"
+
+namespace mta {
+
+// Elements between the rows of a plane of n columns: whole steps of 64, and
+// not a multiple of 1024, whose rows would lie in few of the memory's channels.
+__host__ __device__ constexpr int64_t plane_pitch(int64_t n) {
+  const int64_t p = (n + 63) / 64 * 64;
+  return p % 1024 == 0 ? p + 64 : p;
+}
+
+// ---- orthogonalised updates ---------------------------------------------
+
+constexpr int kOrthoItems = 40;  // matrices of a launch (they travel in the
+                                 // kernel's arguments, 4 KiB at most)
+constexpr int kOrthoParts = 256;  // workgroups that sum a matrix's squares
+
+// One matrix of a launch.  Its iterate X is [small, large].
+struct OrthoItem {
+  const void *g;
+  float *m;
+  void *out;
+  float *w;
+  void *w16;
+  uint8_t *ws;
+  int64_t ldg, ldout;
+  uint32_t rows, cols;
+  int planes;    // of a product's operands
+  float scale;   // of out
+  float update;  // -lr scale, of w
+};
+
+struct OrthoList {
+  OrthoItem item[kOrthoItems];
+  uint32_t first[kOrthoItems + 1];  // first workgroup of each matrix; the
+                                    // entry behind the last one is the grid
+  uint32_t count;
+};
+
+// What all launches of a call share.
+struct OrthoCall {
+  const float *d_coef;
+  const mta_amp_state *amp;
+  double eps;
+  float mu;
+  float decay;  // of w
+  float a, b, c;  // of the step
+  int type, out_type, copy_type, nesterov;
+  int whole;    // the diagonal times all digits of X, not those of the first
+                // plane alone
+  int which;    // the X that is read; the other one is written
+};
+static_assert(sizeof(OrthoList) + sizeof(OrthoCall) <= 4000,
+              "kernel argument space");
+
+// Planes of a product's operands: two, that is products of 22 bits, with
+// `precise` and for matrices of few rows or columns, whose errors do not
+// average out (3 x 3 with one plane: 2.3e-3 of the result, 16 x 16 6e-4).
+__host__ __device__ inline int ortho_planes(int64_t rows, int64_t cols,
+                                            int precise) {
+  return precise || rows < 16 || cols < 16 ? 2 : 1;
+}
+
+// A matrix's part of the workspace: two X of `planes` planes each, A and B,
+// their diagonals, the partial sums of squares.
+struct OrthoSpace {
+  int64_t small, large, pitch_x, pitch_a;
+  int64_t plane_x, plane_a;          // elements
+  // offsets in bytes, and from the first of two to the second
+  int64_t x, next_x, a, next_a, diag, next_diag, part, bytes;
+};
+__host__ __device__ inline OrthoSpace ortho_space(int64_t rows, int64_t cols,
+                                                  int planes) {
+  OrthoSpace s;
+  s.small = rows < cols ? rows : cols;
+  s.large = rows < cols ? cols : rows;
+  s.pitch_x = plane_pitch(s.large);
+  s.pitch_a = plane_pitch(s.small);
+  s.plane_x = s.small * s.pitch_x;
+  s.plane_a = s.small * s.pitch_a;
+  const auto round = [](int64_t x) { return (x + 255) / 256 * 256; };
+  s.x = 0;
+  s.next_x = round(s.plane_x * 2 * 2);
+  s.a = s.x + 2 * s.next_x;
+  s.next_a = round(s.plane_a * planes * 2);
+  s.diag = s.a + 2 * s.next_a;
+  s.next_diag = round(s.small * 4);
+  s.part = s.diag + 2 * s.next_diag;
+  s.bytes = s.part + kOrthoParts * 8;
+  return s;
+}
+
+// The tiles of a product's workgroups, and those of the kernels before it.
+enum OrthoStep { kOrthoGram, kOrthoSquare, kOrthoNext, kOrthoLast };
+constexpr int kOrthoLoadTile = 64;
+// Workgroups that sum a matrix's squares: 64 elements a lane, as long as they
+// are few enough for one read of their sums by every workgroup that follows.
+__host__ __device__ inline int64_t ortho_parts(int64_t rows, int64_t cols) {
+  const int64_t n = (rows * cols + 16383) / 16384;
+  return n < 1 ? 1 : n < kOrthoParts ? n : kOrthoParts;
+}
+hipError_t launch_ortho_norm(const OrthoList &l, const OrthoCall &c,
+                             hipStream_t s);
+hipError_t launch_ortho_load(const OrthoList &l, const OrthoCall &c,
+                             hipStream_t s);
+// tile: 256 or 128
+hipError_t launch_ortho_product(int step, int tile, const OrthoList &l,
+                                const OrthoCall &c, hipStream_t s);
+
+}  // namespace mta

@@ -1,0 +1,165 @@
+"""The operators of include/mta_matrix.h without a GPU: exports, struct
+layouts and the refusal of every bad argument before any device work."""
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+import mixed_precision_optimizer_mta_amd as M
+from mixed_precision_optimizer_mta_amd import _binding as B
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "mta_matrix.h")
+
+
+def test_library_exports_every_declared_operator():
+    text = re.sub(r"/\*.*?\*/", "", open(HEADER).read(), flags=re.S)
+    names = sorted(set(re.findall(r"\b(mta_[a-z0-9_]+)\s*\(", text)))
+    lib = ctypes.CDLL(B.LIB_PATH)
+    for name in names:
+        assert hasattr(lib, name), name
+    assert sorted(B.MATRIX_EXPORTS) == names
+    assert M.mta_matrix_version() == 1 == B.MATRIX_VERSION
+
+
+def test_struct_layouts():
+    assert ctypes.sizeof(B.mta_ortho_matrix) == 80
+    assert ctypes.sizeof(B.mta_ortho_args) == 112
+
+
+def _code(fn, *a):
+    with pytest.raises(M.MtaError) as e:
+        fn(*a)
+    return e.value.code
+
+
+G, MO, OUT, W, W16, WS = (k << 28 for k in range(1, 7))
+GOOD = dict(g=G, m=MO, out=OUT, w=W, w16=W16, rows=40, cols=70, ldg=70,
+            ldout=70, scale=1.0)
+
+
+def ortho(entries=None, co=(3.4445, -4.7750, 2.0315), **kw):
+    ms = [GOOD] if entries is None else entries
+    table = (B.mta_ortho_matrix * max(1, len(ms)))(
+        *[B.mta_ortho_matrix(**{**GOOD, **m}) for m in ms])
+    steps = kw.get("steps", 5)
+    flat = list(co) * max(1, min(steps, 16))
+    args = B.mta_ortho_args(
+        matrices=table, count=len(ms), workspace=WS,
+        workspace_bytes=1 << 27,
+        coefficients=(ctypes.c_double * len(flat))(*flat), eps=1e-7,
+        momentum=0.95, lr=0.02, weight_decay=0.1, steps=5, type=B.MTA_BF16,
+        out_type=B.MTA_BF16, copy_type=B.MTA_BF16, nesterov=1, precise=0)
+    for k, v in kw.items():
+        setattr(args, k, v)
+    args._keep = table
+    return args
+
+
+@pytest.mark.parametrize("matrix,kw,code", [
+    (dict(rows=-1), {}, -1),
+    (dict(cols=-1), {}, -1),
+    (dict(rows=(1 << 20) + 1), {}, -1),
+    (dict(cols=(1 << 20) + 1), {}, -1),
+    (dict(g=None), {}, -1),
+    (dict(out=None, w=None, w16=None), {}, -1),
+    (dict(w=None), {}, -1),                    # a copy without weights
+    (dict(scale=float("nan")), {}, -1),
+    (dict(scale=float("inf")), {}, -1),
+    (dict(ldg=69), {}, -1),
+    (dict(ldout=69), {}, -1),
+    (dict(ldg=1 << 60), {}, -1),
+    (dict(g=G + 1), {}, -2),
+    (dict(out=OUT + 1), {}, -2),
+    (dict(m=MO + 2), {}, -2),
+    (dict(w=W + 2), {}, -2),
+    (dict(w16=W16 + 1), {}, -2),
+    (dict(g=G + 2), dict(type=B.MTA_F32), -2),
+    (dict(out=G), {}, -1),                     # overlaps
+    (dict(m=G + 64), {}, -1),
+    (dict(w=MO), {}, -1),
+    (dict(w16=W + 16), {}, -1),
+    (dict(out=WS + 256), {}, -1),
+    ({}, dict(type=3), -3),
+    ({}, dict(out_type=-1), -3),
+    ({}, dict(copy_type=B.MTA_F32), -3),
+    ({}, dict(steps=0), -1),
+    ({}, dict(steps=17), -1),
+    ({}, dict(coefficients=None), -1),
+    ({}, dict(co=(3.4445, -4.7750, float("nan"))), -1),
+    ({}, dict(co=(9.0, 0.0, 0.0)), -1),        # grows to 9^5
+    ({}, dict(co=(3.4445, 4.7750, 2.0315)), -1),
+    ({}, dict(eps=-1e-9), -1),
+    ({}, dict(eps=float("nan")), -1),
+    ({}, dict(momentum=-0.1), -1),
+    ({}, dict(momentum=float("inf")), -1),
+    ({}, dict(lr=-1.0), -1),
+    ({}, dict(lr=float("nan")), -1),
+    ({}, dict(weight_decay=-1.0), -1),
+    ({}, dict(nesterov=2), -1),
+    ({}, dict(precise=2), -1),
+    ({}, dict(d_coef=0x7000001), -2),
+    ({}, dict(d_amp=0x7000004), -2),
+    ({}, dict(d_coef=W + 4), -1),
+    ({}, dict(workspace=None), -1),
+    ({}, dict(workspace=WS + 128), -2),
+    ({}, dict(workspace_bytes=1000), -1),
+    ({}, dict(matrices=None), -1),
+    ({}, dict(count=-1), -1),
+])
+def test_orthogonalize_refuses(matrix, kw, code):
+    co = kw.pop("co") if "co" in kw else (3.4445, -4.7750, 2.0315)
+    assert _code(B.mta_orthogonalize, ortho([matrix], co, **kw)) == code
+    assert M.mta_last_error() != ""
+
+
+def test_orthogonalize_refuses_shared_outputs_of_a_list():
+    far = {k: GOOD[k] + (1 << 20) for k in ("g", "m", "out", "w", "w16")}
+    assert _code(B.mta_orthogonalize,
+                 ortho([{}, {**far, "out": OUT + 100}])) == -1
+    assert "matrix" in M.mta_last_error() or "tensor" in M.mta_last_error()
+
+
+def test_orthogonalize_workspace():
+    one = B.mta_orthogonalize_workspace(ortho([{}]))
+    # two X of two planes, A and B, 40 rows each; the partial sums
+    assert one >= 40 * (128 * 2 * 2 * 2 + 64 * 2 * 2)
+    assert one % 256 == 0
+    assert B.mta_orthogonalize_workspace(ortho([{}], precise=1)) > one
+    # forty matrices share a launch
+    assert B.mta_orthogonalize_workspace(ortho([{}] * 40)) == 40 * one
+    assert B.mta_orthogonalize_workspace(ortho([{}] * 81)) == 40 * one
+    # 4 GiB at a time, unless one matrix needs more
+    big = dict(rows=8192, cols=8192)
+    each = B.mta_orthogonalize_workspace(ortho([big]))
+    assert B.mta_orthogonalize_workspace(ortho([big] * 30)) <= 1 << 32
+    assert B.mta_orthogonalize_workspace(
+        ortho([dict(rows=1 << 16, cols=1 << 16)])) > 1 << 32 > each
+    assert B.mta_orthogonalize_workspace(ortho([dict(rows=0)])) == 0
+    assert _code(B.mta_orthogonalize_workspace, ortho([dict(rows=-1)])) == -1
+
+
+def test_nothing_to_do_touches_no_device():
+    B.mta_orthogonalize(ortho([]))
+    B.mta_orthogonalize(ortho([dict(rows=0), dict(cols=0, g=None)],
+                              workspace=None, workspace_bytes=0))
+
+
+def test_python_refusals():
+    x = torch.zeros(4, 4)
+    with pytest.raises(ValueError, match="GPU"):
+        M.orthogonalize(x)
+    with pytest.raises(ValueError, match="steps"):
+        M.orthogonalize([], steps=0)
+    with pytest.raises(ValueError, match="coefficients"):
+        M.orthogonalize([], coefficients=(1.0, 2.0))
+    with pytest.raises(ValueError, match="coefficients"):
+        M.orthogonalize([], steps=3, coefficients=[(1.0, 2.0, 3.0)] * 2)
+    with pytest.raises(ValueError, match="one momentum"):
+        M.muon_update([x], [])
+    with pytest.raises(ValueError, match="scale"):
+        M.orthogonalize([x], scale=[1.0, 2.0])
+    with pytest.raises(ValueError, match="out"):
+        M.orthogonalize([x], out=[])
