@@ -7,6 +7,11 @@
  *   mta_orthogonalize     the orthogonalised update of the Muon rule for a
  *                         list of matrices: momentum, Newton-Schulz steps, and
  *                         the result written out or applied to the weights
+ *   mta_linear_loss       the cross entropy of a linear output layer from its
+ *                         input and weights, without keeping the logits, and
+ *                         its gradients with respect to both
+ *   mta_linear_loss_backward
+ *                         those gradients in a second call
  *
  * No call allocates, waits or keeps anything between calls, so all of them may
  * be captured into a HIP graph and calls on different streams are independent
@@ -91,6 +96,71 @@ int mta_orthogonalize(const mta_ortho_args *args, void *stream);
 /* Host only: workspace bytes of mta_orthogonalize for these arguments, of
  * which it looks at the matrices' sizes and at `precise`. */
 int mta_orthogonalize_workspace(const mta_ortho_args *args, int64_t *bytes);
+
+/* What the forward keeps of a row for mta_linear_loss_backward of the same
+ * library: softmax(z)[j] is exp(z[j] - top) / total.  All 0 in a row of weight
+ * 0. */
+typedef struct {
+  float top;    /* the row's largest logit */
+  float total;  /* the sum of exp(z - top) */
+  float weight; /* of the row in the loss */
+  float rest;   /* 1 - softmax(z)[target], with all its digits near 0 */
+} mta_linear_row;
+
+/* The cross entropy of a linear output layer, z = h w^T, summed over the rows
+ * (tokens) with weights:
+ *   loss = sum over rows of weight (-logp),  logp = log softmax(z)[target]
+ * and its gradients, times S = *d_grad_scale (1 when NULL):
+ *   dz[j] = S weight (softmax(z)[j] - [j == target])
+ *   dh = dz w,   dw (+)= dz^T h
+ * The logits are never stored: the gradients' half makes them a second time,
+ * in pieces of the vocabulary, and keeps one piece of dz, in h's type.
+ * A row whose target is ignore_index or whose weight is 0 is left out: its h
+ * is not read, its logp is 0 and its dh +0.  Without weights every other row
+ * has 1 / their number; a call without such rows has loss 0.  Another target
+ * outside [0, vocab) reads nothing out of range and makes the row's logp and
+ * dh, the loss and dw NaN.
+ * Products of 16-bit elements are exact, those of float32 elements are taken as
+ * the six largest of nine products of three bfloat16 values; sums are float32.
+ * dz is rounded once to the 16-bit type (float32: to three bfloat16 values)
+ * before dh and dw are made of it, scaled so that its largest weight is 1
+ * (float16: 2^14): neither S nor small weights cost digits. */
+typedef struct {
+  const void *h;              /* [rows, width], rows of ldh elements */
+  const void *w;              /* [vocab, width], rows of ldw elements */
+  const int64_t *targets;     /* [rows] */
+  const float *weights;       /* [rows], or NULL */
+  const float *d_grad_scale;  /* device float, or NULL: 1 */
+  void *dh;                   /* [rows, width], rows of lddh, or NULL */
+  void *dw;                   /* [vocab, width], rows of lddw, or NULL */
+  mta_linear_row *saved;      /* [rows], or NULL */
+  float *logp;                /* [rows], or NULL */
+  float *loss;                /* [1] */
+  void *workspace;            /* mta_linear_loss_workspace bytes */
+  int64_t workspace_bytes;
+  int64_t rows, vocab, width; /* rows may be 0; vocab >= 1, width >= 1 */
+  int64_t ldh, ldw, lddh, lddw;
+  int64_t ignore_index;
+  int32_t type;               /* of h, w and dh */
+  int32_t dw_type;
+  int32_t accumulate;         /* 0: overwrite dw, 1: add to what is there */
+  int32_t reserved;           /* 0 */
+} mta_linear_loss_args;
+
+/* The loss, and with dh or dw their gradients (saved may then be NULL too). */
+int mta_linear_loss(const mta_linear_loss_args *args, void *stream);
+
+/* The gradients from what mta_linear_loss saved for the same h, w and targets:
+ * reads h, w, targets, saved and d_grad_scale, writes dh and dw, one of which
+ * may be NULL.  weights, logp and loss are not looked at. */
+int mta_linear_loss_backward(const mta_linear_loss_args *args, void *stream);
+
+/* Host only: workspace bytes of either call for these arguments, of which it
+ * looks at the sizes and types, at w's address and pitch and at which of dh
+ * and dw are there, on a device of `cus` compute units (0: the current
+ * device's). */
+int mta_linear_loss_workspace(const mta_linear_loss_args *args, int32_t cus,
+                              int64_t *bytes);
 
 /* MTA_MATRIX_VERSION of the built library. */
 int mta_matrix_version(void);

@@ -4,7 +4,7 @@ The work runs in libmta.so (HIP, gfx950) behind the C ABI of include/mta.h
 (the optimizer step), include/mta_ops.h (what makes its gradients: 8-bit
 activation checkpoints with their backward, and a clipped policy loss) and
 include/mta_matrix.h (operators whose work is matrix products: orthogonalised
-updates).
+updates, and the cross entropy of a linear output layer).
 ``_binding`` mirrors that ABI name for name; ``MtaList`` marshals PyTorch
 tensors and the current HIP stream into it.  Nothing here computes any part
 of the step, and nothing falls back to another implementation: if
@@ -32,3 +32,7 @@ from .policy import (PolicyLoss, policy_loss,  # noqa: F401
                      policy_loss_grad)
 from ._binding import MATRIX_EXPORTS, mta_matrix_version  # noqa: F401
 from .muon import muon_update, orthogonalize  # noqa: F401
+from .linear_loss import (LinearLoss, linear_cross_entropy,  # noqa: F401
+                          linear_cross_entropy_backward,
+                          linear_cross_entropy_forward,
+                          linear_cross_entropy_grad)

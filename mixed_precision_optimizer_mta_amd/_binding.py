@@ -56,7 +56,8 @@ OPS_EXPORTS = ("mta_ckpt_pack", "mta_ckpt_unpack", "mta_ckpt_act_backward",
 
 # every symbol include/mta_matrix.h declares
 MATRIX_EXPORTS = ("mta_orthogonalize", "mta_orthogonalize_workspace",
-                  "mta_matrix_version")
+                  "mta_linear_loss", "mta_linear_loss_backward",
+                  "mta_linear_loss_workspace", "mta_matrix_version")
 
 
 class mta_tensor(ctypes.Structure):
@@ -155,6 +156,17 @@ class mta_ortho_args(ctypes.Structure):
                 ("nesterov", ctypes.c_int32), ("precise", ctypes.c_int32)]
 
 
+class mta_linear_loss_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("h", "w", "targets", "weights", "d_grad_scale", "dh", "dw",
+                 "saved", "logp", "loss", "workspace")] + \
+        [(n, ctypes.c_int64) for n in
+         ("workspace_bytes", "rows", "vocab", "width", "ldh", "ldw", "lddh",
+          "lddw", "ignore_index")] + \
+        [(n, ctypes.c_int32) for n in
+         ("type", "dw_type", "accumulate", "reserved")]
+
+
 class MtaError(RuntimeError):
     """A libmta call returned a negative mta_status."""
 
@@ -230,6 +242,11 @@ def lib():
         L.mta_orthogonalize.argtypes = [ctypes.POINTER(mta_ortho_args), vp]
         L.mta_orthogonalize_workspace.argtypes = [
             ctypes.POINTER(mta_ortho_args), ctypes.POINTER(i64)]
+        for fn in (L.mta_linear_loss, L.mta_linear_loss_backward):
+            fn.argtypes = [ctypes.POINTER(mta_linear_loss_args), vp]
+        L.mta_linear_loss_workspace.argtypes = [
+            ctypes.POINTER(mta_linear_loss_args), ctypes.c_int32,
+            ctypes.POINTER(i64)]
         L.mta_matrix_version.argtypes = []
         for name in EXPORTS + OPS_EXPORTS + MATRIX_EXPORTS:
             if name != "mta_last_error":
@@ -521,6 +538,25 @@ def mta_orthogonalize(args, stream=0):
     """args: an mta_ortho_args."""
     _check(lib().mta_orthogonalize(ctypes.byref(args), stream),
            "mta_orthogonalize")
+
+
+def mta_linear_loss_workspace(args, cus=0):
+    out = ctypes.c_int64()
+    _check(lib().mta_linear_loss_workspace(ctypes.byref(args), cus,
+                                           ctypes.byref(out)),
+           "mta_linear_loss_workspace")
+    return out.value
+
+
+def mta_linear_loss(args, stream=0):
+    """args: an mta_linear_loss_args."""
+    _check(lib().mta_linear_loss(ctypes.byref(args), stream),
+           "mta_linear_loss")
+
+
+def mta_linear_loss_backward(args, stream=0):
+    _check(lib().mta_linear_loss_backward(ctypes.byref(args), stream),
+           "mta_linear_loss_backward")
 
 
 def mta_matrix_version():

@@ -26,6 +26,7 @@
 // 1228 there.  Tiles of 128 x 128, two workgroups a CU, are at 1000.
 #pragma once
 
+#include "matrix_internal.h"
 #include "ops_device.h"
 
 namespace mta {
@@ -74,9 +75,9 @@ struct Pairs {
 };
 __host__ __device__ constexpr Pairs pairs_of(int planes) {
   // 1: hi hi.  2: lo hi, hi lo, hi hi.  3: 2 0, 0 2, 1 1, 1 0, 0 1, 0 0.
-  return planes == 1 ? Pairs{1, 0, 0}
-         : planes == 2 ? Pairs{3, 0x01, 0x04}
-                       : Pairs{6, 0x052, 0x118};
+  return planes == 1   ? Pairs{pair_count(1), 0, 0}
+         : planes == 2 ? Pairs{pair_count(2), 0x01, 0x04}
+                       : Pairs{pair_count(3), 0x052, 0x118};
 }
 
 // A value that is the same in all lanes, for the scalar registers.

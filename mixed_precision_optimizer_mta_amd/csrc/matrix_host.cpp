@@ -13,12 +13,16 @@
 
 static_assert(sizeof(mta_ortho_matrix) == 80, "mta_ortho_matrix layout");
 static_assert(sizeof(mta_ortho_args) == 112, "mta_ortho_args layout");
+static_assert(sizeof(mta_linear_loss_args) == 176,
+              "mta_linear_loss_args layout");
 
 namespace {
 
 using namespace mta::check;
 
 long long ll(int64_t x) { return static_cast<long long>(x); }
+
+int64_t up(int64_t n, int64_t d) { return (n + d - 1) / d; }
 
 // ---- orthogonalised updates ---------------------------------------------
 
@@ -172,8 +176,6 @@ std::vector<OrthoGroup> ortho_groups(const mta_ortho_args *a) {
   return groups;
 }
 
-int64_t up(int64_t n, int64_t d) { return (n + d - 1) / d; }
-
 // Output tiles of a matrix in one product.
 int64_t ortho_tiles(int step, int64_t rows, int64_t cols, int64_t tile) {
   const int64_t m = up(std::min(rows, cols), tile);
@@ -262,9 +264,286 @@ hipError_t run_ortho(const mta_ortho_args *a,
   return e;
 }
 
+// ---- cross entropy of a linear output layer -----------------------------
+
+constexpr int64_t kMostVocab = int64_t{1} << 28;
+// (255 rows of an operand are a 32-bit offset on the device)
+constexpr int64_t kMostWidth = int64_t{1} << 20;
+constexpr int64_t kMostPitch = int64_t{1} << 22;
+constexpr int64_t kMostRows = int64_t{1} << 30;
+// Workgroups of a launch.
+constexpr int64_t kMostGroups = int64_t{1} << 22;
+// dz of a piece of the vocabulary, at most, unless 256 columns need more.
+constexpr int64_t kPieceBytes = int64_t{256} << 20;
+
+// Whether the products can read w where it is.
+bool lies_well(const mta_linear_loss_args *a) {
+  return a->type != MTA_F32 && a->width % 64 == 0 && a->ldw % 8 == 0 &&
+         a->ldw <= kMostPitch && aligned(a->w, 16);
+}
+
+// How a product of m x n outputs over k is dealt out.  In us, measured here: a
+// step of 64 of k takes the large tile 1.8 and two small ones that share a CU
+// 1.1, one alone 0.65; a workgroup's start and end 6 and 4; the joining of
+// parts 5 and their bytes at 4 TB/s.
+mta::LinearCut linear_cut(int64_t m, int64_t n, int64_t k, int runs, int most,
+                          int cus) {
+  mta::LinearCut best{};
+  double best_us = 0.0;
+  const int64_t steps = std::max<int64_t>(1, up(k, 64));
+  for (int tile : {256, 128}) {
+    const int64_t tiles = up(m, tile) * up(n, tile);
+    for (int64_t parts = 1; parts <= most; ++parts) {
+      if (parts > 1 && parts * 4 > steps) break;
+      const int64_t each = up(steps, parts);
+      const int64_t groups = tiles * parts;
+      const int64_t held = tile == 256 ? 1 : 2;
+      const double step = tile == 256 ? 1.8 : groups <= cus ? 0.65 : 1.1;
+      double us = static_cast<double>(up(groups, cus * held)) *
+                  (step * static_cast<double>(each * runs) +
+                   (tile == 256 ? 6.0 : 4.0));
+      if (parts > 1)
+        us += 5.0 + static_cast<double>(parts) * static_cast<double>(m) *
+                        static_cast<double>(n) * 8.0 / 4e6;
+      if (best.tile && us >= best_us) continue;
+      best_us = us;
+      best.tile = tile;
+      best.parts = static_cast<int>(up(steps, each));
+      best.part_k = each * 64;
+      if (groups > 8 * cus) break;
+    }
+  }
+  return best;
+}
+
+mta::LinearPlan linear_plan(const mta_linear_loss_args *a, bool copy_w,
+                            int cus) {
+  mta::LinearPlan p{};
+  p.planes = a->type == MTA_F32 ? 3 : 1;
+  const int runs = mta::pair_count(p.planes);
+  p.copy_w = copy_w;
+  p.pitch = mta::plane_pitch(a->width);
+  p.deep_rows = up(a->rows, 64) * 64;
+  const bool grad = a->dh || a->dw;
+  p.logits = linear_cut(a->rows, a->vocab, a->width, runs, 1, cus);
+  if (grad) {
+    const int64_t column = std::max<int64_t>(1, p.deep_rows) * 2 * p.planes;
+    const int64_t most =
+        std::max<int64_t>(256, kPieceBytes / column / 256 * 256);
+    p.pieces = up(a->vocab, most);
+    p.piece = p.pieces == 1 ? a->vocab
+                            : up(up(a->vocab, p.pieces), 256) * 256;
+    p.pieces = up(a->vocab, p.piece);
+    p.pitch_z = mta::plane_pitch(p.piece);
+    p.grad = linear_cut(a->rows, p.piece, a->width, runs, 1, cus);
+    p.dh = linear_cut(a->rows, a->width, p.piece, runs, 32, cus);
+    p.dw = linear_cut(p.piece, a->width, a->rows, runs, 32, cus);
+    p.hold_dh = a->dh && (p.pieces > 1 || p.dh.parts > 1);
+    p.hold_dw = a->dw && p.dw.parts > 1;
+  }
+  int64_t at = 0;
+  const auto take = [&](int64_t bytes) {
+    const int64_t here = at;
+    at += up(bytes, 256) * 256;
+    return here;
+  };
+  p.scalars = take(8);
+  p.terms = take(a->rows * 8);
+  p.rows = take(a->rows * 16);
+  p.z_target = take(a->rows * 4);
+  p.partial = take(up(a->vocab, p.logits.tile) * a->rows * 8);
+  p.h = take(a->rows * p.pitch * 2 * p.planes);
+  p.w = take(copy_w ? a->vocab * p.pitch * 2 * p.planes : 0);
+  p.z = take(grad ? p.deep_rows * p.pitch_z * 2 * p.planes : 0);
+  p.sum_h = take(p.hold_dh ? p.dh.parts * a->rows * p.pitch * 4 : 0);
+  p.sum_w = take(p.hold_dw ? p.dw.parts * p.piece * p.pitch * 4 : 0);
+  p.bytes = at;
+  return p;
+}
+
+int check_linear_sizes(const mta_linear_loss_args *a) {
+  if (!a) return fail(MTA_EINVAL, "args is NULL");
+  if (a->rows < 0 || a->rows > kMostRows)
+    return fail(MTA_EINVAL, "rows must be in [0, 2^30]");
+  if (a->vocab < 1 || a->vocab > kMostVocab)
+    return fail(MTA_EINVAL, "vocab must be in [1, 2^28] (got %lld)",
+                ll(a->vocab));
+  if (a->width < 1 || a->width > kMostWidth)
+    return fail(MTA_EINVAL, "width must be in [1, 2^20] (got %lld)",
+                ll(a->width));
+  if (!known_type(a->type)) return fail(MTA_EDTYPE, "unknown type %d", a->type);
+  if (up(a->rows, 128) * up(a->vocab, 128) > kMostGroups ||
+      up(a->vocab, 128) * up(a->width, 128) > kMostGroups ||
+      up(a->rows, 128) * up(a->width, 128) > kMostGroups)
+    return fail(MTA_EINVAL, "too large");
+  return MTA_OK;
+}
+
+int check_linear(const mta_linear_loss_args *a, bool backward,
+                 mta::LinearPlan *plan) {
+  int rc = check_linear_sizes(a);
+  if (rc) return rc;
+  if (!known_type(a->dw_type))
+    return fail(MTA_EDTYPE, "unknown type %d", a->dw_type);
+  if (a->accumulate != 0 && a->accumulate != 1)
+    return fail(MTA_EINVAL, "accumulate must be 0 or 1");
+  if (a->reserved) return fail(MTA_EINVAL, "reserved must be 0");
+  const int64_t sz = size_of(a->type), wsz = size_of(a->dw_type);
+  if (!a->w) return fail(MTA_EINVAL, "w is NULL");
+  if (a->rows > 0 && (!a->h || !a->targets))
+    return fail(MTA_EINVAL, "h or targets is NULL");
+  if (backward && a->rows > 0 && !a->saved)
+    return fail(MTA_EINVAL, "saved is NULL");
+  if (backward && !a->dh && !a->dw)
+    return fail(MTA_EINVAL, "neither dh nor dw");
+  if (!backward && !a->loss) return fail(MTA_EINVAL, "loss is NULL");
+  if (a->ldh < a->width || a->ldw < a->width ||
+      (a->dh && a->lddh < a->width) || (a->dw && a->lddw < a->width))
+    return fail(MTA_EINVAL, "a row pitch is below width");
+  if (!fits(a->rows, a->ldh, 4) || !fits(a->vocab, a->ldw, 4) ||
+      (a->dh && !fits(a->rows, a->lddh, 4)) ||
+      (a->dw && !fits(a->vocab, a->lddw, 4)))
+    return fail(MTA_EINVAL, "too large");
+  if (!aligned(a->h, sz) || !aligned(a->w, sz) || !aligned(a->dh, sz) ||
+      !aligned(a->dw, wsz) || !aligned(a->targets, 8) ||
+      !aligned(a->weights, 4) || !aligned(a->d_grad_scale, 4) ||
+      !aligned(a->saved, 16) || !aligned(a->logp, 4) || !aligned(a->loss, 4))
+    return fail(MTA_EALIGN, "a buffer is not aligned to its element size");
+  std::vector<Region> r;
+  r.reserve(16);
+  const auto flat = [&](const void *p, int64_t bytes, const char *name,
+                        bool written) {
+    if (p && bytes > 0)
+      r.push_back(region(p, 1, bytes, bytes, name, -1, written));
+  };
+  const auto rows = [&](const void *p, int64_t n, int64_t ld, int64_t size,
+                        const char *name, bool written) {
+    if (p)
+      r.push_back(region(p, n, ld * size, a->width * size, name, -1, written));
+  };
+  rows(a->h, a->rows, a->ldh, sz, "h", false);
+  rows(a->w, a->vocab, a->ldw, sz, "w", false);
+  rows(a->dh, a->rows, a->lddh, sz, "dh", true);
+  rows(a->dw, a->vocab, a->lddw, wsz, "dw", true);
+  flat(a->targets, a->rows * 8, "targets", false);
+  flat(a->d_grad_scale, 4, "d_grad_scale", false);
+  flat(a->saved, a->rows * 16, "saved", !backward);
+  if (!backward) {
+    flat(a->weights, a->rows * 4, "weights", false);
+    flat(a->logp, a->rows * 4, "logp", true);
+    flat(a->loss, 4, "loss", true);
+  }
+  if ((rc = check_regions(&r))) return rc;
+  int cus = 0;
+  if ((rc = current_cus(&cus))) return rc;
+  *plan = linear_plan(a, !lies_well(a), cus);
+  const int64_t need = plan->bytes;
+  if (!a->workspace) return fail(MTA_EINVAL, "workspace is NULL");
+  if (a->workspace_bytes < need)
+    return fail(MTA_EINVAL, "workspace has %lld bytes, %lld are needed",
+                ll(a->workspace_bytes), ll(need));
+  if (!aligned(a->workspace, 256))
+    return fail(MTA_EALIGN, "workspace must be 256-byte aligned");
+  flat(a->workspace, need, "workspace", true);
+  return check_regions(&r);
+}
+
+hipError_t run_linear(const mta_linear_loss_args *a, const mta::LinearPlan &p,
+                      bool backward, hipStream_t s) {
+  uint8_t *ws = static_cast<uint8_t *>(a->workspace);
+  mta::LinearArgs l{};
+  l.a = *a;
+  l.rows = a->saved ? a->saved
+                    : reinterpret_cast<mta_linear_row *>(ws + p.rows);
+  l.scalars = reinterpret_cast<float *>(ws + p.scalars);
+  l.terms = reinterpret_cast<double *>(ws + p.terms);
+  l.z_target = reinterpret_cast<float *>(ws + p.z_target);
+  l.partial = reinterpret_cast<float2 *>(ws + p.partial);
+  l.h = reinterpret_cast<uint16_t *>(ws + p.h);
+  l.z = reinterpret_cast<uint16_t *>(ws + p.z);
+  l.sum_h = reinterpret_cast<float *>(ws + p.sum_h);
+  l.sum_w = reinterpret_cast<float *>(ws + p.sum_w);
+  l.planes = p.planes;
+  l.backward = backward;
+  l.pitch = p.pitch;
+  l.pitch_z = p.pitch_z;
+  l.deep_rows = p.deep_rows;
+  l.h_plane = a->rows * p.pitch;
+  l.z_plane = p.deep_rows * p.pitch_z;
+  l.tiles = up(a->vocab, p.logits.tile);
+  hipError_t e;
+  const auto ok = [&](hipError_t x) { return (e = x) == hipSuccess; };
+  if (!ok(mta::launch_linear_weights(l, s))) return e;
+  if (a->rows > 0) {
+    if (!ok(mta::launch_linear_pack_h(l, s))) return e;
+    if (p.copy_w) {
+      uint16_t *to = reinterpret_cast<uint16_t *>(ws + p.w);
+      l.w = to;
+      l.w_pitch = p.pitch;
+      l.w_plane = a->vocab * p.pitch;
+      if (!ok(mta::launch_linear_pack_w(l, to, s))) return e;
+    } else {
+      l.w = static_cast<const uint16_t *>(a->w);
+      l.w_pitch = a->ldw;
+    }
+  }
+  if (!backward) {
+    if (a->rows > 0 && !ok(mta::launch_linear_logits(l, p.logits, s))) return e;
+    if (!ok(mta::launch_linear_rows(l, s))) return e;
+  }
+  if (!a->dh && !a->dw) return e;
+  if (a->rows == 0) return a->dw ? mta::launch_linear_none(l, s) : e;
+  for (int64_t k = 0; k < p.pieces; ++k) {
+    l.first = k * p.piece;
+    l.count = std::min(p.piece, a->vocab - l.first);
+    if (!ok(mta::launch_linear_grad(l, p.grad, s))) return e;
+    if (a->dh && !ok(mta::launch_linear_dh(l, p.dh, p.hold_dh, s))) return e;
+    if (!a->dw) continue;
+    if (!ok(mta::launch_linear_dw(l, p.dw, p.hold_dw, s))) return e;
+    if (p.hold_dw && !ok(mta::launch_linear_out(l, false, p.dw.parts, s)))
+      return e;
+  }
+  if (p.hold_dh) e = mta::launch_linear_out(l, true, p.dh.parts, s);
+  return e;
+}
+
+int call_linear(const mta_linear_loss_args *a, bool backward, void *stream,
+                const char *what) {
+  mta::LinearPlan plan{};
+  try {
+    const int rc = check_linear(a, backward, &plan);
+    if (rc) return rc;
+  } catch (const std::bad_alloc &) {
+    return fail(MTA_ENOMEM, "host allocation failed");
+  }
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return mta::report_launch(run_linear(a, plan, backward, s), s, what);
+}
+
 }  // namespace
 
 extern "C" {
+
+int mta_linear_loss_workspace(const mta_linear_loss_args *a, int32_t cus,
+                              int64_t *bytes) {
+  if (!bytes) return fail(MTA_EINVAL, "bytes is NULL");
+  *bytes = 0;
+  int rc = check_linear_sizes(a);
+  if (rc) return rc;
+  if (cus < 0) return fail(MTA_EINVAL, "cus must be >= 0");
+  int n = cus;
+  if (n == 0 && (rc = current_cus(&n))) return rc;
+  *bytes = linear_plan(a, !lies_well(a), n).bytes;
+  return ok();
+}
+
+int mta_linear_loss(const mta_linear_loss_args *args, void *stream) {
+  return call_linear(args, false, stream, "mta_linear_loss");
+}
+
+int mta_linear_loss_backward(const mta_linear_loss_args *args, void *stream) {
+  return call_linear(args, true, stream, "mta_linear_loss_backward");
+}
 
 int mta_matrix_version(void) { return MTA_MATRIX_VERSION; }
 

@@ -18,6 +18,11 @@ __host__ __device__ constexpr int64_t plane_pitch(int64_t n) {
   return p % 1024 == 0 ? p + 64 : p;
 }
 
+// Products of planes that make one product: all but those of the smallest.
+__host__ __device__ constexpr int pair_count(int planes) {
+  return planes == 1 ? 1 : planes == 2 ? 3 : 6;
+}
+
 // ---- orthogonalised updates ---------------------------------------------
 
 constexpr int kOrthoItems = 40;  // matrices of a launch (they travel in the
@@ -115,5 +120,70 @@ hipError_t launch_ortho_load(const OrthoList &l, const OrthoCall &c,
 // tile: 256 or 128
 hipError_t launch_ortho_product(int step, int tile, const OrthoList &l,
                                 const OrthoCall &c, hipStream_t s);
+
+// ---- cross entropy of a linear output layer -----------------------------
+
+static_assert(sizeof(mta_linear_row) == 16, "saved row layout");
+
+// One product of a call: its tile and into how many parts of k it is cut, whose
+// sums a second kernel joins.
+struct LinearCut {
+  int tile;
+  int parts;
+  int64_t part_k;  // multiples of 64
+};
+
+// The course of a call.
+struct LinearPlan {
+  int planes;
+  bool copy_w;          // w does not lie as the products want it
+  int64_t pitch;        // of h's and w's planes
+  int64_t piece;        // columns of the vocabulary at a time, all but the last
+  int64_t pieces;
+  int64_t pitch_z;      // of dz
+  int64_t deep_rows;    // rows of dz: whole steps of 64
+  LinearCut logits, grad, dh, dw;
+  bool hold_dh, hold_dw;  // sums held in the workspace before they go out
+  // offsets in the workspace
+  int64_t scalars, terms, rows, z_target, partial, h, w, z, sum_h, sum_w, bytes;
+};
+
+struct LinearArgs {
+  mta_linear_loss_args a;
+  mta_linear_row *rows;   // of the workspace or the caller's
+  float *scalars;         // [0] weight of a row without weights, [1] largest
+  double *terms;          // [rows] of the loss
+  float *z_target;        // [rows]
+  float2 *partial;        // [tiles][rows]: largest, sum without the target
+  uint16_t *h;            // planes
+  const uint16_t *w;
+  uint16_t *z;            // planes of a piece of dz
+  float *sum_h, *sum_w;   // [parts][rows or piece][pitch]
+  int64_t h_plane, w_plane, w_pitch, z_plane;
+  int64_t pitch, pitch_z, deep_rows;
+  int64_t first, count;   // the piece
+  int64_t tiles;          // of the vocabulary
+  int planes;
+  int backward;           // rows are the caller's, and say what is left out
+};
+
+hipError_t launch_linear_weights(const LinearArgs &l, hipStream_t s);
+hipError_t launch_linear_pack_h(const LinearArgs &l, hipStream_t s);
+hipError_t launch_linear_pack_w(const LinearArgs &l, uint16_t *to,
+                                hipStream_t s);
+hipError_t launch_linear_logits(const LinearArgs &l, const LinearCut &c,
+                                hipStream_t s);
+hipError_t launch_linear_rows(const LinearArgs &l, hipStream_t s);
+hipError_t launch_linear_grad(const LinearArgs &l, const LinearCut &c,
+                              hipStream_t s);
+// hold: into sum_h (added to what is there after the first piece)
+hipError_t launch_linear_dh(const LinearArgs &l, const LinearCut &c, bool hold,
+                            hipStream_t s);
+hipError_t launch_linear_dw(const LinearArgs &l, const LinearCut &c, bool hold,
+                            hipStream_t s);
+// dw of no rows
+hipError_t launch_linear_none(const LinearArgs &l, hipStream_t s);
+hipError_t launch_linear_out(const LinearArgs &l, bool dh, int parts,
+                             hipStream_t s);
 
 }  // namespace mta

@@ -27,6 +27,7 @@ def test_library_exports_every_declared_operator():
 def test_struct_layouts():
     assert ctypes.sizeof(B.mta_ortho_matrix) == 80
     assert ctypes.sizeof(B.mta_ortho_args) == 112
+    assert ctypes.sizeof(B.mta_linear_loss_args) == 176
 
 
 def _code(fn, *a):
@@ -163,3 +164,89 @@ def test_python_refusals():
         M.orthogonalize([x], scale=[1.0, 2.0])
     with pytest.raises(ValueError, match="out"):
         M.orthogonalize([x], out=[])
+
+
+H, WT, T, WS2, SC, DH, DW, SV, LP, LO = (k << 28 for k in range(8, 18))
+
+
+def linear(**kw):
+    a = B.mta_linear_loss_args(
+        h=H, w=WT, targets=T, weights=None, d_grad_scale=SC, dh=DH, dw=DW,
+        saved=SV, logp=LP, loss=LO, workspace=WS2, workspace_bytes=1 << 27,
+        rows=20, vocab=50, width=64, ldh=64, ldw=64, lddh=64, lddw=64,
+        ignore_index=-100, type=B.MTA_BF16, dw_type=B.MTA_F32)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+REFUSED = [
+    (dict(rows=-1), -1), (dict(rows=(1 << 30) + 1), -1),
+    (dict(vocab=0), -1), (dict(vocab=(1 << 28) + 1), -1),
+    (dict(width=0), -1), (dict(width=(1 << 20) + 1), -1),
+    (dict(rows=1 << 30, vocab=1 << 28), -1),
+    (dict(type=3), -3), (dict(dw_type=-1), -3),
+    (dict(accumulate=2), -1), (dict(reserved=1), -1),
+    (dict(h=None), -1), (dict(w=None), -1), (dict(targets=None), -1),
+    (dict(ldh=63), -1), (dict(ldw=63), -1), (dict(lddh=63), -1),
+    (dict(lddw=63), -1), (dict(ldw=1 << 60), -1),
+    (dict(h=H + 1), -2), (dict(w=WT + 1), -2), (dict(dh=DH + 1), -2),
+    (dict(dw=DW + 2), -2), (dict(targets=T + 4), -2),
+    (dict(d_grad_scale=SC + 2), -2), (dict(saved=SV + 8), -2),
+    (dict(dh=H), -1), (dict(dw=WT), -1), (dict(dw=DH + 64), -1),
+    (dict(dh=T), -1), (dict(dw=SC), -1),
+]
+
+
+@pytest.mark.parametrize("kw,code", REFUSED + [
+    (dict(loss=None), -1), (dict(loss=LO + 2), -2), (dict(logp=LP + 1), -2),
+    (dict(weights=LP + 4), -1), (dict(weights=0x7000002), -2),
+    (dict(logp=LO), -1), (dict(saved=H + 128), -1)])
+def test_linear_loss_refuses(kw, code):
+    assert _code(B.mta_linear_loss, linear(**kw)) == code
+    assert M.mta_last_error() != ""
+
+
+@pytest.mark.parametrize("kw,code", REFUSED + [
+    (dict(saved=None), -1), (dict(dh=None, dw=None), -1),
+    (dict(dh=SV), -1)])
+def test_linear_loss_backward_refuses(kw, code):
+    assert _code(B.mta_linear_loss_backward, linear(**kw)) == code
+
+
+def test_linear_loss_workspace():
+    def need(**kw):
+        return B.mta_linear_loss_workspace(linear(**kw), 256)
+
+    big = dict(rows=8192, vocab=50257, width=1600, ldh=1600, ldw=1600,
+               lddh=1600, lddw=1600)
+    loss = need(**big, dh=None, dw=None)
+    both = need(**big)
+    # no logits: 823 MB in 16 bits; a piece of dz is 256 MiB at most, the
+    # hidden states' sums in 32 bits are 52 MB
+    assert loss < 100 << 20 < both < 420 << 20
+    # the vocabulary adds its tiles' partial sums alone
+    more = need(**{**big, "vocab": 4 * 50257})
+    assert more - both <= 8 * 8192 * (3 * 50257 // 128 + 1) + (300 << 20)
+    # a weight that is not as the products want it is laid out again
+    assert need(**{**big, "w": WT + 2}) >= both + 50257 * 1600 * 2
+    assert need(rows=0) < 1 << 20
+    assert _code(B.mta_linear_loss_workspace, linear(), -1) == -1
+    assert _code(B.mta_linear_loss_workspace, linear(vocab=0), 256) == -1
+    for rows, vocab, width in [(1, 1, 1), (3, 100000, 7), (70000, 2, 9),
+                               (1 << 20, 1 << 10, 64)]:
+        for cus in (1, 8, 256, 304):
+            assert B.mta_linear_loss_workspace(
+                linear(rows=rows, vocab=vocab, width=width, ldh=width,
+                       ldw=width, lddh=width, lddw=width), cus) % 256 == 0
+
+
+def test_linear_loss_python_refusals():
+    h, w = torch.zeros(4, 8), torch.zeros(5, 8)
+    t = torch.zeros(4, dtype=torch.int64)
+    with pytest.raises(ValueError, match="GPU"):
+        M.linear_cross_entropy_grad(h, w, t)
+    with pytest.raises(TypeError, match="hidden"):
+        M.linear_cross_entropy_forward(h.double(), w, t)
+    with pytest.raises(ValueError, match="GPU"):
+        M.linear_cross_entropy(h, w, t)
