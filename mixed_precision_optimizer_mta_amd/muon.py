@@ -59,14 +59,19 @@ def _scales(scale, count):
     return scales
 
 
-def run(entries, dev, type, out_type, copy_type, coefficients, eps, momentum,
+def table(entries):
+    """The matrices of a call: entries (g, m, out, w, w16 as addresses, rows,
+    cols, ldg, ldout, scale)."""
+    return (B.mta_ortho_matrix * max(1, len(entries)))(
+        *[B.mta_ortho_matrix(*e) for e in entries]), len(entries)
+
+
+def run(matrices, dev, type, out_type, copy_type, coefficients, eps, momentum,
         nesterov, precise, lr=0.0, weight_decay=0.0, coef=None, amp=None):
-    """One mta_orthogonalize over entries (g, m, out, w, w16 as addresses,
-    rows, cols, ldg, ldout, scale), its workspace from PyTorch's allocator."""
-    table = (B.mta_ortho_matrix * max(1, len(entries)))(
-        *[B.mta_ortho_matrix(*e) for e in entries])
+    """One mta_orthogonalize over a table(), its workspace from PyTorch's
+    allocator."""
     args = B.mta_ortho_args(
-        matrices=table, count=len(entries), coefficients=coefficients,
+        matrices=matrices[0], count=matrices[1], coefficients=coefficients,
         d_coef=coef, d_amp=amp, eps=eps, momentum=momentum, lr=lr,
         weight_decay=weight_decay, steps=len(coefficients) // 3, type=type,
         out_type=out_type, copy_type=copy_type, nesterov=int(bool(nesterov)),
@@ -123,7 +128,7 @@ def _call(xs, moms, out, dtype, scale, steps, coefficients, eps, momentum,
                         ld, _matrix(o, "out")[2], scales[i]))
     if precise is None:
         precise = odt != torch.bfloat16
-    run(entries, dev, _G[dt], _G[odt], B.MTA_BF16, co, eps, momentum,
+    run(table(entries), dev, _G[dt], _G[odt], B.MTA_BF16, co, eps, momentum,
         nesterov, precise)
     if out is not None:
         _written(*outs)

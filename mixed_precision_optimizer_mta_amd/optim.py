@@ -51,6 +51,18 @@ accumulate updates in float32.  A parameter the model keeps in float32 (one
 whose uses need full precision) is its own master and takes no copy; its
 float32 gradient joins the same joint clip.
 
+``kind="muon"``, for the whole optimizer or as an option of a parameter group
+beside groups of the optimizer's own kind, is for matrices (a parameter of more
+dimensions counts as [shape[0], the rest]): a float32 momentum takes the
+gradient in, and the weights take the orthogonalised momentum
+(mta_orthogonalize, one call per group and gradient dtype) times lr and a scale
+of the matrix's shape, with decoupled weight decay.  The joint clip, the loss
+scale, master weights and capturing are those of the other kinds:
+
+    MtaOptimizer([{"params": matrices, "kind": "muon", "lr": 0.02,
+                   "momentum": 0.95}, {"params": others}],
+                 kind="adamw", lr=3e-4, max_norm=1.0)
+
 Every step of the arithmetic runs in libmta.  Parameters are float32 CUDA
 tensors (with master_weights, also bfloat16 or float16 ones); gradients are
 float32, bfloat16 or float16, a 16-bit parameter's in its own dtype.  The
@@ -74,34 +86,55 @@ checked when the plan is built.  The per-parameter ``state[p]["step"]`` is
 brought up to date by ``state_dict()`` (and whenever the plan is rebuilt);
 in between, the count lives with the plan.
 """
+import math
+
 import torch
 
 from . import _binding as B
+from . import muon
 from .torch_list import MtaList, clip_norm_joint
 
-_KINDS = ("adamw", "adam", "sgd", "momentum")
+_KINDS = ("adamw", "adam", "sgd", "momentum", "muon")
 _GTYPE = {torch.float32: B.MTA_F32, torch.bfloat16: B.MTA_BF16,
           torch.float16: B.MTA_F16}
 
 
 class MtaOptimizer(torch.optim.Optimizer):
     """kind: "adamw" (decoupled decay), "adam" (coupled decay), "sgd",
-    "momentum" (SGD with momentum, no dampening, not Nesterov)."""
+    "momentum" (SGD with momentum, no dampening, not Nesterov), "muon"
+    (orthogonalised momentum, for matrices; also the "kind" of single groups).
+
+    For muon: momentum is the group's, nesterov looks one momentum ahead,
+    ns_steps, ns_coefficients and ns_eps are those of ``orthogonalize``, and
+    ns_precise its `precise` (by default for float32 gradients).  update_scale
+    is the factor of a [rows, cols] matrix's update: "spectral" for
+    sqrt(max(1, rows / cols)), "rms" for 0.2 sqrt(max(rows, cols)) (entries of
+    the size of AdamW's), or a number."""
 
     def __init__(self, params, kind="adamw", lr=1e-3, betas=(0.9, 0.999),
                  eps=1e-8, weight_decay=0.0, momentum=0.0, max_norm=None,
                  packed_moments=False, zero_grad=False, loss_scale=None,
                  growth_factor=2.0, backoff_factor=0.5,
                  growth_interval=2000, capturable=False,
-                 master_weights=False):
+                 master_weights=False, nesterov=True, ns_steps=5,
+                 ns_coefficients=muon.COEFFICIENTS, ns_eps=1e-7,
+                 ns_precise=None, update_scale="spectral"):
         if kind not in _KINDS:
             raise ValueError(f"kind must be one of {_KINDS}")
+        if update_scale not in ("spectral", "rms") and not (
+                isinstance(update_scale, (int, float)) and
+                math.isfinite(update_scale)):
+            raise ValueError('update_scale is "spectral", "rms" or a number')
         if packed_moments and kind not in ("adamw", "adam"):
             raise ValueError("packed moments are for the Adam family")
         defaults = dict(lr=lr, betas=tuple(betas), eps=eps,
                         weight_decay=weight_decay, momentum=momentum)
-        super().__init__(params, defaults)
         self.kind = kind
+        self._ns = dict(
+            coefficients=muon._coefficients(ns_coefficients, ns_steps),
+            eps=float(ns_eps), nesterov=bool(nesterov), precise=ns_precise,
+            scale=update_scale)
+        super().__init__(params, defaults)
         self.max_norm = max_norm
         self.packed = bool(packed_moments)
         self.zero_grad_in_step = bool(zero_grad)
@@ -135,6 +168,23 @@ class MtaOptimizer(torch.optim.Optimizer):
         upload and a wait on the host), as any address change does."""
         super().zero_grad(set_to_none=set_to_none)
 
+    def add_param_group(self, param_group):
+        """As torch.optim.Optimizer.add_param_group; a group may have the
+        "kind" "muon" of its own, which takes matrices alone."""
+        kind = param_group.get("kind", self.kind)
+        if kind != self.kind and kind != "muon":
+            raise ValueError('a group\'s own kind is "muon", not '
+                             f"{kind!r}")
+        super().add_param_group(param_group)
+        if kind == "muon" and any(
+                p.dim() < 2 for p in self.param_groups[-1]["params"]):
+            self.param_groups.pop()
+            raise ValueError("muon is for parameters of two or more "
+                             "dimensions")
+
+    def _kind(self, group):
+        return group.get("kind", self.kind)
+
     # -- state buffers ----------------------------------------------------
     def master(self, p):
         """The float32 weight the update runs on: p itself (a float32
@@ -146,10 +196,10 @@ class MtaOptimizer(torch.optim.Optimizer):
             st["master_weight"] = p.detach().float().contiguous()
         return st["master_weight"]
 
-    def _state_buffers(self, p):
+    def _state_buffers(self, p, kind):
         st = self.state[p]
         mdt = torch.bfloat16 if self.packed else torch.float32
-        if self.kind in ("adamw", "adam"):
+        if kind in ("adamw", "adam"):
             if "exp_avg" not in st:
                 st["exp_avg"] = torch.zeros_like(p, dtype=mdt)
                 st["exp_avg_sq"] = torch.zeros_like(p, dtype=mdt)
@@ -160,7 +210,7 @@ class MtaOptimizer(torch.optim.Optimizer):
                 if st[name].dtype != mdt:
                     st[name] = st[name].to(mdt).contiguous()
             return st["exp_avg"], st["exp_avg_sq"]
-        if self.kind == "momentum":
+        if kind in ("momentum", "muon"):
             if "momentum_buffer" not in st:
                 st["momentum_buffer"] = torch.zeros_like(
                     p, dtype=torch.float32)
@@ -191,7 +241,7 @@ class MtaOptimizer(torch.optim.Optimizer):
         None."""
         groups, key = [], [tuple(no_decay) if no_decay else None]
         for p in params:
-            m, v = self._state_buffers(p)
+            m, v = self._state_buffers(p, self.kind)
             w = self.master(p)
             groups.append((w, p.grad, m, v))
             key.append((w.data_ptr(), p.grad.data_ptr(),
@@ -224,7 +274,7 @@ class MtaOptimizer(torch.optim.Optimizer):
     def _merge_sig(self):
         """The parameter sets the current hyperparameters allow: for each
         group, (index of the first group of its set, its weight decay is
-        0).  Groups with equal lr, betas, eps and momentum form one set when
+        0).  A group of kind "muon" is a set of its own.  Groups with equal lr, betas, eps and momentum form one set when
         at most one nonzero weight decay appears among them; otherwise each
         of them is a set of its own."""
         keys, nonzero = [], {}
@@ -232,11 +282,11 @@ class MtaOptimizer(torch.optim.Optimizer):
             key = (float(g["lr"]), tuple(float(b) for b in g["betas"]),
                    float(g["eps"]), float(g["momentum"]))
             keys.append(key)
-            if float(g["weight_decay"]) != 0.0:
+            if float(g["weight_decay"]) != 0.0 and self._kind(g) != "muon":
                 nonzero.setdefault(key, set()).add(float(g["weight_decay"]))
         first, out = {}, []
         for i, (g, key) in enumerate(zip(self.param_groups, keys)):
-            if len(nonzero.get(key, ())) > 1:
+            if self._kind(g) == "muon" or len(nonzero.get(key, ())) > 1:
                 head = i
             else:
                 head = first.setdefault(key, i)
@@ -312,6 +362,10 @@ class MtaOptimizer(torch.optim.Optimizer):
             wd = next((w for w in (float(self.param_groups[i]
                                          ["weight_decay"])
                                    for i in u["groups"]) if w != 0.0), 0.0)
+            if "muon" in u:
+                u["t"] += 1
+                self._muon_step(u, group, coef)
+                continue
             rule = dict(kind=self.kind, lr=group["lr"], beta1=b1, beta2=b2,
                         eps=group["eps"], weight_decay=wd,
                         momentum=group["momentum"],
@@ -324,6 +378,37 @@ class MtaOptimizer(torch.optim.Optimizer):
         if self.amp is not None:
             self.amp.update(*self._amp_rule)
         return loss
+
+    def _muon_step(self, u, group, coef):
+        """The group's matrices, in one call."""
+        ns = self._ns
+        muon.run(u["muon"], u["params"][0].device, u["type"], B.MTA_F32,
+                 u["copy_type"], ns["coefficients"], ns["eps"],
+                 float(group["momentum"]), ns["nesterov"],
+                 u["type"] == B.MTA_F32 if ns["precise"] is None
+                 else ns["precise"], lr=float(group["lr"]),
+                 weight_decay=float(group["weight_decay"]),
+                 coef=None if coef is None else coef.data_ptr(),
+                 amp=None if self.amp is None else self.amp.ptr)
+        if self.zero_grad_in_step:
+            torch._foreach_zero_([p.grad for p in u["params"]])
+
+    def _muon_table(self, params):
+        entries = []
+        for p in params:
+            rows, cols = p.shape[0], p[0].numel() if p.shape[0] else 0
+            scale = self._ns["scale"]
+            if scale == "spectral":
+                scale = math.sqrt(max(1.0, rows / max(1, cols)))
+            elif scale == "rms":
+                scale = 0.2 * math.sqrt(max(rows, cols))
+            entries.append((
+                p.grad.data_ptr(),
+                self._state_buffers(p, "muon")[0].data_ptr(), None,
+                self.master(p).data_ptr(),
+                None if p.dtype == torch.float32 else p.data_ptr(), rows,
+                cols, cols, cols, float(scale)))
+        return muon.table(entries)
 
     def _build_plan(self, groups, sig, msig):
         all_params = [p for ps in groups for p in ps]
@@ -341,8 +426,9 @@ class MtaOptimizer(torch.optim.Optimizer):
             self.last_norm = torch.zeros(1, device=dev)
             self.last_coef = torch.zeros(1, device=dev)
         plan["norm_lists"] = self._norm_lists(all_params)
-        for p in all_params:
-            self._state_buffers(p)
+        for g, ps in zip(self.param_groups, groups):
+            for p in ps:
+                self._state_buffers(p, self._kind(g))
         steps = []
         for k, ps in enumerate(groups):
             st = {int(self.state[p]["step"]) for p in ps}
@@ -360,6 +446,16 @@ class MtaOptimizer(torch.optim.Optimizer):
                 sets.setdefault((head, t), []).append(k)
         used = set()
         for (head, _), ks in sorted(sets.items(), key=lambda x: x[1][0]):
+            if self._kind(self.param_groups[head]) == "muon":
+                for dt in _GTYPE:   # one call per gradient dtype
+                    ps = [p for p in groups[head] if p.grad.dtype == dt]
+                    if ps:
+                        plan["updates"].append(dict(
+                            group=head, groups=(head,), params=ps,
+                            t=steps[head], muon=self._muon_table(ps),
+                            type=_GTYPE[dt], copy_type=B.MTA_F16 if
+                            dt == torch.float16 else B.MTA_BF16))
+                continue
             flagged = any(not msig[k][1] for k in ks) and \
                 any(msig[k][1] for k in ks)
             for dt in _GTYPE:   # one launch per gradient dtype in the set

@@ -212,9 +212,9 @@ def test_clip_coefficient_loss_scale_and_weights():
         w16 = torch.full((60, 100), 9.0, dtype=torch.bfloat16, device="cuda")
         dg = on_gpu(g)
         from mixed_precision_optimizer_mta_amd import muon
-        muon.run([(dg.data_ptr(), m.data_ptr(), None, w.data_ptr(),
-                   w16.data_ptr(), 60, 100, 100, 0, 0.5)], dg.device,
-                 B.MTA_F16, B.MTA_F32, B.MTA_BF16,
+        muon.run(muon.table([(dg.data_ptr(), m.data_ptr(), None, w.data_ptr(),
+                              w16.data_ptr(), 60, 100, 100, 0, 0.5)]),
+                 dg.device, B.MTA_F16, B.MTA_F32, B.MTA_BF16,
                  muon._coefficients(muon.COEFFICIENTS, 5), 1e-7, 0.95, True,
                  True, lr=0.02, weight_decay=0.1, coef=coef.data_ptr(),
                  amp=amp.ptr)
