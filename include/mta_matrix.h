@@ -64,12 +64,12 @@ typedef struct {
  * unspecified.  A matrix with a NaN or infinity comes out all NaN and leaves
  * the others alone; one of zeros comes out zero.
  *
- * X and A are kept as a float16 value and a second one for what it leaves (22
- * bits), B as one such value and its diagonal in float32; sums are float32.
- * With `precise`, and for a matrix of fewer than 16 rows or columns, all
- * products are those of 22 bits, three float16 products each.  Without,
- * products are of the first values alone, one product each, the diagonals
- * apart: off by 2e-4 to 1.1e-3 of the result's root mean square.
+ * A matrix of up to 64 rows or columns is computed in float64.  Otherwise X is
+ * kept as a float16 value and a second one for what it leaves (22 bits), A and B
+ * as such values and their diagonals in float32; sums are float32.  With
+ * `precise` all products are those of 22 bits, three float16 products each.
+ * Without, products are of the first values alone, one product each, the
+ * diagonals apart: off by 2e-4 to 1.1e-3 of the result's root mean square.
  * The coefficients have to keep every singular value in [0, 1] below 7 from
  * step to step (MTA_EINVAL). */
 typedef struct {

@@ -21,7 +21,8 @@ LIB = os.path.join(HERE, "libmta.so")
 SOURCES = [os.path.join(CSRC, name) for name in
            ("mta_kernels.hip", "mta_host.cpp", "ckpt_kernels.hip",
             "wgrad_kernels.hip", "policy_kernels.hip", "ops_host.cpp",
-            "ortho_kernels.hip", "linear_kernels.hip", "matrix_host.cpp")]
+            "ortho_kernels.hip", "ortho_small.hip", "linear_kernels.hip",
+            "matrix_host.cpp")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -350,65 +350,97 @@ __device__ __forceinline__ void tile_product(
   __asm__ volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
 }
 
-// The sums through LDS, 32 rows of a wave's columns at a time, to
-//   emit(m, n, v)    eight columns n .. n + 7 of a row, where `direct`
-//   turned(n, m, v)  eight rows m .. m + 7 of a column, where `mirror`: with
-//                    Fold what emit has made of them
-// with m and n counted from the tile's corner.
-template <class C, bool Fold, class Emit, class Turned>
+// The sums through LDS, 64 rows and 64 columns of a wave at a time, to
+//   emit(m, n, v, x)    eight columns n .. n + 7 of a row, where `direct`
+//   turned(n, m, v, x)  eight rows m .. m + 7 of a column, where `mirror`: with
+//                       Fold what emit has made of them
+// with m and n counted from the tile's corner and x what look(m, n) or
+// ahead(n, m) gave some turns earlier (they are also asked for what lies behind
+// the tile): global memory is on its way meanwhile.
+// Loops are rolled: a workgroup runs this code once, and straight through it
+// was 20 to 60 KB to fetch.
+template <class C, bool Fold, class Look, class Emit, class Ahead, class Turned>
 __device__ __forceinline__ void tile_out(
     MTA_LDS uint8_t *lds, const f32x16 (&acc)[C::kRM][C::kRN], bool direct,
-    bool mirror, Emit &&emit, Turned &&turned) {
-  // a pitch of 4 more floats: 16 lanes of a row each lie in distinct banks
-  constexpr int kPitch = C::kTN + 4;
-  constexpr int kWave = 32 * kPitch * 4;
-  // (the rows' loop, over the sums' registers, has to be unrolled whole)
-  constexpr int kTurns = Fold ? 1 : 4;
-  static_assert(kWave * C::kWR * C::kWC <= C::kLds, "the staging fits");
+    bool mirror, Look &&look, Emit &&emit, Ahead &&ahead, Turned &&turned) {
+  constexpr int kBlocks = C::kTM / 64;
+  static_assert(C::kTM % 64 == 0 && C::kTN == 64, "wholes of 64 x 64");
+  static_assert(C::kWR * C::kWC * 16384 <= C::kLds, "the staging fits");
   const int lane = threadIdx.x % 64;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int m_at = wave / C::kWC * C::kTM, n_at = wave % C::kWC * C::kTN;
-  auto *mine = (MTA_LDS float *)(lds + wave * kWave);
+  // rows of 16 chunks of four, turned by the row so that no two lanes of a
+  // write, and none of a read, meet in a bank
+  auto *mine = (MTA_LDS float *)(lds + wave * 16384);
+  const auto chunk = [&](int m, int c) {
+    return (MTA_LDS f32x4 *)(mine + m * 64 + ((c ^ (m & 15)) * 4));
+  };
+  // so many turns' memory is on its way (sums that wait for the second 64 rows
+  // leave fewer registers)
+  constexpr int kAhead =
+      C::kTM > 64 && sizeof(decltype(look(0, 0))) > 48 ? 2 : 4;
+  decltype(look(0, 0)) seen[kAhead];
+  if (direct) {
+#pragma unroll
+    for (int p = 0; p < kAhead; ++p)
+      seen[p] = look(m_at + p * 8 + lane / 8, n_at + lane % 8 * 8);
+  }
   __syncthreads();
+#pragma unroll 1
+  for (int b = 0; b < kBlocks; ++b) {
+    const int m_b = m_at + b * 64;
 #pragma unroll
-  for (int i = 0; i < C::kRM; ++i) {
+    for (int i = 0; i < C::kRM; ++i) {
+      if (i / 2 != b) continue;
 #pragma unroll
-    for (int j = 0; j < C::kRN; ++j)
+      for (int j = 0; j < C::kRN; ++j)
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *(MTA_LDS f32x4 *)(mine + lane % 32 * kPitch + j * 32 + q * 8 +
-                           lane / 32 * 4) =
-            f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1],
-                  acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+        for (int q = 0; q < 4; ++q)
+          *chunk(i % 2 * 32 + lane % 32, j * 8 + q * 2 + lane / 32) =
+              f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1],
+                    acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
+    }
     __builtin_amdgcn_wave_barrier();
     if (direct) {
-      constexpr int kAcrossRow = C::kTN / 8, kRows = 64 / kAcrossRow;
-#pragma unroll kTurns
-      for (int p = 0; p < 32 / kRows; ++p) {
-        const int m = p * kRows + lane / kAcrossRow;
-        const int n = lane % kAcrossRow * 8;
-        const f32x4 x = *(MTA_LDS f32x4 *)(mine + m * kPitch + n);
-        const f32x4 y = *(MTA_LDS f32x4 *)(mine + m * kPitch + n + 4);
-        float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-        emit(m_at + i * 32 + m, n_at + n, v);
-        if constexpr (Fold) {
-          *(MTA_LDS f32x4 *)(mine + m * kPitch + n) =
-              f32x4{v[0], v[1], v[2], v[3]};
-          *(MTA_LDS f32x4 *)(mine + m * kPitch + n + 4) =
-              f32x4{v[4], v[5], v[6], v[7]};
+      const int m = lane / 8, n = lane % 8 * 8;
+#pragma unroll 1
+      for (int h = 0; h < 8; h += kAhead) {
+#pragma unroll
+        for (int p = 0; p < kAhead; ++p) {
+          const int row = (h + p) * 8 + m;
+          const f32x4 f = *chunk(row, n / 4);
+          const f32x4 g = *chunk(row, n / 4 + 1);
+          float v[8] = {f[0], f[1], f[2], f[3], g[0], g[1], g[2], g[3]};
+          emit(m_b + row, n_at + n, v, seen[p]);
+          if constexpr (Fold) {
+            *chunk(row, n / 4) = f32x4{v[0], v[1], v[2], v[3]};
+            *chunk(row, n / 4 + 1) = f32x4{v[4], v[5], v[6], v[7]};
+          }
+          // (past the end: the next 64 rows)
+          seen[p] = look(m_b + row + kAhead * 8, n_at + n);
         }
       }
       __builtin_amdgcn_wave_barrier();
     }
     if (mirror) {
-#pragma unroll kTurns
-      for (int c = 0; c < C::kTN / 16; ++c) {
-        // 16 columns, four runs of eight rows each
-        const int n = c * 16 + lane / 4, m = lane % 4 * 8;
-        float v[8];
+      // 8 columns, eight runs of eight rows each
+      const int n = lane / 8, m = lane % 8 * 8;
+      decltype(ahead(0, 0)) seen[kAhead];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = mine[(m + e) * kPitch + n];
-        turned(n_at + n, m_at + i * 32 + m, v);
+      for (int p = 0; p < kAhead; ++p)
+        seen[p] = ahead(n_at + p * 8 + n, m_b + m);
+#pragma unroll 1
+      for (int h = 0; h < 8; h += kAhead) {
+#pragma unroll
+        for (int p = 0; p < kAhead; ++p) {
+          const int at = (h + p) * 8 + n;
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            v[e] = ((MTA_LDS float *)chunk(m + e, at / 4))[at % 4];
+          turned(n_at + at, m_b + m, v, seen[p]);
+          seen[p] = ahead(n_at + at + kAhead * 8, m_b + m);
+        }
       }
     }
     __builtin_amdgcn_wave_barrier();
@@ -432,9 +464,12 @@ __device__ __forceinline__ void banded(uint32_t t, uint32_t rows, uint32_t cols,
   col = u / height;
 }
 
-// The two tiles: the large one, whose workgroup fills a CU, and the small one,
-// of which a CU holds two.
+// The tiles: the large one, whose workgroup fills a CU, the small one, of which
+// a CU holds two, and the small one for launches that bring a CU no second one:
+// four buffers, since there is nobody else to hide a load's way (768 x 768 over
+// 768: 0.8 us a step of 64 with two).
 using Tile256 = Tile<256, 256, 2, 4, 32, 4, 2>;
 using Tile128 = Tile<128, 128, 2, 2, 64, 2, 2>;
+using TileDeep = Tile<128, 128, 2, 2, 64, 4, 1>;
 
 }  // namespace mta

@@ -310,8 +310,8 @@ __global__ __launch_bounds__(C::kThreads)
   const float most = l.scalars[1];
   const int64_t wide = (l.count + 63) / 64 * 64;
   tile_out<C, false>(
-      lds, acc, true, false,
-      [&](int m, int n, float (&v)[8]) {
+      lds, acc, true, false, [](int, int) { return 0; },
+      [&](int m, int n, float (&v)[8], int) {
         const int64_t row = m0 + m, col = n0 + n;
         if (row >= l.deep_rows || col >= wide) return;
         mta_linear_row r{0.0f, 0.0f, 0.0f, 0.0f};
@@ -331,7 +331,7 @@ __global__ __launch_bounds__(C::kThreads)
         }
         put_planes<D>(l.z + row * l.pitch_z + col, l.z_plane, v);
       },
-      [](int, int, float (&)[8]) {});
+      [](int, int) { return 0; }, [](int, int, float (&)[8], int) {});
 }
 
 // The factor that all of dz shares.
@@ -373,8 +373,8 @@ __device__ __forceinline__ void gradient_out(
     bool accumulate) {
   const float factor = shared_factor<D>(l);
   tile_out<C, false>(
-      lds, acc, true, false,
-      [&](int m, int n, float (&v)[8]) {
+      lds, acc, true, false, [](int, int) { return 0; },
+      [&](int m, int n, float (&v)[8], int) {
         const int64_t row = m0 + m, col = n0 + n;
         if (row >= rows || col >= l.a.width) return;
         if (hold) {  // (rows of whole runs)
@@ -395,7 +395,7 @@ __device__ __forceinline__ void gradient_out(
                                       accumulate, factor, v);
         });
       },
-      [](int, int, float (&)[8]) {});
+      [](int, int) { return 0; }, [](int, int, float (&)[8], int) {});
 }
 
 // dh (+)= dz w over a part of a piece.
@@ -505,9 +505,10 @@ uint32_t up(int64_t n, int64_t d) {
 
 // f(tile, type) for the run-time ones.
 template <typename F>
-void with_tile(int tile, int type, F &&f) {
+void with_tile(const LinearCut &c, int type, F &&f) {
   with_type(type, [&](auto t) {
-    if (tile == 256) f(Tile256{}, t);
+    if (c.tile == 256) f(Tile256{}, t);
+    else if (c.deep) f(TileDeep{}, t);
     else f(Tile128{}, t);
   });
 }
@@ -542,7 +543,7 @@ hipError_t launch_linear_pack_w(const LinearArgs &l, uint16_t *to,
 
 hipError_t launch_linear_logits(const LinearArgs &l, const LinearCut &c,
                                 hipStream_t s) {
-  with_tile(c.tile, l.a.type, [&](auto tile, auto t) {
+  with_tile(c, l.a.type, [&](auto tile, auto t) {
     using C = decltype(tile);
     k_linear_logits<C, decltype(t)::value>
         <<<up(l.a.rows, C::kBM) * static_cast<uint32_t>(l.tiles), C::kThreads,
@@ -562,7 +563,7 @@ hipError_t launch_linear_rows(const LinearArgs &l, hipStream_t s) {
 
 hipError_t launch_linear_grad(const LinearArgs &l, const LinearCut &c,
                               hipStream_t s) {
-  with_tile(c.tile, l.a.type, [&](auto tile, auto t) {
+  with_tile(c, l.a.type, [&](auto tile, auto t) {
     using C = decltype(tile);
     k_linear_grad<C, decltype(t)::value>
         <<<up(l.a.rows, C::kBM) * up(l.count, C::kBN), C::kThreads, 0, s>>>(l);
@@ -572,7 +573,7 @@ hipError_t launch_linear_grad(const LinearArgs &l, const LinearCut &c,
 
 hipError_t launch_linear_dh(const LinearArgs &l, const LinearCut &c, bool hold,
                             hipStream_t s) {
-  with_tile(c.tile, l.a.type, [&](auto tile, auto t) {
+  with_tile(c, l.a.type, [&](auto tile, auto t) {
     using C = decltype(tile);
     k_linear_dh<C, decltype(t)::value>
         <<<up(l.a.rows, C::kBM) * up(l.a.width, C::kBN) * c.parts, C::kThreads,
@@ -583,7 +584,7 @@ hipError_t launch_linear_dh(const LinearArgs &l, const LinearCut &c, bool hold,
 
 hipError_t launch_linear_dw(const LinearArgs &l, const LinearCut &c, bool hold,
                             hipStream_t s) {
-  with_tile(c.tile, l.a.type, [&](auto tile, auto t) {
+  with_tile(c, l.a.type, [&](auto tile, auto t) {
     using C = decltype(tile);
     k_linear_dw<C, decltype(t)::value>
         <<<up(l.count, C::kBM) * up(l.a.width, C::kBN) * c.parts, C::kThreads,

@@ -39,7 +39,6 @@ struct OrthoItem {
   uint8_t *ws;
   int64_t ldg, ldout;
   uint32_t rows, cols;
-  int planes;    // of a product's operands
   float scale;   // of out
   float update;  // -lr scale, of w
 };
@@ -60,19 +59,43 @@ struct OrthoCall {
   float decay;  // of w
   float a, b, c;  // of the step
   int type, out_type, copy_type, nesterov;
+  int planes;   // of a product's operands: 2 with `precise`
+  int cuts;     // parts of k that A is summed in
   int whole;    // the diagonal times all digits of X, not those of the first
                 // plane alone
   int which;    // the X that is read; the other one is written
 };
-static_assert(sizeof(OrthoList) + sizeof(OrthoCall) <= 4000,
+static_assert(sizeof(OrthoList) + sizeof(OrthoCall) +
+                      sizeof(double) * 3 * MTA_ORTHO_STEPS + 8 <=
+                  4096,
               "kernel argument space");
 
-// Planes of a product's operands: two, that is products of 22 bits, with
-// `precise` and for matrices of few rows or columns, whose errors do not
-// average out (3 x 3 with one plane: 2.3e-3 of the result, 16 x 16 6e-4).
-__host__ __device__ inline int ortho_planes(int64_t rows, int64_t cols,
-                                            int precise) {
-  return precise || rows < 16 || cols < 16 ? 2 : 1;
+// Up to so many rows or columns a matrix takes the way of the small: its Gram
+// matrix and the polynomial of it in float64.
+constexpr int kOrthoSmall = 64;
+__host__ __device__ inline bool ortho_is_small(int64_t rows, int64_t cols) {
+  return rows <= kOrthoSmall || cols <= kOrthoSmall;
+}
+
+// A small matrix's part of the workspace: partial Gram matrices of `side` rows,
+// whole blocks of 16, and the polynomial's factor.
+struct OrthoSmallSpace {
+  int64_t small, large;
+  int side, parts;
+  int64_t bytes;
+};
+__host__ __device__ inline OrthoSmallSpace ortho_small_space(int64_t rows,
+                                                             int64_t cols) {
+  OrthoSmallSpace s;
+  s.small = rows < cols ? rows : cols;
+  s.large = rows < cols ? cols : rows;
+  s.side = static_cast<int>((s.small + 15) / 16 * 16);
+  // 64 columns at a time; few enough parts for one workgroup to read
+  const int64_t tiles = (s.large + 63) / 64;
+  const int64_t most = s.side > 32 ? 32 : 64;
+  s.parts = static_cast<int>(tiles < most ? tiles : most);
+  s.bytes = (s.parts + 1) * static_cast<int64_t>(s.side) * s.side * 8;
+  return s;
 }
 
 // A matrix's part of the workspace: two X of `planes` planes each, A and B,
@@ -82,9 +105,10 @@ struct OrthoSpace {
   int64_t plane_x, plane_a;          // elements
   // offsets in bytes, and from the first of two to the second
   int64_t x, next_x, a, next_a, diag, next_diag, part, bytes;
+  int64_t cut;  // partial sums of A: [cuts][small][pitch_a] floats
 };
 __host__ __device__ inline OrthoSpace ortho_space(int64_t rows, int64_t cols,
-                                                  int planes) {
+                                                  int planes, int cuts) {
   OrthoSpace s;
   s.small = rows < cols ? rows : cols;
   s.large = rows < cols ? cols : rows;
@@ -98,13 +122,17 @@ __host__ __device__ inline OrthoSpace ortho_space(int64_t rows, int64_t cols,
   s.a = s.x + 2 * s.next_x;
   s.next_a = round(s.plane_a * planes * 2);
   s.diag = s.a + 2 * s.next_a;
-  s.next_diag = round(s.small * 4);
+  s.next_diag = round(s.pitch_a * 4);  // zeros behind the last
   s.part = s.diag + 2 * s.next_diag;
-  s.bytes = s.part + kOrthoParts * 8;
+  s.cut = s.part + kOrthoParts * 8;
+  s.bytes = s.cut + (cuts > 1 ? round(cuts * s.plane_a * 4) : 0);
   return s;
 }
 
 // The tiles of a product's workgroups, and those of the kernels before it.
+// After a Gram product in parts: 64 x 64 of A, and what mirrors it.
+hipError_t launch_ortho_join(const OrthoList &l, const OrthoCall &c,
+                             hipStream_t s);
 enum OrthoStep { kOrthoGram, kOrthoSquare, kOrthoNext, kOrthoLast };
 constexpr int kOrthoLoadTile = 64;
 // Workgroups that sum a matrix's squares: 64 elements a lane, as long as they
@@ -117,8 +145,20 @@ hipError_t launch_ortho_norm(const OrthoList &l, const OrthoCall &c,
                              hipStream_t s);
 hipError_t launch_ortho_load(const OrthoList &l, const OrthoCall &c,
                              hipStream_t s);
-// tile: 256 or 128
-hipError_t launch_ortho_product(int step, int tile, const OrthoList &l,
+hipError_t launch_ortho_small_gram(const OrthoList &l, const OrthoCall &c,
+                                   hipStream_t s);
+// coefficients: a, b, c of each step
+struct OrthoCoefficients {
+  double v[MTA_ORTHO_STEPS][3];
+  int steps;
+};
+hipError_t launch_ortho_small_factor(const OrthoList &l, const OrthoCall &c,
+                                     const OrthoCoefficients &k, hipStream_t s);
+hipError_t launch_ortho_small_apply(const OrthoList &l, const OrthoCall &c,
+                                    hipStream_t s);
+// tile: 256 or 128; deep: no CU gets a second workgroup
+hipError_t launch_ortho_product(int step, int tile, bool deep,
+                                const OrthoList &l,
                                 const OrthoCall &c, hipStream_t s);
 
 // ---- cross entropy of a linear output layer -----------------------------
@@ -129,6 +169,7 @@ static_assert(sizeof(mta_linear_row) == 16, "saved row layout");
 // sums a second kernel joins.
 struct LinearCut {
   int tile;
+  bool deep;  // no CU gets a second workgroup of the small tile
   int parts;
   int64_t part_k;  // multiples of 64
 };

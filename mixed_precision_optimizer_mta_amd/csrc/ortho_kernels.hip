@@ -22,7 +22,7 @@
 // 6.8e-4 where eight directions stand out); in the last two the whole X.  With
 // `precise` every product is of both values: 4e-7.
 #include "gemm_device.h"
-#include "matrix_internal.h"
+#include "ortho_device.h"
 
 namespace mta {
 namespace {
@@ -31,60 +31,21 @@ namespace {
 // values of 7 in X, of 49 in A and a multiple of that in B.
 constexpr float kScaleX = 8192.0f, kScaleA = 1024.0f, kScaleB = 512.0f;
 
-__device__ __forceinline__ float unscale_of(const OrthoCall &c) {
-  return c.amp ? static_cast<float>(1.0 / static_cast<double>(c.amp->scale))
-               : 1.0f;
-}
-
-__device__ __forceinline__ int item_of(const OrthoList &l, uint32_t block) {
-  int k = 0;
-  while (k + 1 < static_cast<int>(l.count) && block >= l.first[k + 1]) ++k;
-  return k;
-}
-
-// Two float16 values of x: its rounding and the rounding of what is left.
-__device__ __forceinline__ void halves(float x, float &hi, float &lo) {
-  hi = static_cast<float>(static_cast<_Float16>(x));
-  lo = x - hi;
-  // an infinity would leave a NaN, which the first value says already
-  lo = lo == lo ? lo : 0.0f;
-}
-
-__device__ __forceinline__ void store_planes(uint16_t *hi_at, uint16_t *lo_at,
+// Eight values as float16, and with Two what their roundings leave as a second
+// eight (an infinity leaves a NaN: its matrix is lost anyway).
+template <bool Two>
+__device__ __forceinline__ void store_planes(uint16_t *hi_at, int64_t plane,
                                              const float (&x)[8]) {
-  float hi[8], lo[8];
+  u32x4 hi, lo;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) halves(x[e], hi[e], lo[e]);
-  store<MTA_F16, 8, false>(hi_at, 0, hi);
-  if (lo_at) store<MTA_F16, 8, false>(lo_at, 0, lo);
-}
-
-// Sum of a value of every lane of a workgroup of 256, in all of them.
-__device__ __forceinline__ double sum256(double x, double *four) {
-#pragma unroll
-  for (int d = 32; d > 0; d /= 2) x += __shfl_xor(x, d);
-  __syncthreads();
-  if (threadIdx.x % 64 == 0) four[threadIdx.x / 64] = x;
-  __syncthreads();
-  return (four[0] + four[1]) + (four[2] + four[3]);
-}
-
-// g' and, with a momentum, its new value and u.
-struct Look {
-  float s, c, mu;
-  int nesterov;
-  __device__ __forceinline__ float gradient(float g) const {
-    return (g * s) * c;
+  for (int k = 0; k < 4; ++k) {
+    hi[k] = narrow2<MTA_F16>(x[2 * k], x[2 * k + 1]);
+    if constexpr (Two)
+      lo[k] = narrow2<MTA_F16>(x[2 * k] - widen<MTA_F16>(hi[k] & 0xFFFFu),
+                               x[2 * k + 1] - widen<MTA_F16>(hi[k] >> 16));
   }
-  __device__ __forceinline__ float next(float m, float g) const {
-    return m * mu + g;
-  }
-  __device__ __forceinline__ float ahead(float m, float g) const {
-    return nesterov ? g + mu * m : m;
-  }
-};
-__device__ __forceinline__ Look look_of(const OrthoCall &c) {
-  return Look{unscale_of(c), c.d_coef ? *c.d_coef : 1.0f, c.mu, c.nesterov};
+  *(MTA_GLOBAL u32x4 *)hi_at = hi;
+  if constexpr (Two) *(MTA_GLOBAL u32x4 *)(hi_at + plane) = lo;
 }
 
 // The momentum takes the gradient in, and the squares of u are summed: partial
@@ -141,7 +102,7 @@ __global__ __launch_bounds__(256) void k_ortho_norm(const OrthoList l,
   }
   __shared__ double four[4];
   sum = sum256(sum, four);
-  const OrthoSpace sp = ortho_space(it.rows, it.cols, it.planes);
+  const OrthoSpace sp = ortho_space(it.rows, it.cols, c.planes, c.cuts);
   if (threadIdx.x == 0)
     reinterpret_cast<double *>(it.ws + sp.part)[part] = sum;
 }
@@ -154,7 +115,7 @@ __global__ __launch_bounds__(256) void k_ortho_load(const OrthoList l,
   constexpr int kT = kOrthoLoadTile;
   const int k = item_of(l, blockIdx.x);
   const OrthoItem &it = l.item[k];
-  const OrthoSpace sp = ortho_space(it.rows, it.cols, it.planes);
+  const OrthoSpace sp = ortho_space(it.rows, it.cols, c.planes, c.cuts);
   __shared__ double four[4];
   __shared__ float tile[kT][kT + 1];
   const int64_t parts = ortho_parts(it.rows, it.cols);
@@ -167,6 +128,9 @@ __global__ __launch_bounds__(256) void k_ortho_load(const OrthoList l,
   const Look look = look_of(c);
   const bool skip = c.amp && c.amp->found_inf != 0.0f;
   const bool tall = it.rows > it.cols;
+  if (blockIdx.x == l.first[k])
+    for (int64_t i = sp.small + threadIdx.x; i < sp.pitch_a; i += 256)
+      reinterpret_cast<float *>(it.ws + sp.diag)[i] = 0.0f;
   const uint32_t t = blockIdx.x - l.first[k];
   const uint32_t wide = static_cast<uint32_t>(sp.pitch_x) / kT;
   const int64_t m0 = int64_t{t / wide} * kT, n0 = int64_t{t % wide} * kT;
@@ -208,7 +172,7 @@ __global__ __launch_bounds__(256) void k_ortho_load(const OrthoList l,
     } else if (r < sp.small && col < sp.pitch_x) {
       auto *hi = reinterpret_cast<uint16_t *>(it.ws + sp.x) +
                  r * sp.pitch_x + col;
-      store_planes(hi, hi + sp.plane_x, v);
+      store_planes<true>(hi, sp.plane_x, v);
     }
   }
   if (!tall) return;
@@ -223,62 +187,84 @@ __global__ __launch_bounds__(256) void k_ortho_load(const OrthoList l,
     for (int e = 0; e < 8; ++e) v[e] = tile[y][x + e];
     auto *hi =
         reinterpret_cast<uint16_t *>(it.ws + sp.x) + m * sp.pitch_x + n;
-    store_planes(hi, hi + sp.plane_x, v);
+    store_planes<true>(hi, sp.plane_x, v);
   }
 }
 
-// Eight results of a row: out, and the weights' step.
-__device__ __forceinline__ void put_result(const OrthoItem &it,
-                                           const OrthoCall &c, int64_t row,
-                                           int64_t col, const float (&x)[8],
-                                           bool skip) {
-  if (row >= it.rows || col >= it.cols) return;
-  const int n = static_cast<int>(min(int64_t{8}, it.cols - col));
-  float y[8];
-  if (it.out) {
+// The diagonal's value among eight of a row, if it is there, goes to its own
+// array and leaves a zero; so do the values behind the last column.
+__device__ __forceinline__ void take_diagonal(float *diag, int64_t row,
+                                              int64_t col, int64_t small,
+                                              float (&v)[8]) {
+  const int64_t own = row - col, left = small - col;
+  float d = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = x[e] * it.scale;
-    with_type(c.out_type, [&](auto type) {
-      constexpr int T = decltype(type)::value;
-      if (n == 8) {
-        store8<T, false>(it.out, row * it.ldout + col, y);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (e < n) store_elem<T>(it.out, row * it.ldout + col + e, y[e]);
-      }
-    });
+  for (int e = 0; e < 8; ++e) {
+    d = e == own ? v[e] : d;
+    v[e] = e == own || e >= left ? 0.0f : v[e];
   }
-  if (it.w && !skip) {
-    const int64_t at = row * it.cols + col;
-    const Raw8<MTA_F32> w = n == 8 ? load8<MTA_F32, false>(it.w, at)
-                                   : load8_part<MTA_F32>(it.w, at, n, 0);
+  if (own >= 0 && own < 8) diag[row] = d;
+}
+
+// A's parts joined in order: a workgroup takes 64 x 64 on or right of the
+// diagonal and writes its mirror image too.
+__global__ __launch_bounds__(256) void k_ortho_join(const OrthoList l,
+                                                    const OrthoCall c) {
+  __shared__ float tile[64][65];
+  const int k = item_of(l, blockIdx.x);
+  const OrthoItem &it = l.item[k];
+  const OrthoSpace sp = ortho_space(it.rows, it.cols, c.planes, c.cuts);
+  const uint32_t side = static_cast<uint32_t>(sp.small + 63) / 64;
+  uint32_t tn = blockIdx.x - l.first[k], tm = 0;
+  while (tn >= side - tm) tn -= side - tm++;
+  tn += tm;
+  auto *to = reinterpret_cast<uint16_t *>(it.ws + sp.a);
+  auto *diag = reinterpret_cast<float *>(it.ws + sp.diag);
+  const auto *from = reinterpret_cast<const float *>(it.ws + sp.cut);
+  const int y = threadIdx.x / 8, x = threadIdx.x % 8 * 8;
+  const auto put = [&](int64_t row, int64_t col, float (&v)[8]) {
+    if (tm == tn || tn + 1 == side) take_diagonal(diag, row, col, sp.small, v);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = w[e] * c.decay + it.update * x[e];
-    if (n == 8) {
-      store8<MTA_F32, false>(it.w, at, y);
+    for (int e = 0; e < 8; ++e) v[e] *= kScaleA;
+    auto *at = to + row * sp.pitch_a + col;
+    if (c.planes > 1) store_planes<true>(at, sp.plane_a, v);
+    else store_planes<false>(at, 0, v);
+  };
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    const int64_t row = tm * 64 + p * 32 + y, col = tn * 64 + x;
+    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (row < sp.small) {
+#pragma unroll 4
+      for (int q = 0; q < c.cuts; ++q) {
+        const Raw8<MTA_F32> u = load8<MTA_F32, false>(
+            from, q * sp.plane_a + row * sp.pitch_a + col);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] += u[e];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) tile[x + e][p * 32 + y] = v[e];
+      put(row, col, v);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (e < n) it.w[at + e] = y[e];
+      for (int e = 0; e < 8; ++e) tile[x + e][p * 32 + y] = 0.0f;
     }
-    if (it.w16) {
-      with_type(c.copy_type, [&](auto type) {
-        constexpr int T = decltype(type)::value;
-        if (n == 8) {
-          store8<T, false>(it.w16, at, y);
-        } else {
+  }
+  if (tm == tn) return;
+  __syncthreads();
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (e < n) store_elem<T>(it.w16, at + e, y[e]);
-        }
-      });
-    }
+  for (int p = 0; p < 2; ++p) {
+    const int64_t row = tn * 64 + p * 32 + y, col = tm * 64 + x;
+    if (row >= sp.small) continue;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = tile[p * 32 + y][x + e];
+    put(row, col, v);
   }
 }
 
 // One tile of a step's product.
-template <class C, int Step>
+template <class C, int Step, int Planes>
 __global__ __launch_bounds__(C::kThreads)
     __attribute__((amdgpu_waves_per_eu(C::kPerSimd, C::kPerSimd))) void
     k_ortho_product(const OrthoList l, const OrthoCall c) {
@@ -287,14 +273,16 @@ __global__ __launch_bounds__(C::kThreads)
   const uint32_t block = beside(blockIdx.x, gridDim.x);
   const int k = item_of(l, block);
   const OrthoItem &it = l.item[k];
-  const OrthoSpace sp = ortho_space(it.rows, it.cols, it.planes);
+  const OrthoSpace sp = ortho_space(it.rows, it.cols, Planes, c.cuts);
   const uint32_t t = block - l.first[k];
   constexpr bool kSym = Step == kOrthoGram || Step == kOrthoSquare;
+  constexpr bool kTwo = Planes > 1;
   const uint32_t side = static_cast<uint32_t>(sp.small + C::kBM - 1) / C::kBM;
+  const uint32_t part = Step == kOrthoGram ? t % c.cuts : 0;
   uint32_t tm, tn;
   if constexpr (kSym) {
     // tiles on and right of the diagonal, row by row
-    uint32_t left = t;
+    uint32_t left = Step == kOrthoGram ? t / c.cuts : t;
     tm = 0;
     while (left >= side - tm) left -= side - tm++;
     tn = tm + left;
@@ -303,119 +291,195 @@ __global__ __launch_bounds__(C::kThreads)
            tn);
   }
   const int64_t m0 = int64_t{tm} * C::kBM, n0 = int64_t{tn} * C::kBN;
-  auto *x_old = reinterpret_cast<uint16_t *>(it.ws + sp.x + c.which * sp.next_x);
-  auto *x_new = reinterpret_cast<uint16_t *>(it.ws + sp.x + (1 - c.which) * sp.next_x);
+  auto *x_old =
+      reinterpret_cast<uint16_t *>(it.ws + sp.x + c.which * sp.next_x);
   auto *pa = reinterpret_cast<uint16_t *>(it.ws + sp.a);
   auto *pb = reinterpret_cast<uint16_t *>(it.ws + sp.a + sp.next_a);
   auto *da = reinterpret_cast<float *>(it.ws + sp.diag);
   auto *db = reinterpret_cast<float *>(it.ws + sp.diag + sp.next_diag);
-  const Operand x{x_old, sp.plane_x, sp.pitch_x, sp.small, sp.small};
-  const Operand a{pa, sp.plane_a, sp.pitch_a, sp.small, sp.small};
-  const Operand b{pb, sp.plane_a, sp.pitch_a, sp.small, sp.small};
-  const Pairs pairs = pairs_of(it.planes);
+  const Pairs pairs = pairs_of(Planes);
   const int64_t deep_x = (sp.large + 63) / 64 * 64;
   const int64_t deep_a = (sp.small + 63) / 64 * 64;
+  // rows that are there, from the tile's first
+  const int rows = static_cast<int>(min(sp.small - m0, int64_t{C::kBM}));
   f32x16 acc[C::kRM][C::kRN];
 
   if constexpr (kSym) {
-    if constexpr (Step == kOrthoGram)
-      tile_product<C, true, kAlong, kAlong>(x, x, pairs, m0, n0, 0, deep_x, lds,
-                                            acc);
-    else
+    if constexpr (Step == kOrthoGram) {
+      const Operand x{x_old, sp.plane_x, sp.pitch_x, sp.small, sp.small};
+      const int64_t each = (deep_x / 64 + c.cuts - 1) / c.cuts * 64;
+      const int64_t k0 = min(deep_x, part * each);
+      tile_product<C, true, kAlong, kAlong>(x, x, pairs, m0, n0, k0,
+                                            min(deep_x, k0 + each), lds, acc);
+    } else {
+      const Operand a{pa, sp.plane_a, sp.pitch_a, sp.small, sp.small};
       tile_product<C, true, kAlong, kAlong>(a, a, pairs, m0, n0, 0, deep_a, lds,
                                             acc);
+    }
+    float *cut = Step == kOrthoGram && c.cuts > 1
+                     ? reinterpret_cast<float *>(it.ws + sp.cut) +
+                           part * sp.plane_a + m0 * sp.pitch_a + n0
+                     : nullptr;
+    // from the tile's corner, and from its mirror image's, in 32 bits a lane
+    const uint32_t pitch = static_cast<uint32_t>(sp.pitch_a);
+    const int cols = static_cast<int>(min(sp.pitch_a - n0, int64_t{C::kBN}));
     uint16_t *to = Step == kOrthoGram ? pa : pb;
     float *diag = Step == kOrthoGram ? da : db;
-    const bool two = it.planes > 1;
-    const auto put = [&](int64_t row, int64_t col, float (&v)[8]) {
-      if (row >= sp.small || col >= sp.pitch_a) return;
-      const int64_t at = row * sp.pitch_a + col;
-      constexpr float kTo = Step == kOrthoGram ? kScaleA : kScaleB;
-      if constexpr (Step == kOrthoGram) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= 1.0f / (kScaleX * kScaleX);
-      } else {
-        // with A = D + O, D its diagonal: A A = O O + D O + O D + D D
-        const Raw8<MTA_F16> hi = load8<MTA_F16, false>(pa, at);
-        Raw8<MTA_F16> lo = fill8<MTA_F16>(0);
-        if (two) lo = load8<MTA_F16, false>(pa + sp.plane_a, at);
-        const float dr = da[row];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float o = (hi[e] + lo[e]) * (1.0f / kScaleA);
-          const float dc = col + e < sp.small ? da[col + e] : 0.0f;
-          const float oo = v[e] * (1.0f / (kScaleA * kScaleA));
-          v[e] = row == col + e ? c.b * dr + c.c * (oo + dr * dr)
-                                : c.b * o + c.c * (oo + (dr + dc) * o);
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (row == col + e) diag[row] = v[e];
-        v[e] = row == col + e || col + e >= sp.small ? 0.0f : v[e] * kTo;
-      }
-      store_planes(to + at, two ? to + at + sp.plane_a : nullptr, v);
+    uint16_t *here = to + m0 * sp.pitch_a + n0;
+    uint16_t *there = to + n0 * sp.pitch_a + m0;
+    const uint16_t *seen = pa + m0 * sp.pitch_a + n0;
+    // the tile holds a part of the diagonal, or a last column
+    const bool edge = tm == tn || tn + 1 == side;
+    struct Seen {
+      Raw8<MTA_F16> hi, lo;
+      float row;
+      Raw8<MTA_F32> col;
     };
-    tile_out<C, false>(
-        lds, acc, true, tm != tn,
-        [&](int m, int n, float (&v)[8]) { put(m0 + m, n0 + n, v); },
-        [&](int n, int m, float (&v)[8]) { put(n0 + n, m0 + m, v); });
+    // B, in units of kScaleB, of A = D + O with D its diagonal:
+    // A A = O O + D O + O D + D D
+    const float to_o = c.b * (kScaleB / kScaleA);
+    const float to_do = c.c * (kScaleB / kScaleA);
+    const float to_oo = c.c * (kScaleB / (kScaleA * kScaleA));
+    tile_out<C, true>(
+        lds, acc, true, tm != tn && !cut,
+        [&](int m, int n) {
+          Seen x;
+          if constexpr (Step == kOrthoSquare) {
+            m = min(m, rows - 1);
+            n = min(n, cols - 8);
+            const uint32_t at = static_cast<uint32_t>(m) * pitch + n;
+            x.hi = load8<MTA_F16, false>(seen + at, 0);
+            if constexpr (kTwo)
+              x.lo = load8<MTA_F16, false>(seen + at + sp.plane_a, 0);
+            x.row = da[m0 + m];
+            x.col = load8<MTA_F32, false>(da + n0, n);
+          }
+          return x;
+        },
+        [&](int m, int n, float (&v)[8], const Seen &x) {
+          if (m >= rows || n >= cols) return;
+          const uint32_t at = static_cast<uint32_t>(m) * pitch + n;
+          if constexpr (Step == kOrthoGram) {
+            if (cut) {
+#pragma unroll
+              for (int e = 0; e < 8; ++e) v[e] *= 1.0f / (kScaleX * kScaleX);
+              auto *p = (MTA_GLOBAL f32x4 *)(cut + at);
+              p[0] = f32x4{v[0], v[1], v[2], v[3]};
+              p[1] = f32x4{v[4], v[5], v[6], v[7]};
+              return;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              v[e] *= kScaleA / (kScaleX * kScaleX);
+          } else {
+            const float of_row = __builtin_fmaf(to_do, x.row, to_o);
+            const int64_t own = m0 + m - (n0 + n);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              float o = x.hi[e];
+              if constexpr (kTwo) o += x.lo[e];
+              const float f = __builtin_fmaf(to_do, x.col[e], of_row);
+              float y = __builtin_fmaf(f, o, v[e] * to_oo);
+              // (O is 0 there, and the diagonal's own)
+              if (edge && e == own)
+                y += kScaleB * (x.row * (c.b + c.c * x.row));
+              v[e] = y;
+            }
+          }
+          if (edge) {
+            constexpr float kTo = Step == kOrthoGram ? kScaleA : kScaleB;
+            const int64_t own = m0 + m - (n0 + n);
+            const int64_t left = sp.small - (n0 + n);
+            float d = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              d = e == own ? v[e] : d;
+              v[e] = e == own || e >= left ? 0.0f : v[e];
+            }
+            if (own >= 0 && own < 8) diag[m0 + m] = d * (1.0f / kTo);
+          }
+          store_planes<kTwo>(here + at, sp.plane_a, v);
+        },
+        [](int, int) { return 0; },
+        [&](int n, int m, float (&v)[8], int) {
+          // (rows of the mirror image are the columns; all of its columns are)
+          if (n0 + n >= sp.small) return;
+          const uint32_t at = static_cast<uint32_t>(n) * pitch + m;
+          store_planes<kTwo>(there + at, sp.plane_a, v);
+        });
   } else {
+    const Operand b{pb, sp.plane_a, sp.pitch_a, sp.small, sp.small};
     tile_product<C, true, kAlong, kAcross>(
         b, Operand{x_old, sp.plane_x, sp.pitch_x, sp.pitch_x, sp.small}, pairs,
         m0, n0, 0, deep_a, lds, acc);
     const bool tall = it.rows > it.cols;
     const bool skip = c.amp && c.amp->found_inf != 0.0f;
-    const bool whole = c.whole || it.planes > 1;
-    const auto next = [&](int m, int n, float (&v)[8]) {
-      const int64_t row = m0 + m, col = n0 + n;
-      if (row >= sp.small || col >= sp.pitch_x) return;
-      const int64_t at = row * sp.pitch_x + col;
-      const Raw8<MTA_F16> hi = load8<MTA_F16, false>(x_old, at);
-      const Raw8<MTA_F16> lo = load8<MTA_F16, false>(x_old + sp.plane_x, at);
-      const float e_i = db[row];
-      // kept: times kScaleX; handed out: as it is
-      constexpr float kTo = Step == kOrthoLast ? 1.0f / kScaleX : 1.0f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float all = hi[e] + lo[e];
-        v[e] = (c.a * all + (e_i * (whole ? all : hi[e]) +
-                             v[e] * (1.0f / kScaleB))) *
-               kTo;
-      }
-      if constexpr (Step == kOrthoNext) {
-        store_planes(x_new + at, x_new + at + sp.plane_x, v);
-      } else if (!tall) {
-        put_result(it, c, row, col, v, skip);
-      }
+    const uint32_t pitch = static_cast<uint32_t>(sp.pitch_x);
+    const int cols = static_cast<int>(min(sp.pitch_x - n0, int64_t{C::kBN}));
+    const uint16_t *from = x_old + m0 * sp.pitch_x + n0;
+    uint16_t *to = reinterpret_cast<uint16_t *>(
+                       it.ws + sp.x + (1 - c.which) * sp.next_x) +
+                   m0 * sp.pitch_x + n0;
+    // kept: times kScaleX; handed out: as it is
+    constexpr float kTo = Step == kOrthoLast ? 1.0f / kScaleX : 1.0f;
+    struct Seen {
+      Raw8<MTA_F16> hi, lo;
+      float diag;
     };
     tile_out<C, Step == kOrthoLast>(
-        lds, acc, true, Step == kOrthoLast && tall, next,
-        [&](int n, int m, float (&v)[8]) {
+        lds, acc, true, Step == kOrthoLast && tall,
+        [&](int m, int n) {
+          m = min(m, rows - 1);
+          n = min(n, cols - 8);
+          const uint32_t at = static_cast<uint32_t>(m) * pitch + n;
+          return Seen{load8<MTA_F16, false>(from + at, 0),
+                      load8<MTA_F16, false>(from + at + sp.plane_x, 0),
+                      db[m0 + m]};
+        },
+        [&](int m, int n, float (&v)[8], const Seen &x) {
+          if (m >= rows || n >= cols) return;
+          // a X + e X, the second one of the first values alone at first
+          const float of_hi = (c.a + x.diag) * kTo;
+          const float of_lo = kTwo || c.whole ? of_hi : c.a * kTo;
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            v[e] = __builtin_fmaf(
+                of_hi, x.hi[e],
+                __builtin_fmaf(of_lo, x.lo[e], v[e] * (kTo / kScaleB)));
+          if constexpr (Step == kOrthoNext)
+            store_planes<true>(to + static_cast<uint32_t>(m) * pitch + n,
+                               sp.plane_x, v);
+          else if (!tall)
+            put_result(it, c, m0 + m, n0 + n, v, skip);
+        },
+        [](int, int) { return 0; },
+        [&](int n, int m, float (&v)[8], int) {
           if constexpr (Step == kOrthoLast)
             put_result(it, c, n0 + n, m0 + m, v, skip);
         });
   }
 }
 
+template <class C, int Planes>
+hipError_t start(int step, const OrthoList &l, const OrthoCall &c,
+                 hipStream_t s) {
+  const auto go = [&](auto which) {
+    k_ortho_product<C, decltype(which)::value, Planes>
+        <<<l.first[l.count], C::kThreads, 0, s>>>(l, c);
+    return hipGetLastError();
+  };
+  switch (step) {
+    case kOrthoGram: return go(std::integral_constant<int, kOrthoGram>{});
+    case kOrthoSquare: return go(std::integral_constant<int, kOrthoSquare>{});
+    case kOrthoNext: return go(std::integral_constant<int, kOrthoNext>{});
+    default: return go(std::integral_constant<int, kOrthoLast>{});
+  }
+}
+
 template <class C>
 hipError_t start(int step, const OrthoList &l, const OrthoCall &c,
                  hipStream_t s) {
-  const uint32_t grid = l.first[l.count];
-  switch (step) {
-    case kOrthoGram:
-      k_ortho_product<C, kOrthoGram><<<grid, C::kThreads, 0, s>>>(l, c);
-      break;
-    case kOrthoSquare:
-      k_ortho_product<C, kOrthoSquare><<<grid, C::kThreads, 0, s>>>(l, c);
-      break;
-    case kOrthoNext:
-      k_ortho_product<C, kOrthoNext><<<grid, C::kThreads, 0, s>>>(l, c);
-      break;
-    default:
-      k_ortho_product<C, kOrthoLast><<<grid, C::kThreads, 0, s>>>(l, c);
-  }
-  return hipGetLastError();
+  return c.planes > 1 ? start<C, 2>(step, l, c, s) : start<C, 1>(step, l, c, s);
 }
 
 }  // namespace
@@ -438,10 +502,16 @@ hipError_t launch_ortho_load(const OrthoList &l, const OrthoCall &c,
   return hipGetLastError();
 }
 
-hipError_t launch_ortho_product(int step, int tile, const OrthoList &l,
+hipError_t launch_ortho_join(const OrthoList &l, const OrthoCall &c,
+                             hipStream_t s) {
+  k_ortho_join<<<l.first[l.count], 256, 0, s>>>(l, c);
+  return hipGetLastError();
+}
+
+hipError_t launch_ortho_product(int step, int tile, bool deep, const OrthoList &l,
                                 const OrthoCall &c, hipStream_t s) {
-  return tile == 256 ? start<Tile256>(step, l, c, s)
-                     : start<Tile128>(step, l, c, s);
+  if (tile == 256) return start<Tile256>(step, l, c, s);
+  return deep ? start<TileDeep>(step, l, c, s) : start<Tile128>(step, l, c, s);
 }
 
 }  // namespace mta
