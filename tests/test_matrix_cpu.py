@@ -124,21 +124,28 @@ def test_orthogonalize_refuses_shared_outputs_of_a_list():
 
 
 def test_orthogonalize_workspace():
-    one = B.mta_orthogonalize_workspace(ortho([{}]))
-    # two X of two planes, A and B, 40 rows each; the partial sums
-    assert one >= 40 * (128 * 2 * 2 * 2 + 64 * 2 * 2)
-    assert one % 256 == 0
-    assert B.mta_orthogonalize_workspace(ortho([{}], precise=1)) > one
-    # forty matrices share a launch
-    assert B.mta_orthogonalize_workspace(ortho([{}] * 40)) == 40 * one
-    assert B.mta_orthogonalize_workspace(ortho([{}] * 81)) == 40 * one
+    def need(entries, **kw):
+        return B.mta_orthogonalize_workspace(ortho(entries, **kw))
+
+    small = need([{}])
+    # two runs of 64 columns: their Gram matrices and the factor in float64
+    assert small >= 3 * 48 * 48 * 8
+    size = dict(rows=600, cols=700, ldg=700, ldout=700)
+    one = need([size])
+    # two X of two planes, A and B, 600 rows each
+    assert one >= 600 * (704 * 2 * 2 * 2 + 640 * 2 * 2)
+    assert small % 256 == 0 and one % 256 == 0
+    assert need([size], precise=1) > one
+    # forty matrices share a launch, the small ones another
+    assert need([{}] * 40) == 40 * small == need([{}] * 81)
+    many = need([size] * 40)
+    assert 40 * 600 * (704 * 8 + 640 * 4) <= many == need([size] * 81)
+    assert need([size] * 40 + [{}] * 40) == many
     # 4 GiB at a time, unless one matrix needs more
     big = dict(rows=8192, cols=8192)
-    each = B.mta_orthogonalize_workspace(ortho([big]))
-    assert B.mta_orthogonalize_workspace(ortho([big] * 30)) <= 1 << 32
-    assert B.mta_orthogonalize_workspace(
-        ortho([dict(rows=1 << 16, cols=1 << 16)])) > 1 << 32 > each
-    assert B.mta_orthogonalize_workspace(ortho([dict(rows=0)])) == 0
+    assert need([big]) < need([big] * 30) <= 1 << 32
+    assert need([dict(rows=1 << 16, cols=1 << 16)]) > 1 << 32
+    assert need([dict(rows=0)]) == 0
     assert _code(B.mta_orthogonalize_workspace, ortho([dict(rows=-1)])) == -1
 
 
