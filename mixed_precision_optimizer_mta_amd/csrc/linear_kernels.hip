@@ -4,6 +4,10 @@
 //   z = h w^T,  p = softmax(z),  loss = sum weight (-log p[target])
 //   dz = weight (p - [target]),  dh = dz w,  dw = dz^T h
 //
+// Rows that are left out (padding, prompts) cost nothing: a first kernel lists
+// the others, h is packed in that order, and every product ends at their number,
+// which stays on the device.
+//
 // The forward is one product whose tiles leave two numbers a row, the largest
 // logit and the sum of exponentials beside it (without the target's: 1 - p keeps
 // its digits as p nears 1), and a kernel that joins a row's tiles.  The
@@ -34,43 +38,56 @@ __device__ __forceinline__ bool left_out(const LinearArgs &l, int64_t r) {
          (l.a.weights && l.a.weights[r] == 0.0f);
 }
 
-// The weight of a row without weights, and the largest magnitude of any.
-__global__ __launch_bounds__(1024) void k_linear_weights(const LinearArgs l) {
+// The rows that take part, in order, their number, the weight of a row without
+// weights and the largest magnitude of any: one workgroup, a run of rows a lane.
+__global__ __launch_bounds__(1024) void k_linear_rows_in(const LinearArgs l) {
   const mta_linear_loss_args &a = l.a;
-  int64_t count = 0;
+  const int64_t each = (a.rows + 1023) / 1024;
+  const int64_t from = min(a.rows, each * threadIdx.x);
+  const int64_t to = min(a.rows, from + each);
+  int count = 0;
   float most = 0.0f;
-  for (int64_t r = threadIdx.x; r < a.rows; r += 1024) {
-    if (l.backward) {
-      most = fmaxf(most, fabsf(l.rows[r].weight));
-    } else if (a.weights) {
-      if (!left_out(l, r)) most = fmaxf(most, fabsf(a.weights[r]));
-    } else {
-      count += a.targets[r] != a.ignore_index;
-    }
+#pragma unroll 8
+  for (int64_t r = from; r < to; ++r) {
+    const bool in = !left_out(l, r);
+    count += in;
+    if (l.backward) most = fmaxf(most, fabsf(l.rows[r].weight));
+    else if (a.weights && in) most = fmaxf(most, fabsf(a.weights[r]));
   }
-  __shared__ int64_t counts[16];
-  __shared__ float mosts[16];
+  // counts of the lanes before
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  int before = count;
 #pragma unroll
-  for (int d = 32; d > 0; d /= 2) {
-    count += __shfl_xor(count, d);
+  for (int d = 1; d < 64; d *= 2) {
+    const int x = __shfl_up(before, d);
+    if (lane >= d) before += x;
     most = fmaxf(most, __shfl_xor(most, d));
   }
-  if (threadIdx.x % 64 == 0) {
-    counts[threadIdx.x / 64] = count;
-    mosts[threadIdx.x / 64] = most;
+  __shared__ int counts[16];
+  __shared__ float mosts[16];
+  if (lane == 63) {
+    counts[wave] = before;
+    mosts[wave] = most;
   }
   __syncthreads();
+  before -= count;
+  int all = 0;
+  most = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    if (k < wave) before += counts[k];
+    all += counts[k];
+    most = fmaxf(most, mosts[k]);
+  }
+#pragma unroll 8
+  for (int64_t r = from; r < to; ++r)
+    if (!left_out(l, r)) l.index[before++] = static_cast<int>(r);
   if (threadIdx.x == 0) {
-    count = 0;
-    most = 0.0f;
-    for (int k = 0; k < 16; ++k) {
-      count += counts[k];
-      most = fmaxf(most, mosts[k]);
-    }
-    const float each =
-        count > 0 ? static_cast<float>(1.0 / static_cast<double>(count)) : 0.0f;
-    l.scalars[0] = each;
-    l.scalars[1] = l.backward || a.weights ? most : each;
+    const float one =
+        all > 0 ? static_cast<float>(1.0 / static_cast<double>(all)) : 0.0f;
+    l.scalars[0] = one;
+    l.scalars[1] = l.backward || a.weights ? most : one;
+    *l.active = all;
   }
 }
 
@@ -111,158 +128,242 @@ __device__ __forceinline__ void put_planes(uint16_t *to, int64_t plane,
   }
 }
 
-// Rows of an operand into its planes, with zeros behind the last column and in
-// the rows that are left out.
+// Rows of w into its planes, with zeros behind the last column.
 template <int D>
-__global__ __launch_bounds__(256) void k_linear_pack(
-    const LinearArgs l, const void *from, int64_t ld, int64_t rows,
-    uint16_t *to, int64_t plane, bool mask) {
-  const int64_t runs = l.pitch / 8;
-  for (int64_t q = int64_t{blockIdx.x} * 256 + threadIdx.x; q < rows * runs;
-       q += int64_t{gridDim.x} * 256) {
-    const int64_t r = q / runs, i = (q - r * runs) * 8;
-    const int64_t left = l.a.width - i;
-    const int n = static_cast<int>(left >= 8 ? 8 : left > 0 ? left : 0);
-    float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (n > 0 && !(mask && left_out(l, r))) {
-      const Raw8<D> x = n == 8 ? load8<D, false>(from, r * ld + i)
-                               : load8_part<D>(from, r * ld + i, n, 0);
+__device__ __forceinline__ void pack_run(const LinearArgs &l, const void *from,
+                                         int64_t row, int64_t i,
+                                         uint16_t *to, int64_t plane) {
+  const int64_t left = l.a.width - i;
+  const int n = static_cast<int>(left >= 8 ? 8 : left > 0 ? left : 0);
+  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (n > 0) {
+    const Raw8<D> x = n == 8 ? load8<D, false>(from, row + i)
+                             : load8_part<D>(from, row + i, n, 0);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = x[e];
-    }
-    put_planes<D>(to + r * l.pitch + i, plane, v);
+    for (int e = 0; e < 8; ++e) v[e] = x[e];
+  }
+  put_planes<D>(to, plane, v);
+}
+
+template <int D>
+__global__ __launch_bounds__(256) void k_linear_pack_w(const LinearArgs l,
+                                                       uint16_t *to) {
+  const int64_t runs = l.pitch / 8;
+  for (int64_t q = int64_t{blockIdx.x} * 256 + threadIdx.x;
+       q < l.a.vocab * runs; q += int64_t{gridDim.x} * 256) {
+    const int64_t r = q / runs, i = (q - r * runs) * 8;
+    pack_run<D>(l, l.a.w, r * l.a.ldw, i, to + r * l.pitch + i, l.w_plane);
   }
 }
 
-// e^x of x <= 0.  For float32 calls with all digits.
+// The rows of h that take part into its planes, and zeros where the others'
+// results are.
 template <int D>
-__device__ __forceinline__ float exponential(float x) {
-  if constexpr (D == MTA_F32) return expf(x);
-  else return __builtin_amdgcn_exp2f(x * 1.44269504f);
+__global__ __launch_bounds__(256) void k_linear_pack_h(const LinearArgs l) {
+  const int64_t runs = l.pitch / 8, active = *l.active;
+  for (int64_t q = int64_t{blockIdx.x} * 256 + threadIdx.x;
+       q < l.a.rows * runs; q += int64_t{gridDim.x} * 256) {
+    const int64_t r = q / runs, i = (q - r * runs) * 8;
+    if (r < active)
+      pack_run<D>(l, l.a.h, l.index[r] * l.a.ldh, i, l.h + r * l.pitch + i,
+                  l.h_plane);
+    if (active == l.a.rows || !left_out(l, r)) continue;
+    if (i == 0 && !l.backward) {
+      l.rows[r] = mta_linear_row{0.0f, 0.0f, 0.0f, 0.0f};
+      if (l.a.logp) l.a.logp[r] = 0.0f;
+    }
+    if (l.a.dh) {
+      const int64_t left = l.a.width - i;
+      const float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      if (left >= 8) {
+        store8<D, false>(l.a.dh, r * l.a.lddh + i, v);
+      } else {
+        for (int e = 0; e < left; ++e)
+          store_elem<D>(l.a.dh, r * l.a.lddh + i + e, 0.0f);
+      }
+    }
+  }
+}
+
+// e^(z - top) with `shift` = shift_of(top): in one fused step, whose rounding of
+// the shift is no larger than that of a logit of top's size; for float32 calls
+// with all digits.
+constexpr float kLog2e = 1.44269504f;
+template <int D>
+__device__ __forceinline__ float shift_of(float top) {
+  // (a row of nothing but -infinity)
+  const float t = top == -__builtin_inff() ? 0.0f : top;
+  return D == MTA_F32 ? t : t * -kLog2e;
+}
+template <int D>
+__device__ __forceinline__ float exponential(float z, float shift) {
+  if constexpr (D == MTA_F32) return expf(z - shift);
+  else return __builtin_amdgcn_exp2f(__builtin_fmaf(z, kLog2e, shift));
 }
 
 template <class C, int D>
-__device__ __forceinline__ void logits_tile(const LinearArgs &l, int64_t m0,
+__device__ __forceinline__ void logits_tile(const LinearArgs &l,
+                                            int64_t active, int64_t m0,
                                             int64_t n0, MTA_LDS uint8_t *lds,
                                             f32x16 (&acc)[C::kRM][C::kRN]) {
-  const Operand h{l.h, l.h_plane, l.pitch, l.a.rows, 0};
+  const Operand h{l.h, l.h_plane, l.pitch, active, 0};
   const Operand w{l.w, l.w_plane, l.w_pitch, l.a.vocab, 0};
   tile_product<C, D == MTA_F16, kAlong, kAlong>(
       h, w, pairs_of(l.planes), m0, n0, 0, (l.a.width + 63) / 64 * 64, lds,
       acc);
 }
 
-// A tile of logits as each row's largest and its sum of exponentials.
+// The tile of block number `blockIdx.x` where `rows` x cols of them are; false:
+// there is none.
+__device__ __forceinline__ bool my_tile(uint32_t rows, uint32_t cols,
+                                        uint32_t &tm, uint32_t &tn) {
+  if (blockIdx.x >= rows * cols) return false;
+  banded(beside(blockIdx.x, rows * cols), rows, cols, tm, tn);
+  return true;
+}
+
+// A tile of logits as each row's largest and its sum of exponentials without
+// the target's.
 template <class C, int D>
 __global__ __launch_bounds__(C::kThreads)
     __attribute__((amdgpu_waves_per_eu(C::kPerSimd, C::kPerSimd))) void
     k_linear_logits(const LinearArgs l) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds_[C::kLds];
   auto *lds = (MTA_LDS uint8_t *)lds_;
+  const int64_t active = *l.active;
   uint32_t tm, tn;
-  banded(beside(blockIdx.x, gridDim.x),
-         static_cast<uint32_t>((l.a.rows + C::kBM - 1) / C::kBM),
-         static_cast<uint32_t>(l.tiles), tm, tn);
+  if (!my_tile(static_cast<uint32_t>((active + C::kBM - 1) / C::kBM),
+               static_cast<uint32_t>(l.tiles), tm, tn))
+    return;
   const int64_t m0 = int64_t{tm} * C::kBM, n0 = int64_t{tn} * C::kBN;
   f32x16 acc[C::kRM][C::kRN];
-  logits_tile<C, D>(l, m0, n0, lds, acc);
+  logits_tile<C, D>(l, active, m0, n0, lds, acc);
 
   const int lane = threadIdx.x % 64;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int wr = wave / C::kWC, wc = wave % C::kWC;
   auto *side = (MTA_LDS f32x2 *)lds;  // [WC][BM]
-  __syncthreads();
   // columns of this lane: n1 + 32 j + 8 q + e
   const int64_t n1 = n0 + wc * C::kTN + lane / 32 * 4;
   const int many =
       static_cast<int>(min(int64_t{C::kBN}, l.a.vocab - n1));
+  const auto column = [](int j, int r) { return j * 32 + r / 4 * 8 + r % 4; };
+  if (n0 + C::kBN > l.a.vocab) {
+#pragma unroll
+    for (int i = 0; i < C::kRM; ++i)
+#pragma unroll
+      for (int j = 0; j < C::kRN; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (column(j, r) >= many) acc[i][j][r] = -__builtin_inff();
+  }
+  int64_t target[C::kRM];
+#pragma unroll
+  for (int i = 0; i < C::kRM; ++i) {
+    const int64_t row = min(m0 + wr * C::kTM + i * 32 + lane % 32, active - 1);
+    target[i] = l.a.targets[l.index[row]] - n1;
+  }
+  __syncthreads();
 #pragma unroll
   for (int i = 0; i < C::kRM; ++i) {
     const int m = wr * C::kTM + i * 32 + lane % 32;
-    const int64_t row = m0 + m;
-    const int64_t target =
-        row < l.a.rows ? ((const MTA_GLOBAL int64_t *)l.a.targets)[row] : -1;
-    const int64_t far = target - n1;
-    const int mine = far >= 0 && far < C::kBN ? static_cast<int>(far) : -1;
-    float top = -__builtin_inff();
+    float top = acc[i][0][0];
 #pragma unroll
     for (int j = 0; j < C::kRN; ++j)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int at = j * 32 + r / 4 * 8 + r % 4;
-        if (at >= many) acc[i][j][r] = -__builtin_inff();
-        top = fmaxf(top, acc[i][j][r]);
-      }
+      for (int r = 0; r < 16; ++r) top = fmaxf(top, acc[i][j][r]);
     top = fmaxf(top, __shfl_xor(top, 32));
-    const float shift = top == -__builtin_inff() ? 0.0f : top;
+    const float shift = shift_of<D>(top);
     float sum = 0.0f;
+    const bool mine = target[i] >= 0 && target[i] < C::kTN;
+    if (__builtin_expect(__any(mine && m0 + m < active), 0)) {
+      const int at = mine ? static_cast<int>(target[i]) : -1;
 #pragma unroll
-    for (int j = 0; j < C::kRN; ++j)
+      for (int j = 0; j < C::kRN; ++j)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const int at = j * 32 + r / 4 * 8 + r % 4;
-        if (at == mine) {
-          l.z_target[row] = acc[i][j][r];
-        } else {
-          sum += exponential<D>(acc[i][j][r] - shift);
+        for (int r = 0; r < 16; ++r) {
+          const float e = exponential<D>(acc[i][j][r], shift);
+          if (column(j, r) == at) {
+            if (m0 + m < active) l.z_target[m0 + m] = acc[i][j][r];
+          } else {
+            sum += e;
+          }
         }
-      }
+    } else {
+      // (two sums: one would be a chain of additions as long as the row)
+      float other = 0.0f;
+#pragma unroll
+      for (int j = 0; j < C::kRN; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; r += 2) {
+          sum += exponential<D>(acc[i][j][r], shift);
+          other += exponential<D>(acc[i][j][r + 1], shift);
+        }
+      sum += other;
+    }
     sum += __shfl_xor(sum, 32);
     if (lane < 32) side[wc * C::kBM + m] = f32x2{top, sum};
   }
   __syncthreads();
   for (int m = threadIdx.x; m < C::kBM; m += C::kThreads) {
-    if (m0 + m >= l.a.rows) break;
+    if (m0 + m >= active) break;
     f32x2 v = side[m];
 #pragma unroll
     for (int k = 1; k < C::kWC; ++k) {
       const f32x2 u = side[k * C::kBM + m];
-      const float top = fmaxf(v[0], u[0]);
-      const float shift = top == -__builtin_inff() ? 0.0f : top;
-      v = f32x2{top, v[1] * exponential<D>(v[0] - shift) +
-                         u[1] * exponential<D>(u[0] - shift)};
+      const float top = fmaxf(v[0], u[0]), shift = shift_of<D>(top);
+      v = f32x2{top, v[1] * exponential<D>(v[0], shift) +
+                         u[1] * exponential<D>(u[0], shift)};
     }
     l.partial[tn * l.a.rows + m0 + m] = make_float2(v[0], v[1]);
   }
 }
 
 // Rows' tiles joined: 64 rows to a workgroup, 16 waves that take every 16th
-// tile and are joined in order.
+// tile and are joined in order.  A workgroup that has all rows sums the loss
+// too.
 template <int D>
 __global__ __launch_bounds__(1024) void k_linear_rows(const LinearArgs l) {
   const mta_linear_loss_args &a = l.a;
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  const int64_t row = int64_t{blockIdx.x} * 64 + lane;
+  const int64_t at = int64_t{blockIdx.x} * 64 + lane, active = *l.active;
+  if (blockIdx.x * 64 >= active && gridDim.x > 1) return;
   const auto join = [](float &top, float &sum, float t, float s) {
-    const float most = fmaxf(top, t);
-    const float shift = most == -__builtin_inff() ? 0.0f : most;
-    sum = sum * exponential<D>(top - shift) + s * exponential<D>(t - shift);
+    const float most = fmaxf(top, t), shift = shift_of<D>(most);
+    sum = sum * exponential<D>(top, shift) + s * exponential<D>(t, shift);
     top = most;
   };
   float top = -__builtin_inff(), sum = 0.0f;
-  if (row < a.rows) {
-#pragma unroll 4
-    for (int64_t t = wave; t < l.tiles; t += 16) {
-      const float2 v = l.partial[t * a.rows + row];
-      join(top, sum, v.x, v.y);
+  if (at < active) {
+    constexpr int kMany = 8;  // on their way at a time
+    for (int64_t t = wave; t < l.tiles; t += 16 * kMany) {
+      float2 v[kMany];
+#pragma unroll
+      for (int k = 0; k < kMany; ++k)
+        v[k] = l.partial[min(t + 16 * k, l.tiles - 1) * a.rows + at];
+#pragma unroll
+      for (int k = 0; k < kMany; ++k)
+        if (t + 16 * k < l.tiles) join(top, sum, v[k].x, v[k].y);
     }
   }
   __shared__ float2 side[16][64];
   side[wave][lane] = make_float2(top, sum);
   __syncthreads();
-  if (wave != 0 || row >= a.rows) return;
+  if (wave != 0) return;
+  double term = 0.0;
+  if (at < active) {
 #pragma unroll
-  for (int k = 1; k < 16; ++k) join(top, sum, side[k][lane].x, side[k][lane].y);
-  const int64_t target = a.targets[row];
-  mta_linear_row r{0.0f, 0.0f, 0.0f, 0.0f};
-  float logp = 0.0f;
-  if (!left_out(l, row)) {
+    for (int k = 1; k < 16; ++k)
+      join(top, sum, side[k][lane].x, side[k][lane].y);
+    const int64_t row = l.index[at], target = a.targets[row];
+    mta_linear_row r;
+    float logp;
     r.weight = a.weights ? a.weights[row] : l.scalars[0];
     if (target < 0 || target >= a.vocab) {
       r.top = r.total = r.rest = logp = __builtin_nanf("");
     } else {
-      const float zt = l.z_target[row];
-      const float own = exponential<D>(zt - top);
+      const float zt = l.z_target[at];
+      const float own = exponential<D>(zt, shift_of<D>(top));
       r.top = top;
       r.total = sum + own;
       r.rest = sum / r.total;
@@ -270,17 +371,23 @@ __global__ __launch_bounds__(1024) void k_linear_rows(const LinearArgs l) {
       // (the largest may be infinite)
       if (!(own == own)) logp = own;
     }
+    l.rows[row] = r;
+    if (a.logp) a.logp[row] = logp;
+    term = -static_cast<double>(r.weight) * logp;
+    l.terms[at] = term;
   }
-  l.rows[row] = r;
-  if (a.logp) a.logp[row] = logp;
-  l.terms[row] = r.weight == 0.0f ? 0.0 : -static_cast<double>(r.weight) * logp;
+  if (gridDim.x == 1) {
+#pragma unroll
+    for (int d = 32; d > 0; d /= 2) term += __shfl_xor(term, d);
+    if (lane == 0) *a.loss = static_cast<float>(term);
+  }
 }
 
 // The loss: each lane's terms in order, then the lanes'.
 __global__ __launch_bounds__(1024) void k_linear_sum(const LinearArgs l) {
   double x = 0.0;
 #pragma unroll 8
-  for (int64_t r = threadIdx.x; r < l.a.rows; r += 1024) x += l.terms[r];
+  for (int64_t r = threadIdx.x; r < *l.active; r += 1024) x += l.terms[r];
 #pragma unroll
   for (int d = 32; d > 0; d /= 2) x += __shfl_xor(x, d);
   __shared__ double side[16];
@@ -293,6 +400,28 @@ __global__ __launch_bounds__(1024) void k_linear_sum(const LinearArgs l) {
   }
 }
 
+// What dz takes of a row, for the rows that take part and, up to a whole step of
+// 64, rows of zeros.
+template <int D>
+__global__ __launch_bounds__(256) void k_linear_info(const LinearArgs l) {
+  const int64_t active = *l.active, deep = (active + 63) / 64 * 64;
+  const int64_t q = int64_t{blockIdx.x} * 256 + threadIdx.x;
+  if (q >= deep) return;
+  LinearInfo x{-__builtin_inff(), 0.0f, 0.0f, -1};
+  if (D == MTA_F32) x.shift = __builtin_inff();
+  if (q < active) {
+    const int64_t row = l.index[q];
+    const mta_linear_row r = l.rows[row];
+    const float share = r.weight / l.scalars[1] * kRoom<D>;
+    x.shift = shift_of<D>(r.top);
+    x.each = share / r.total;
+    x.own = -r.rest * share;
+    const int64_t t = l.a.targets[row];
+    x.target = t >= 0 && t < l.a.vocab ? static_cast<int>(t) : -1;
+  }
+  l.info[q] = x;
+}
+
 // A tile of logits as dz, without the factor that all rows share.
 template <class C, int D>
 __global__ __launch_bounds__(C::kThreads)
@@ -300,36 +429,41 @@ __global__ __launch_bounds__(C::kThreads)
     k_linear_grad(const LinearArgs l) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds_[C::kLds];
   auto *lds = (MTA_LDS uint8_t *)lds_;
+  const int64_t active = *l.active;
   uint32_t tm, tn;
-  banded(beside(blockIdx.x, gridDim.x),
-         static_cast<uint32_t>((l.a.rows + C::kBM - 1) / C::kBM),
-         static_cast<uint32_t>((l.count + C::kBN - 1) / C::kBN), tm, tn);
+  if (!my_tile(static_cast<uint32_t>((active + C::kBM - 1) / C::kBM),
+               static_cast<uint32_t>((l.count + C::kBN - 1) / C::kBN), tm, tn))
+    return;
   const int64_t m0 = int64_t{tm} * C::kBM, n0 = int64_t{tn} * C::kBN;
   f32x16 acc[C::kRM][C::kRN];
-  logits_tile<C, D>(l, m0, l.first + n0, lds, acc);
-  const float most = l.scalars[1];
-  const int64_t wide = (l.count + 63) / 64 * 64;
+  logits_tile<C, D>(l, active, m0, l.first + n0, lds, acc);
+  const int rows = static_cast<int>(
+      min((active + 63) / 64 * 64 - m0, int64_t{C::kBM}));
+  const int cols = static_cast<int>(
+      min((l.count + 63) / 64 * 64 - n0, int64_t{C::kBN}));
+  const int there = static_cast<int>(min(l.count - n0, int64_t{C::kBN}));
+  const int from = static_cast<int>(l.first + n0);
+  uint16_t *to = l.z + m0 * l.pitch_z + n0;
+  const LinearInfo *info = l.info + m0;
+  const uint32_t pitch = static_cast<uint32_t>(l.pitch_z);
   tile_out<C, false>(
-      lds, acc, true, false, [](int, int) { return 0; },
-      [&](int m, int n, float (&v)[8], int) {
-        const int64_t row = m0 + m, col = n0 + n;
-        if (row >= l.deep_rows || col >= wide) return;
-        mta_linear_row r{0.0f, 0.0f, 0.0f, 0.0f};
-        int64_t target = -1;
-        if (row < l.a.rows) {
-          r = l.rows[row];
-          target = l.a.targets[row] - l.first - col;
-        }
-        const float share =
-            r.weight == 0.0f ? 0.0f : r.weight / most * kRoom<D>;
-        const float each = share / r.total;
+      lds, acc, true, false,
+      [&](int m, int) { return info[min(m, rows - 1)]; },
+      [&](int m, int n, float (&v)[8], const LinearInfo &x) {
+        if (m >= rows || n >= cols) return;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float p = e == target ? -r.rest * share
-                                      : exponential<D>(v[e] - r.top) * each;
-          v[e] = share == 0.0f || col + e >= l.count ? 0.0f : p;
+        for (int e = 0; e < 8; ++e)
+          v[e] = exponential<D>(v[e], x.shift) * x.each;
+        const int own = x.target - from - n;
+        if (__any(own >= 0 && own < 8)) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = e == own ? x.own : v[e];
         }
-        put_planes<D>(l.z + row * l.pitch_z + col, l.z_plane, v);
+        if (there < C::kBN) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = n + e < there ? v[e] : 0.0f;
+        }
+        put_planes<D>(to + static_cast<uint32_t>(m) * pitch + n, l.z_plane, v);
       },
       [](int, int) { return 0; }, [](int, int, float (&)[8], int) {});
 }
@@ -364,21 +498,26 @@ __device__ __forceinline__ void put_out(void *to, int64_t at, int n,
   }
 }
 
-// Sums of a tile, rows x width, either out or to the workspace.
+// Sums of a tile, rows x width, either out, to row from + m or index[m], or to
+// the workspace.
 template <class C, int D>
 __device__ __forceinline__ void gradient_out(
     const LinearArgs &l, MTA_LDS uint8_t *lds,
     const f32x16 (&acc)[C::kRM][C::kRN], int64_t m0, int64_t n0, int64_t rows,
-    float *hold, bool add, void *to, int64_t ld, int64_t from, int type,
-    bool accumulate) {
+    float *hold, bool add, void *to, int64_t ld, int64_t from,
+    const int *index, int type, bool accumulate) {
   const float factor = shared_factor<D>(l);
+  const int high = static_cast<int>(min(rows - m0, int64_t{C::kBM}));
   tile_out<C, false>(
-      lds, acc, true, false, [](int, int) { return 0; },
-      [&](int m, int n, float (&v)[8], int) {
-        const int64_t row = m0 + m, col = n0 + n;
-        if (row >= rows || col >= l.a.width) return;
+      lds, acc, true, false,
+      [&](int m, int) {
+        return index ? int64_t{index[m0 + min(m, high - 1)]} : from + m0 + m;
+      },
+      [&](int m, int n, float (&v)[8], int64_t row) {
+        const int64_t col = n0 + n;
+        if (m >= high || col >= l.a.width) return;
         if (hold) {  // (rows of whole runs)
-          auto *at = (MTA_GLOBAL f32x4 *)(hold + row * l.pitch + col);
+          auto *at = (MTA_GLOBAL f32x4 *)(hold + (m0 + m) * l.pitch + col);
           f32x4 x{v[0], v[1], v[2], v[3]}, y{v[4], v[5], v[6], v[7]};
           if (add) {
             x += at[0];
@@ -391,8 +530,8 @@ __device__ __forceinline__ void gradient_out(
         const int many =
             static_cast<int>(min(int64_t{8}, l.a.width - col));
         with_type(type, [&](auto t) {
-          put_out<decltype(t)::value>(to, (from + row) * ld + col, many,
-                                      accumulate, factor, v);
+          put_out<decltype(t)::value>(to, row * ld + col, many, accumulate,
+                                      factor, v);
         });
       },
       [](int, int) { return 0; }, [](int, int, float (&)[8], int) {});
@@ -402,38 +541,43 @@ __device__ __forceinline__ void gradient_out(
 template <class C, int D>
 __global__ __launch_bounds__(C::kThreads)
     __attribute__((amdgpu_waves_per_eu(C::kPerSimd, C::kPerSimd))) void
-    k_linear_dh(const LinearArgs l, const int64_t part_k, const bool hold) {
+    k_linear_dh(const LinearArgs l, const int parts, const bool hold) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds_[C::kLds];
   auto *lds = (MTA_LDS uint8_t *)lds_;
-  const uint32_t rows = static_cast<uint32_t>((l.a.rows + C::kBM - 1) / C::kBM);
+  const int64_t active = *l.active;
   const uint32_t cols =
       static_cast<uint32_t>((l.a.width + C::kBN - 1) / C::kBN);
-  const uint32_t block = beside(blockIdx.x, gridDim.x);
-  const uint32_t part = block / (rows * cols);
+  const uint32_t tiles =
+      static_cast<uint32_t>((active + C::kBM - 1) / C::kBM) * cols;
+  if (blockIdx.x >= tiles * parts) return;
+  const uint32_t block = beside(blockIdx.x, tiles * parts);
+  const uint32_t part = block / tiles;
   uint32_t tm, tn;
-  banded(block % (rows * cols), rows, cols, tm, tn);
+  banded(block % tiles, tiles / cols, cols, tm, tn);
   const int64_t m0 = int64_t{tm} * C::kBM, n0 = int64_t{tn} * C::kBN;
   const int64_t deep = (l.count + 63) / 64 * 64;
-  const int64_t k0 = min(deep, part * part_k), k1 = min(deep, k0 + part_k);
+  const int64_t each = (deep / 64 + parts - 1) / parts * 64;
+  const int64_t k0 = min(deep, part * each), k1 = min(deep, k0 + each);
   f32x16 acc[C::kRM][C::kRN];
-  const Operand z{l.z, l.z_plane, l.pitch_z, l.a.rows, 0};
+  const Operand z{l.z, l.z_plane, l.pitch_z, active, 0};
   const Operand w{l.w + l.first * l.w_pitch, l.w_plane, l.w_pitch,
                   (l.a.width + 7) / 8 * 8, l.count};
   tile_product<C, D == MTA_F16, kAlong, kAcross>(z, w, pairs_of(l.planes), m0,
                                                  n0, k0, k1, lds, acc);
   gradient_out<C, D>(
-      l, lds, acc, m0, n0, l.a.rows,
+      l, lds, acc, m0, n0, active,
       hold ? l.sum_h + part * l.a.rows * l.pitch : nullptr, l.first > 0, l.a.dh,
-      l.a.lddh, 0, l.a.type, false);
+      l.a.lddh, 0, l.index, l.a.type, false);
 }
 
 // A piece of dw = dz^T h over a part of the rows.
 template <class C, int D>
 __global__ __launch_bounds__(C::kThreads)
     __attribute__((amdgpu_waves_per_eu(C::kPerSimd, C::kPerSimd))) void
-    k_linear_dw(const LinearArgs l, const int64_t part_k, const bool hold) {
+    k_linear_dw(const LinearArgs l, const int parts, const bool hold) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds_[C::kLds];
   auto *lds = (MTA_LDS uint8_t *)lds_;
+  const int64_t active = *l.active;
   const uint32_t rows = static_cast<uint32_t>((l.count + C::kBM - 1) / C::kBM);
   const uint32_t cols =
       static_cast<uint32_t>((l.a.width + C::kBN - 1) / C::kBN);
@@ -442,17 +586,18 @@ __global__ __launch_bounds__(C::kThreads)
   uint32_t tm, tn;
   banded(block % (rows * cols), rows, cols, tm, tn);
   const int64_t m0 = int64_t{tm} * C::kBM, n0 = int64_t{tn} * C::kBN;
-  const int64_t k0 = min(l.deep_rows, part * part_k);
-  const int64_t k1 = min(l.deep_rows, k0 + part_k);
+  const int64_t deep = (active + 63) / 64 * 64;
+  const int64_t each = (deep / 64 + parts - 1) / parts * 64;
+  const int64_t k0 = min(deep, part * each), k1 = min(deep, k0 + each);
   f32x16 acc[C::kRM][C::kRN];
-  const Operand z{l.z, l.z_plane, l.pitch_z, (l.count + 63) / 64 * 64,
-                  l.deep_rows};
-  const Operand h{l.h, l.h_plane, l.pitch, l.pitch, l.a.rows};
+  const Operand z{l.z, l.z_plane, l.pitch_z, (l.count + 63) / 64 * 64, deep};
+  const Operand h{l.h, l.h_plane, l.pitch, l.pitch, active};
   tile_product<C, D == MTA_F16, kAcross, kAcross>(z, h, pairs_of(l.planes), m0,
                                                   n0, k0, k1, lds, acc);
   gradient_out<C, D>(l, lds, acc, m0, n0, l.count,
                      hold ? l.sum_w + part * l.count * l.pitch : nullptr, false,
-                     l.a.dw, l.a.lddw, l.first, l.a.dw_type, l.a.accumulate);
+                     l.a.dw, l.a.lddw, l.first, nullptr, l.a.dw_type,
+                     l.a.accumulate);
 }
 
 // Parts held in the workspace, joined in order and out.
@@ -460,7 +605,8 @@ template <int D>
 __global__ __launch_bounds__(256) void k_linear_out(const LinearArgs l,
                                                     const bool dh,
                                                     const int parts) {
-  const int64_t rows = dh ? l.a.rows : l.count;
+  const int64_t rows = dh ? *l.active : l.count;
+  const int64_t step = (dh ? l.a.rows : l.count) * l.pitch;
   const float *from = dh ? l.sum_h : l.sum_w;
   const int64_t runs = (l.a.width + 7) / 8;
   const float factor = shared_factor<D>(l);
@@ -472,14 +618,14 @@ __global__ __launch_bounds__(256) void k_linear_out(const LinearArgs l,
 #pragma unroll 4
     for (int k = 0; k < parts; ++k) {
       const Raw8<MTA_F32> x =
-          load8<MTA_F32, false>(at + k * rows * l.pitch, 0);
+          load8<MTA_F32, false>(at + k * step, 0);
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] += x[e];
     }
     const int many = static_cast<int>(min(int64_t{8}, l.a.width - i));
     with_type(dh ? l.a.type : l.a.dw_type, [&](auto t) {
       if (dh)
-        put_out<decltype(t)::value>(l.a.dh, r * l.a.lddh + i, many, false,
+        put_out<decltype(t)::value>(l.a.dh, l.index[r] * l.a.lddh + i, many, false,
                                     factor, v);
       else
         put_out<decltype(t)::value>(l.a.dw, (l.first + r) * l.a.lddw + i, many,
@@ -515,28 +661,34 @@ void with_tile(const LinearCut &c, int type, F &&f) {
 
 }  // namespace
 
-hipError_t launch_linear_weights(const LinearArgs &l, hipStream_t s) {
-  k_linear_weights<<<1, 1024, 0, s>>>(l);
+hipError_t launch_linear_rows_in(const LinearArgs &l, hipStream_t s) {
+  k_linear_rows_in<<<1, 1024, 0, s>>>(l);
   return hipGetLastError();
 }
 
 hipError_t launch_linear_pack_h(const LinearArgs &l, hipStream_t s) {
-  const int64_t runs = l.a.rows * (l.pitch / 8);
-  const uint32_t grid = std::min<uint32_t>(up(runs, 256), 1u << 20);
+  const uint32_t grid =
+      std::min<uint32_t>(up(l.a.rows * (l.pitch / 8), 256), 1u << 20);
   with_type(l.a.type, [&](auto t) {
-    k_linear_pack<decltype(t)::value><<<grid, 256, 0, s>>>(
-        l, l.a.h, l.a.ldh, l.a.rows, l.h, l.h_plane, true);
+    k_linear_pack_h<decltype(t)::value><<<grid, 256, 0, s>>>(l);
   });
   return hipGetLastError();
 }
 
 hipError_t launch_linear_pack_w(const LinearArgs &l, uint16_t *to,
                                 hipStream_t s) {
-  const int64_t runs = l.a.vocab * (l.pitch / 8);
-  const uint32_t grid = std::min<uint32_t>(up(runs, 256), 1u << 20);
+  const uint32_t grid =
+      std::min<uint32_t>(up(l.a.vocab * (l.pitch / 8), 256), 1u << 20);
   with_type(l.a.type, [&](auto t) {
-    k_linear_pack<decltype(t)::value><<<grid, 256, 0, s>>>(
-        l, l.a.w, l.a.ldw, l.a.vocab, to, l.w_plane, false);
+    k_linear_pack_w<decltype(t)::value><<<grid, 256, 0, s>>>(l, to);
+  });
+  return hipGetLastError();
+}
+
+hipError_t launch_linear_info(const LinearArgs &l, hipStream_t s) {
+  with_type(l.a.type, [&](auto t) {
+    k_linear_info<decltype(t)::value>
+        <<<up(l.a.rows + 63, 256), 256, 0, s>>>(l);
   });
   return hipGetLastError();
 }
@@ -553,11 +705,11 @@ hipError_t launch_linear_logits(const LinearArgs &l, const LinearCut &c,
 }
 
 hipError_t launch_linear_rows(const LinearArgs &l, hipStream_t s) {
-  if (l.a.rows > 0)
-    with_type(l.a.type, [&](auto t) {
-      k_linear_rows<decltype(t)::value><<<up(l.a.rows, 64), 1024, 0, s>>>(l);
-    });
-  k_linear_sum<<<1, 1024, 0, s>>>(l);
+  const uint32_t grid = std::max(1u, up(l.a.rows, 64));
+  with_type(l.a.type, [&](auto t) {
+    k_linear_rows<decltype(t)::value><<<grid, 1024, 0, s>>>(l);
+  });
+  if (grid > 1) k_linear_sum<<<1, 1024, 0, s>>>(l);
   return hipGetLastError();
 }
 
@@ -577,7 +729,7 @@ hipError_t launch_linear_dh(const LinearArgs &l, const LinearCut &c, bool hold,
     using C = decltype(tile);
     k_linear_dh<C, decltype(t)::value>
         <<<up(l.a.rows, C::kBM) * up(l.a.width, C::kBN) * c.parts, C::kThreads,
-           0, s>>>(l, c.part_k, hold);
+           0, s>>>(l, c.parts, hold);
   });
   return hipGetLastError();
 }
@@ -588,7 +740,7 @@ hipError_t launch_linear_dw(const LinearArgs &l, const LinearCut &c, bool hold,
     using C = decltype(tile);
     k_linear_dw<C, decltype(t)::value>
         <<<up(l.count, C::kBM) * up(l.a.width, C::kBN) * c.parts, C::kThreads,
-           0, s>>>(l, c.part_k, hold);
+           0, s>>>(l, c.parts, hold);
   });
   return hipGetLastError();
 }

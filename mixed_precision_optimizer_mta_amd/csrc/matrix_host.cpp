@@ -369,7 +369,7 @@ mta::LinearCut linear_cut(int64_t m, int64_t n, int64_t k, int runs, int most,
       best.tile = tile;
       best.deep = groups <= cus;
       best.parts = static_cast<int>(up(steps, each));
-      best.part_k = each * 64;
+      best.us = us;
       if (groups > 8 * cus) break;
     }
   }
@@ -387,17 +387,31 @@ mta::LinearPlan linear_plan(const mta_linear_loss_args *a, bool copy_w,
   const bool grad = a->dh || a->dw;
   p.logits = linear_cut(a->rows, a->vocab, a->width, runs, 1, cus);
   if (grad) {
+    // As many pieces as keep dz within its bytes, or up to three more, if they
+    // fill the rounds of workgroups better.
     const int64_t column = std::max<int64_t>(1, p.deep_rows) * 2 * p.planes;
     const int64_t most =
         std::max<int64_t>(256, kPieceBytes / column / 256 * 256);
-    p.pieces = up(a->vocab, most);
-    p.piece = p.pieces == 1 ? a->vocab
-                            : up(up(a->vocab, p.pieces), 256) * 256;
+    const int64_t least = up(a->vocab, most);
+    double best = 0.0;
+    for (int64_t n = least; n <= least + (least > 1 ? 3 : 0); ++n) {
+      const int64_t piece =
+          n == 1 ? a->vocab : up(up(a->vocab, n), 256) * 256;
+      const auto grad = linear_cut(a->rows, piece, a->width, runs, 1, cus);
+      const auto dh = linear_cut(a->rows, a->width, piece, runs, 32, cus);
+      const auto dw = linear_cut(piece, a->width, a->rows, runs, 32, cus);
+      const double us = static_cast<double>(up(a->vocab, piece)) *
+                        (grad.us + (a->dh ? dh.us : 0.0) +
+                         (a->dw ? dw.us : 0.0));
+      if (n > least && us >= best) continue;
+      best = us;
+      p.piece = piece;
+      p.grad = grad;
+      p.dh = dh;
+      p.dw = dw;
+    }
     p.pieces = up(a->vocab, p.piece);
     p.pitch_z = mta::plane_pitch(p.piece);
-    p.grad = linear_cut(a->rows, p.piece, a->width, runs, 1, cus);
-    p.dh = linear_cut(a->rows, a->width, p.piece, runs, 32, cus);
-    p.dw = linear_cut(p.piece, a->width, a->rows, runs, 32, cus);
     p.hold_dh = a->dh && (p.pieces > 1 || p.dh.parts > 1);
     p.hold_dw = a->dw && p.dw.parts > 1;
   }
@@ -407,7 +421,10 @@ mta::LinearPlan linear_plan(const mta_linear_loss_args *a, bool copy_w,
     at += up(bytes, 256) * 256;
     return here;
   };
+  p.active = take(4);
   p.scalars = take(8);
+  p.index = take(a->rows * 4);
+  p.info = take(grad ? p.deep_rows * 16 : 0);
   p.terms = take(a->rows * 8);
   p.rows = take(a->rows * 16);
   p.z_target = take(a->rows * 4);
@@ -516,6 +533,9 @@ hipError_t run_linear(const mta_linear_loss_args *a, const mta::LinearPlan &p,
   l.rows = a->saved ? a->saved
                     : reinterpret_cast<mta_linear_row *>(ws + p.rows);
   l.scalars = reinterpret_cast<float *>(ws + p.scalars);
+  l.active = reinterpret_cast<int *>(ws + p.active);
+  l.index = reinterpret_cast<int *>(ws + p.index);
+  l.info = reinterpret_cast<mta::LinearInfo *>(ws + p.info);
   l.terms = reinterpret_cast<double *>(ws + p.terms);
   l.z_target = reinterpret_cast<float *>(ws + p.z_target);
   l.partial = reinterpret_cast<float2 *>(ws + p.partial);
@@ -527,13 +547,12 @@ hipError_t run_linear(const mta_linear_loss_args *a, const mta::LinearPlan &p,
   l.backward = backward;
   l.pitch = p.pitch;
   l.pitch_z = p.pitch_z;
-  l.deep_rows = p.deep_rows;
   l.h_plane = a->rows * p.pitch;
   l.z_plane = p.deep_rows * p.pitch_z;
   l.tiles = up(a->vocab, p.logits.tile);
   hipError_t e;
   const auto ok = [&](hipError_t x) { return (e = x) == hipSuccess; };
-  if (!ok(mta::launch_linear_weights(l, s))) return e;
+  if (!ok(mta::launch_linear_rows_in(l, s))) return e;
   if (a->rows > 0) {
     if (!ok(mta::launch_linear_pack_h(l, s))) return e;
     if (p.copy_w) {
@@ -553,6 +572,7 @@ hipError_t run_linear(const mta_linear_loss_args *a, const mta::LinearPlan &p,
   }
   if (!a->dh && !a->dw) return e;
   if (a->rows == 0) return a->dw ? mta::launch_linear_none(l, s) : e;
+  if (!ok(mta::launch_linear_info(l, s))) return e;
   for (int64_t k = 0; k < p.pieces; ++k) {
     l.first = k * p.piece;
     l.count = std::min(p.piece, a->vocab - l.first);

@@ -171,7 +171,7 @@ struct LinearCut {
   int tile;
   bool deep;  // no CU gets a second workgroup of the small tile
   int parts;
-  int64_t part_k;  // multiples of 64
+  double us;  // estimated
 };
 
 // The course of a call.
@@ -182,16 +182,30 @@ struct LinearPlan {
   int64_t piece;        // columns of the vocabulary at a time, all but the last
   int64_t pieces;
   int64_t pitch_z;      // of dz
-  int64_t deep_rows;    // rows of dz: whole steps of 64
+  int64_t deep_rows;    // rows of dz, at most: whole steps of 64
   LinearCut logits, grad, dh, dw;
   bool hold_dh, hold_dw;  // sums held in the workspace before they go out
   // offsets in the workspace
-  int64_t scalars, terms, rows, z_target, partial, h, w, z, sum_h, sum_w, bytes;
+  int64_t active, scalars, terms, rows, index, info, z_target, partial, h, w, z,
+      sum_h, sum_w, bytes;
 };
 
+// What dz takes of a row, besides the factor that all rows share.
+struct LinearInfo {
+  float shift;  // of its exponentials
+  float each;   // weight / total
+  float own;    // the target's value
+  int target;   // -1: none
+};
+
+// Rows that take part come first, in order, in h, z_target, partial, terms, info
+// and dz: index[] says which they are, *active how many.
 struct LinearArgs {
   mta_linear_loss_args a;
   mta_linear_row *rows;   // of the workspace or the caller's
+  int *active;
+  int *index;             // [rows]
+  LinearInfo *info;       // [deep_rows]
   float *scalars;         // [0] weight of a row without weights, [1] largest
   double *terms;          // [rows] of the loss
   float *z_target;        // [rows]
@@ -201,14 +215,15 @@ struct LinearArgs {
   uint16_t *z;            // planes of a piece of dz
   float *sum_h, *sum_w;   // [parts][rows or piece][pitch]
   int64_t h_plane, w_plane, w_pitch, z_plane;
-  int64_t pitch, pitch_z, deep_rows;
+  int64_t pitch, pitch_z;
   int64_t first, count;   // the piece
   int64_t tiles;          // of the vocabulary
   int planes;
   int backward;           // rows are the caller's, and say what is left out
 };
 
-hipError_t launch_linear_weights(const LinearArgs &l, hipStream_t s);
+hipError_t launch_linear_rows_in(const LinearArgs &l, hipStream_t s);
+hipError_t launch_linear_info(const LinearArgs &l, hipStream_t s);
 hipError_t launch_linear_pack_h(const LinearArgs &l, hipStream_t s);
 hipError_t launch_linear_pack_w(const LinearArgs &l, uint16_t *to,
                                 hipStream_t s);
