@@ -39,50 +39,70 @@ __device__ __forceinline__ bool left_out(const LinearArgs &l, int64_t r) {
 }
 
 // The rows that take part, in order, their number, the weight of a row without
-// weights and the largest magnitude of any: one workgroup, a run of rows a lane.
+// weights and the largest magnitude of any: one workgroup, a run of up to 64 rows
+// a lane at a time, whose answers are bits of a word.
 __global__ __launch_bounds__(1024) void k_linear_rows_in(const LinearArgs l) {
   const mta_linear_loss_args &a = l.a;
-  const int64_t each = (a.rows + 1023) / 1024;
-  const int64_t from = min(a.rows, each * threadIdx.x);
-  const int64_t to = min(a.rows, from + each);
-  int count = 0;
-  float most = 0.0f;
-#pragma unroll 8
-  for (int64_t r = from; r < to; ++r) {
-    const bool in = !left_out(l, r);
-    count += in;
-    if (l.backward) most = fmaxf(most, fabsf(l.rows[r].weight));
-    else if (a.weights && in) most = fmaxf(most, fabsf(a.weights[r]));
-  }
-  // counts of the lanes before
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  int before = count;
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const int x = __shfl_up(before, d);
-    if (lane >= d) before += x;
-    most = fmaxf(most, __shfl_xor(most, d));
-  }
   __shared__ int counts[16];
   __shared__ float mosts[16];
-  if (lane == 63) {
-    counts[wave] = before;
-    mosts[wave] = most;
-  }
-  __syncthreads();
-  before -= count;
+  float most = 0.0f;
   int all = 0;
-  most = 0.0f;
-#pragma unroll
-  for (int k = 0; k < 16; ++k) {
-    if (k < wave) before += counts[k];
-    all += counts[k];
-    most = fmaxf(most, mosts[k]);
-  }
+  constexpr int64_t kRun = 65536;
+  for (int64_t base = 0; base < a.rows; base += kRun) {
+    const int64_t n = min(a.rows - base, kRun);
+    const int each = static_cast<int>((n + 1023) / 1024);
+    const int64_t from = base + min(n, int64_t{each} * threadIdx.x);
+    const int here = static_cast<int>(min(base + n - from, int64_t{each}));
+    uint64_t in = 0;
+    const auto mark = [&](auto &&takes_part) {
 #pragma unroll 8
-  for (int64_t r = from; r < to; ++r)
-    if (!left_out(l, r)) l.index[before++] = static_cast<int>(r);
+      for (int k = 0; k < here; ++k)
+        if (takes_part(from + k)) in |= uint64_t{1} << k;
+    };
+    if (l.backward)
+      mark([&](int64_t r) {
+        const float w = l.rows[r].weight;
+        most = fmaxf(most, fabsf(w));
+        return w != 0.0f;
+      });
+    else if (a.weights)
+      mark([&](int64_t r) {
+        const float w = a.weights[r];
+        const bool is = a.targets[r] != a.ignore_index && w != 0.0f;
+        most = is ? fmaxf(most, fabsf(w)) : most;
+        return is;
+      });
+    else
+      mark([&](int64_t r) { return a.targets[r] != a.ignore_index; });
+    // counts of the lanes before
+    const int count = __popcll(in);
+    int before = count;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int x = __shfl_up(before, d);
+      if (lane >= d) before += x;
+    }
+    if (lane == 63) counts[wave] = before;
+    __syncthreads();
+    before += all - count;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      if (k < wave) before += counts[k];
+      all += counts[k];
+    }
+    for (; in; in &= in - 1)
+      l.index[before++] =
+          static_cast<int>(from) + __ffsll(static_cast<long long>(in)) - 1;
+    __syncthreads();
+  }
+#pragma unroll
+  for (int d = 32; d > 0; d /= 2) most = fmaxf(most, __shfl_xor(most, d));
+  if (lane == 0) mosts[wave] = most;
+  __syncthreads();
   if (threadIdx.x == 0) {
+#pragma unroll
+    for (int k = 1; k < 16; ++k) most = fmaxf(most, mosts[k]);
     const float one =
         all > 0 ? static_cast<float>(1.0 / static_cast<double>(all)) : 0.0f;
     l.scalars[0] = one;
@@ -213,12 +233,13 @@ __device__ __forceinline__ void logits_tile(const LinearArgs &l,
       acc);
 }
 
-// The tile of block number `blockIdx.x` where `rows` x cols of them are; false:
+// The tile of workgroup number `block` where rows x cols of them are; false:
 // there is none.
-__device__ __forceinline__ bool my_tile(uint32_t rows, uint32_t cols,
-                                        uint32_t &tm, uint32_t &tn) {
-  if (blockIdx.x >= rows * cols) return false;
-  banded(beside(blockIdx.x, rows * cols), rows, cols, tm, tn);
+__device__ __forceinline__ bool my_tile(uint32_t block, uint32_t rows,
+                                        uint32_t cols, uint32_t &tm,
+                                        uint32_t &tn) {
+  if (block >= rows * cols) return false;
+  banded(beside(block, rows * cols), rows, cols, tm, tn);
   return true;
 }
 
@@ -232,7 +253,8 @@ __global__ __launch_bounds__(C::kThreads)
   auto *lds = (MTA_LDS uint8_t *)lds_;
   const int64_t active = *l.active;
   uint32_t tm, tn;
-  if (!my_tile(static_cast<uint32_t>((active + C::kBM - 1) / C::kBM),
+  if (!my_tile(blockIdx.x,
+               static_cast<uint32_t>((active + C::kBM - 1) / C::kBM),
                static_cast<uint32_t>(l.tiles), tm, tn))
     return;
   const int64_t m0 = int64_t{tm} * C::kBM, n0 = int64_t{tn} * C::kBN;
@@ -422,52 +444,6 @@ __global__ __launch_bounds__(256) void k_linear_info(const LinearArgs l) {
   l.info[q] = x;
 }
 
-// A tile of logits as dz, without the factor that all rows share.
-template <class C, int D>
-__global__ __launch_bounds__(C::kThreads)
-    __attribute__((amdgpu_waves_per_eu(C::kPerSimd, C::kPerSimd))) void
-    k_linear_grad(const LinearArgs l) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds_[C::kLds];
-  auto *lds = (MTA_LDS uint8_t *)lds_;
-  const int64_t active = *l.active;
-  uint32_t tm, tn;
-  if (!my_tile(static_cast<uint32_t>((active + C::kBM - 1) / C::kBM),
-               static_cast<uint32_t>((l.count + C::kBN - 1) / C::kBN), tm, tn))
-    return;
-  const int64_t m0 = int64_t{tm} * C::kBM, n0 = int64_t{tn} * C::kBN;
-  f32x16 acc[C::kRM][C::kRN];
-  logits_tile<C, D>(l, active, m0, l.first + n0, lds, acc);
-  const int rows = static_cast<int>(
-      min((active + 63) / 64 * 64 - m0, int64_t{C::kBM}));
-  const int cols = static_cast<int>(
-      min((l.count + 63) / 64 * 64 - n0, int64_t{C::kBN}));
-  const int there = static_cast<int>(min(l.count - n0, int64_t{C::kBN}));
-  const int from = static_cast<int>(l.first + n0);
-  uint16_t *to = l.z + m0 * l.pitch_z + n0;
-  const LinearInfo *info = l.info + m0;
-  const uint32_t pitch = static_cast<uint32_t>(l.pitch_z);
-  tile_out<C, false>(
-      lds, acc, true, false,
-      [&](int m, int) { return info[min(m, rows - 1)]; },
-      [&](int m, int n, float (&v)[8], const LinearInfo &x) {
-        if (m >= rows || n >= cols) return;
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          v[e] = exponential<D>(v[e], x.shift) * x.each;
-        const int own = x.target - from - n;
-        if (__any(own >= 0 && own < 8)) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = e == own ? x.own : v[e];
-        }
-        if (there < C::kBN) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = n + e < there ? v[e] : 0.0f;
-        }
-        put_planes<D>(to + static_cast<uint32_t>(m) * pitch + n, l.z_plane, v);
-      },
-      [](int, int) { return 0; }, [](int, int, float (&)[8], int) {});
-}
-
 // The factor that all of dz shares.
 template <int D>
 __device__ __forceinline__ float shared_factor(const LinearArgs &l) {
@@ -537,51 +513,97 @@ __device__ __forceinline__ void gradient_out(
       [](int, int) { return 0; }, [](int, int, float (&)[8], int) {});
 }
 
+// A tile of logits as dz, without the factor that all rows share.
+template <class C, int D>
+__device__ __forceinline__ void make_dz(const LinearArgs &l,
+                                        const LinearPiece &piece,
+                                        int64_t active, uint32_t block,
+                                        MTA_LDS uint8_t *lds) {
+  uint32_t tm, tn;
+  if (!my_tile(block, static_cast<uint32_t>((active + C::kBM - 1) / C::kBM),
+               static_cast<uint32_t>((piece.count + C::kBN - 1) / C::kBN), tm,
+               tn))
+    return;
+  const int64_t m0 = int64_t{tm} * C::kBM, n0 = int64_t{tn} * C::kBN;
+  f32x16 acc[C::kRM][C::kRN];
+  logits_tile<C, D>(l, active, m0, piece.first + n0, lds, acc);
+  const int rows = static_cast<int>(
+      min((active + 63) / 64 * 64 - m0, int64_t{C::kBM}));
+  const int cols = static_cast<int>(
+      min((piece.count + 63) / 64 * 64 - n0, int64_t{C::kBN}));
+  const int there = static_cast<int>(min(piece.count - n0, int64_t{C::kBN}));
+  const int from = static_cast<int>(piece.first + n0);
+  uint16_t *to = piece.z + m0 * l.pitch_z + n0;
+  const LinearInfo *info = l.info + m0;
+  const uint32_t pitch = static_cast<uint32_t>(l.pitch_z);
+  tile_out<C, false>(
+      lds, acc, true, false,
+      [&](int m, int) { return info[min(m, rows - 1)]; },
+      [&](int m, int n, float (&v)[8], const LinearInfo &x) {
+        if (m >= rows || n >= cols) return;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          v[e] = exponential<D>(v[e], x.shift) * x.each;
+        const int own = x.target - from - n;
+        if (__any(own >= 0 && own < 8)) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = e == own ? x.own : v[e];
+        }
+        if (there < C::kBN) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] = n + e < there ? v[e] : 0.0f;
+        }
+        put_planes<D>(to + static_cast<uint32_t>(m) * pitch + n, l.z_plane, v);
+      },
+      [](int, int) { return 0; }, [](int, int, float (&)[8], int) {});
+}
+
 // dh (+)= dz w over a part of a piece.
 template <class C, int D>
-__global__ __launch_bounds__(C::kThreads)
-    __attribute__((amdgpu_waves_per_eu(C::kPerSimd, C::kPerSimd))) void
-    k_linear_dh(const LinearArgs l, const int parts, const bool hold) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds_[C::kLds];
-  auto *lds = (MTA_LDS uint8_t *)lds_;
-  const int64_t active = *l.active;
+__device__ __forceinline__ void make_dh(const LinearArgs &l,
+                                        const LinearPiece &piece,
+                                        const LinearBack &back, int64_t active,
+                                        uint32_t number,
+                                        MTA_LDS uint8_t *lds) {
+  const int parts = back.dh_parts;
   const uint32_t cols =
       static_cast<uint32_t>((l.a.width + C::kBN - 1) / C::kBN);
   const uint32_t tiles =
       static_cast<uint32_t>((active + C::kBM - 1) / C::kBM) * cols;
-  if (blockIdx.x >= tiles * parts) return;
-  const uint32_t block = beside(blockIdx.x, tiles * parts);
+  if (number >= tiles * parts) return;
+  const uint32_t block = beside(number, tiles * parts);
   const uint32_t part = block / tiles;
   uint32_t tm, tn;
   banded(block % tiles, tiles / cols, cols, tm, tn);
   const int64_t m0 = int64_t{tm} * C::kBM, n0 = int64_t{tn} * C::kBN;
-  const int64_t deep = (l.count + 63) / 64 * 64;
+  const int64_t deep = (piece.count + 63) / 64 * 64;
   const int64_t each = (deep / 64 + parts - 1) / parts * 64;
   const int64_t k0 = min(deep, part * each), k1 = min(deep, k0 + each);
   f32x16 acc[C::kRM][C::kRN];
-  const Operand z{l.z, l.z_plane, l.pitch_z, active, 0};
-  const Operand w{l.w + l.first * l.w_pitch, l.w_plane, l.w_pitch,
-                  (l.a.width + 7) / 8 * 8, l.count};
+  const Operand z{piece.z, l.z_plane, l.pitch_z, active, 0};
+  const Operand w{l.w + piece.first * l.w_pitch, l.w_plane, l.w_pitch,
+                  (l.a.width + 7) / 8 * 8, piece.count};
   tile_product<C, D == MTA_F16, kAlong, kAcross>(z, w, pairs_of(l.planes), m0,
                                                  n0, k0, k1, lds, acc);
   gradient_out<C, D>(
       l, lds, acc, m0, n0, active,
-      hold ? l.sum_h + part * l.a.rows * l.pitch : nullptr, l.first > 0, l.a.dh,
+      back.hold_dh ? l.sum_h + part * l.a.rows * l.pitch : nullptr, piece.first > 0, l.a.dh,
       l.a.lddh, 0, l.index, l.a.type, false);
 }
 
 // A piece of dw = dz^T h over a part of the rows.
 template <class C, int D>
-__global__ __launch_bounds__(C::kThreads)
-    __attribute__((amdgpu_waves_per_eu(C::kPerSimd, C::kPerSimd))) void
-    k_linear_dw(const LinearArgs l, const int parts, const bool hold) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds_[C::kLds];
-  auto *lds = (MTA_LDS uint8_t *)lds_;
-  const int64_t active = *l.active;
-  const uint32_t rows = static_cast<uint32_t>((l.count + C::kBM - 1) / C::kBM);
+__device__ __forceinline__ void make_dw(const LinearArgs &l,
+                                        const LinearPiece &piece,
+                                        const LinearBack &back, int64_t active,
+                                        uint32_t number,
+                                        MTA_LDS uint8_t *lds) {
+  const int parts = back.dw_parts;
+  const uint32_t rows = static_cast<uint32_t>((piece.count + C::kBM - 1) / C::kBM);
   const uint32_t cols =
       static_cast<uint32_t>((l.a.width + C::kBN - 1) / C::kBN);
-  const uint32_t block = beside(blockIdx.x, gridDim.x);
+  if (number >= rows * cols * parts) return;
+  const uint32_t block = beside(number, rows * cols * parts);
   const uint32_t part = block / (rows * cols);
   uint32_t tm, tn;
   banded(block % (rows * cols), rows, cols, tm, tn);
@@ -590,23 +612,43 @@ __global__ __launch_bounds__(C::kThreads)
   const int64_t each = (deep / 64 + parts - 1) / parts * 64;
   const int64_t k0 = min(deep, part * each), k1 = min(deep, k0 + each);
   f32x16 acc[C::kRM][C::kRN];
-  const Operand z{l.z, l.z_plane, l.pitch_z, (l.count + 63) / 64 * 64, deep};
+  const Operand z{piece.z, l.z_plane, l.pitch_z, (piece.count + 63) / 64 * 64, deep};
   const Operand h{l.h, l.h_plane, l.pitch, l.pitch, active};
   tile_product<C, D == MTA_F16, kAcross, kAcross>(z, h, pairs_of(l.planes), m0,
                                                   n0, k0, k1, lds, acc);
-  gradient_out<C, D>(l, lds, acc, m0, n0, l.count,
-                     hold ? l.sum_w + part * l.count * l.pitch : nullptr, false,
-                     l.a.dw, l.a.lddw, l.first, nullptr, l.a.dw_type,
+  gradient_out<C, D>(l, lds, acc, m0, n0, piece.count,
+                     back.hold_dw ? l.sum_w + part * piece.count * l.pitch : nullptr, false,
+                     l.a.dw, l.a.lddw, piece.first, nullptr, l.a.dw_type,
                      l.a.accumulate);
+}
+
+// dh and dw of a piece and dz of the next one, or any of them: none needs
+// another, and together they fill the compute units better than one after the
+// other (8192 rows of 1600 are 224 tiles of dh).  Long sums come first.
+template <class C, int D>
+__global__ __launch_bounds__(C::kThreads)
+    __attribute__((amdgpu_waves_per_eu(C::kPerSimd, C::kPerSimd))) void
+    k_linear_back(const LinearArgs l, const LinearPiece piece,
+                  const LinearPiece next, const LinearBack back) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds_[C::kLds];
+  auto *lds = (MTA_LDS uint8_t *)lds_;
+  const int64_t active = *l.active;
+  const uint32_t block = blockIdx.x;
+  if (block < back.first_dw)
+    make_dh<C, D>(l, piece, back, active, block, lds);
+  else if (block < back.first_dz)
+    make_dw<C, D>(l, piece, back, active, block - back.first_dw, lds);
+  else
+    make_dz<C, D>(l, next, active, block - back.first_dz, lds);
 }
 
 // Parts held in the workspace, joined in order and out.
 template <int D>
-__global__ __launch_bounds__(256) void k_linear_out(const LinearArgs l,
-                                                    const bool dh,
-                                                    const int parts) {
-  const int64_t rows = dh ? *l.active : l.count;
-  const int64_t step = (dh ? l.a.rows : l.count) * l.pitch;
+__global__ __launch_bounds__(256) void k_linear_out(
+    const LinearArgs l, const LinearPiece piece, const bool dh,
+    const int parts) {
+  const int64_t rows = dh ? *l.active : piece.count;
+  const int64_t step = (dh ? l.a.rows : piece.count) * l.pitch;
   const float *from = dh ? l.sum_h : l.sum_w;
   const int64_t runs = (l.a.width + 7) / 8;
   const float factor = shared_factor<D>(l);
@@ -628,7 +670,7 @@ __global__ __launch_bounds__(256) void k_linear_out(const LinearArgs l,
         put_out<decltype(t)::value>(l.a.dh, l.index[r] * l.a.lddh + i, many, false,
                                     factor, v);
       else
-        put_out<decltype(t)::value>(l.a.dw, (l.first + r) * l.a.lddw + i, many,
+        put_out<decltype(t)::value>(l.a.dw, (piece.first + r) * l.a.lddw + i, many,
                                     l.a.accumulate, factor, v);
     });
   }
@@ -649,12 +691,13 @@ uint32_t up(int64_t n, int64_t d) {
   return static_cast<uint32_t>((n + d - 1) / d);
 }
 
-// f(tile, type) for the run-time ones.
+// f(tile, type) for the run-time ones; a small tile's workgroups that are too few
+// for two on a CU get the deep one.
 template <typename F>
-void with_tile(const LinearCut &c, int type, F &&f) {
+void with_tile(int tile, uint32_t groups, int type, F &&f) {
   with_type(type, [&](auto t) {
-    if (c.tile == 256) f(Tile256{}, t);
-    else if (c.deep) f(TileDeep{}, t);
+    if (tile == 256) f(Tile256{}, t);
+    else if (groups <= 256) f(TileDeep{}, t);
     else f(Tile128{}, t);
   });
 }
@@ -693,13 +736,11 @@ hipError_t launch_linear_info(const LinearArgs &l, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_linear_logits(const LinearArgs &l, const LinearCut &c,
-                                hipStream_t s) {
-  with_tile(c, l.a.type, [&](auto tile, auto t) {
-    using C = decltype(tile);
-    k_linear_logits<C, decltype(t)::value>
-        <<<up(l.a.rows, C::kBM) * static_cast<uint32_t>(l.tiles), C::kThreads,
-           0, s>>>(l);
+hipError_t launch_linear_logits(const LinearArgs &l, int tile, hipStream_t s) {
+  const uint32_t grid = up(l.a.rows, tile) * static_cast<uint32_t>(l.tiles);
+  with_tile(tile, grid, l.a.type, [&](auto which, auto t) {
+    using C = decltype(which);
+    k_linear_logits<C, decltype(t)::value><<<grid, C::kThreads, 0, s>>>(l);
   });
   return hipGetLastError();
 }
@@ -713,34 +754,27 @@ hipError_t launch_linear_rows(const LinearArgs &l, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_linear_grad(const LinearArgs &l, const LinearCut &c,
+hipError_t launch_linear_back(const LinearArgs &l, int tile,
+                              const LinearPiece *piece,
+                              const LinearPiece *next, LinearBack back,
                               hipStream_t s) {
-  with_tile(c, l.a.type, [&](auto tile, auto t) {
-    using C = decltype(tile);
-    k_linear_grad<C, decltype(t)::value>
-        <<<up(l.a.rows, C::kBM) * up(l.count, C::kBN), C::kThreads, 0, s>>>(l);
-  });
-  return hipGetLastError();
-}
-
-hipError_t launch_linear_dh(const LinearArgs &l, const LinearCut &c, bool hold,
-                            hipStream_t s) {
-  with_tile(c, l.a.type, [&](auto tile, auto t) {
-    using C = decltype(tile);
-    k_linear_dh<C, decltype(t)::value>
-        <<<up(l.a.rows, C::kBM) * up(l.a.width, C::kBN) * c.parts, C::kThreads,
-           0, s>>>(l, c.parts, hold);
-  });
-  return hipGetLastError();
-}
-
-hipError_t launch_linear_dw(const LinearArgs &l, const LinearCut &c, bool hold,
-                            hipStream_t s) {
-  with_tile(c, l.a.type, [&](auto tile, auto t) {
-    using C = decltype(tile);
-    k_linear_dw<C, decltype(t)::value>
-        <<<up(l.count, C::kBM) * up(l.a.width, C::kBN) * c.parts, C::kThreads,
-           0, s>>>(l, c.parts, hold);
+  // (segments in wholes of eight, so that each begins on the first XCD)
+  const auto eight = [](uint32_t n) { return (n + 7) / 8 * 8; };
+  back.first_dw = back.first_dz = 0;
+  if (piece && l.a.dh)
+    back.first_dw = eight(up(l.a.rows, tile) * up(l.a.width, tile) *
+                          back.dh_parts);
+  back.first_dz = back.first_dw;
+  if (piece && l.a.dw)
+    back.first_dz += eight(up(piece->count, tile) * up(l.a.width, tile) *
+                           back.dw_parts);
+  uint32_t grid = back.first_dz;
+  if (next) grid += up(l.a.rows, tile) * up(next->count, tile);
+  const LinearPiece none{};
+  with_tile(tile, grid, l.a.type, [&](auto which, auto t) {
+    using C = decltype(which);
+    k_linear_back<C, decltype(t)::value><<<grid, C::kThreads, 0, s>>>(
+        l, piece ? *piece : none, next ? *next : none, back);
   });
   return hipGetLastError();
 }
@@ -750,13 +784,14 @@ hipError_t launch_linear_none(const LinearArgs &l, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_linear_out(const LinearArgs &l, bool dh, int parts,
-                             hipStream_t s) {
+hipError_t launch_linear_out(const LinearArgs &l, const LinearPiece &piece,
+                             bool dh, int parts, hipStream_t s) {
   const int64_t runs =
-      (dh ? l.a.rows : l.count) * ((l.a.width + 7) / 8);
+      (dh ? l.a.rows : piece.count) * ((l.a.width + 7) / 8);
   const uint32_t grid = std::min<uint32_t>(up(runs, 256), 1u << 20);
   with_type(l.a.type, [&](auto t) {
-    k_linear_out<decltype(t)::value><<<grid, 256, 0, s>>>(l, dh, parts);
+    k_linear_out<decltype(t)::value>
+        <<<grid, 256, 0, s>>>(l, piece, dh, parts);
   });
   return hipGetLastError();
 }

@@ -332,8 +332,9 @@ constexpr int64_t kMostPitch = int64_t{1} << 22;
 constexpr int64_t kMostRows = int64_t{1} << 30;
 // Workgroups of a launch.
 constexpr int64_t kMostGroups = int64_t{1} << 22;
-// dz of a piece of the vocabulary, at most, unless 256 columns need more.
-constexpr int64_t kPieceBytes = int64_t{256} << 20;
+// dz of a piece of the vocabulary, at most, unless 256 columns need more; there
+// are two.
+constexpr int64_t kPieceBytes = int64_t{128} << 20;
 
 // Whether the products can read w where it is.
 bool lies_well(const mta_linear_loss_args *a) {
@@ -341,39 +342,80 @@ bool lies_well(const mta_linear_loss_args *a) {
          a->ldw <= kMostPitch && aligned(a->w, 16);
 }
 
-// How a product of m x n outputs over k is dealt out.  In us, measured here: a
-// step of 64 of k takes the large tile 1.8 and two small ones that share a CU
-// 1.1, one alone 0.5; a workgroup's start and end 6 and 4; the joining of
-// parts 5 and their bytes at 4 TB/s.
-mta::LinearCut linear_cut(int64_t m, int64_t n, int64_t k, int runs, int most,
-                          int cus) {
-  mta::LinearCut best{};
-  double best_us = 0.0;
-  const int64_t steps = std::max<int64_t>(1, up(k, 64));
-  for (int tile : {256, 128}) {
-    const int64_t tiles = up(m, tile) * up(n, tile);
-    for (int64_t parts = 1; parts <= most; ++parts) {
-      if (parts > 1 && parts * 4 > steps) break;
-      const int64_t each = up(steps, parts);
-      const int64_t groups = tiles * parts;
-      const int64_t held = tile == 256 ? 1 : 2;
-      const double step = tile == 256 ? 1.8 : groups <= cus ? 0.5 : 1.1;
-      double us = static_cast<double>(up(groups, cus * held)) *
-                  (step * static_cast<double>(each * runs) +
-                   (tile == 256 ? 6.0 : 4.0));
-      if (parts > 1)
-        us += 5.0 + static_cast<double>(parts) * static_cast<double>(m) *
-                        static_cast<double>(n) * 8.0 / 4e6;
-      if (best.tile && us >= best_us) continue;
-      best_us = us;
-      best.tile = tile;
-      best.deep = groups <= cus;
-      best.parts = static_cast<int>(up(steps, each));
-      best.us = us;
-      if (groups > 8 * cus) break;
+// Times of workgroups in us, measured here: a step of 64 of k takes the large
+// tile 1.75 and two small ones that share a CU 1.1, a workgroup's start and end 6
+// and 4.
+struct TileTime {
+  double step, ends;
+  int64_t slots;  // workgroups at a time
+};
+TileTime tile_time(int tile, int64_t cus) {
+  return tile == 256 ? TileTime{1.75, 6.0, cus} : TileTime{1.1, 4.0, 2 * cus};
+}
+
+// The tile of a product that is a launch of its own.
+int lone_tile(int64_t m, int64_t n, int64_t k, int runs, int cus) {
+  double us[2];
+  for (int t = 0; t < 2; ++t) {
+    const int tile = t ? 128 : 256;
+    const TileTime x = tile_time(tile, cus);
+    us[t] = static_cast<double>(up(up(m, tile) * up(n, tile), x.slots)) *
+            (x.step * static_cast<double>(up(k, 64) * runs) + x.ends);
+  }
+  return us[0] <= us[1] ? 256 : 128;
+}
+
+// Pieces, tile and parts of the gradients' launches.  A launch has dh and dw of a
+// piece and dz of the next: it takes as long as its work on all CUs and, behind
+// that, about half of its longest workgroup, or as that one alone; held sums cost
+// their bytes at 4 TB/s.
+void plan_back(const mta_linear_loss_args *a, int runs, int64_t cus,
+               mta::LinearPlan *p) {
+  const auto real = [](int64_t x) { return static_cast<double>(x); };
+  const int64_t column = std::max<int64_t>(64, p->deep_rows) * 2 * p->planes;
+  const int64_t most = std::max<int64_t>(256, kPieceBytes / column / 256 * 256);
+  const int64_t least = up(a->vocab, most);
+  double best = 0.0;
+  for (int64_t n = least; n <= least + (least > 1 ? 2 : 0); ++n) {
+    const int64_t piece = n == 1 ? a->vocab : up(up(a->vocab, n), 256) * 256;
+    const int64_t pieces = up(a->vocab, piece);
+    for (int tile : {256, 128}) {
+      const TileTime x = tile_time(tile, cus);
+      const int64_t rows = up(a->rows, tile), cols = up(a->width, tile);
+      const int64_t high = up(piece, tile);
+      const double dz = real(up(a->width, 64) * runs) * x.step + x.ends;
+      for (int hp : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
+        if (hp > 1 && (!a->dh || hp * 4 > up(piece, 64))) break;
+        const double dh =
+            a->dh ? real(up(up(piece, 64), hp) * runs) * x.step + x.ends : 0.0;
+        for (int wp : {1, 2, 4, 8, 16, 32}) {
+          if (wp > 1 && (!a->dw || wp * 4 > up(a->rows, 64))) break;
+          const double dw =
+              a->dw ? real(up(up(a->rows, 64), wp) * runs) * x.step + x.ends
+                    : 0.0;
+          const double longest = std::max(std::max(dh, dw), dz);
+          const double work = real(rows * cols * hp) * dh +
+                              real(high * cols * wp) * dw +
+                              real(rows * high) * dz;
+          double us = std::max(work / real(x.slots) + longest / 2, longest);
+          const bool hold_h = a->dh && (pieces > 1 || hp > 1);
+          if (hold_h) us += real(hp * a->rows * p->pitch) * 8.0 / 4e6;
+          if (wp > 1) us += 5.0 + real(wp * piece * p->pitch) * 8.0 / 4e6;
+          us = us * real(pieces) + (hold_h ? 5.0 : 0.0);
+          if (best > 0.0 && us >= best) continue;
+          best = us;
+          p->piece = piece;
+          p->pieces = pieces;
+          p->back_tile = tile;
+          p->dh_parts = hp;
+          p->dw_parts = wp;
+        }
+      }
     }
   }
-  return best;
+  p->pitch_z = mta::plane_pitch(p->piece);
+  p->hold_dh = a->dh && (p->pieces > 1 || p->dh_parts > 1);
+  p->hold_dw = a->dw && p->dw_parts > 1;
 }
 
 mta::LinearPlan linear_plan(const mta_linear_loss_args *a, bool copy_w,
@@ -385,42 +427,15 @@ mta::LinearPlan linear_plan(const mta_linear_loss_args *a, bool copy_w,
   p.pitch = mta::plane_pitch(a->width);
   p.deep_rows = up(a->rows, 64) * 64;
   const bool grad = a->dh || a->dw;
-  p.logits = linear_cut(a->rows, a->vocab, a->width, runs, 1, cus);
-  if (grad) {
-    // As many pieces as keep dz within its bytes, or up to three more, if they
-    // fill the rounds of workgroups better.
-    const int64_t column = std::max<int64_t>(1, p.deep_rows) * 2 * p.planes;
-    const int64_t most =
-        std::max<int64_t>(256, kPieceBytes / column / 256 * 256);
-    const int64_t least = up(a->vocab, most);
-    double best = 0.0;
-    for (int64_t n = least; n <= least + (least > 1 ? 3 : 0); ++n) {
-      const int64_t piece =
-          n == 1 ? a->vocab : up(up(a->vocab, n), 256) * 256;
-      const auto grad = linear_cut(a->rows, piece, a->width, runs, 1, cus);
-      const auto dh = linear_cut(a->rows, a->width, piece, runs, 32, cus);
-      const auto dw = linear_cut(piece, a->width, a->rows, runs, 32, cus);
-      const double us = static_cast<double>(up(a->vocab, piece)) *
-                        (grad.us + (a->dh ? dh.us : 0.0) +
-                         (a->dw ? dw.us : 0.0));
-      if (n > least && us >= best) continue;
-      best = us;
-      p.piece = piece;
-      p.grad = grad;
-      p.dh = dh;
-      p.dw = dw;
-    }
-    p.pieces = up(a->vocab, p.piece);
-    p.pitch_z = mta::plane_pitch(p.piece);
-    p.hold_dh = a->dh && (p.pieces > 1 || p.dh.parts > 1);
-    p.hold_dw = a->dw && p.dw.parts > 1;
-  }
+  p.tile = lone_tile(a->rows, a->vocab, a->width, runs, cus);
+  if (grad) plan_back(a, runs, cus, &p);
   int64_t at = 0;
   const auto take = [&](int64_t bytes) {
     const int64_t here = at;
     at += up(bytes, 256) * 256;
     return here;
   };
+  const int64_t z = grad ? p.deep_rows * p.pitch_z * 2 * p.planes : 0;
   p.active = take(4);
   p.scalars = take(8);
   p.index = take(a->rows * 4);
@@ -428,12 +443,13 @@ mta::LinearPlan linear_plan(const mta_linear_loss_args *a, bool copy_w,
   p.terms = take(a->rows * 8);
   p.rows = take(a->rows * 16);
   p.z_target = take(a->rows * 4);
-  p.partial = take(up(a->vocab, p.logits.tile) * a->rows * 8);
+  p.partial = take(up(a->vocab, p.tile) * a->rows * 8);
   p.h = take(a->rows * p.pitch * 2 * p.planes);
   p.w = take(copy_w ? a->vocab * p.pitch * 2 * p.planes : 0);
-  p.z = take(grad ? p.deep_rows * p.pitch_z * 2 * p.planes : 0);
-  p.sum_h = take(p.hold_dh ? p.dh.parts * a->rows * p.pitch * 4 : 0);
-  p.sum_w = take(p.hold_dw ? p.dw.parts * p.piece * p.pitch * 4 : 0);
+  p.z[0] = take(z);
+  p.z[1] = p.pieces > 1 ? take(z) : p.z[0];
+  p.sum_h = take(p.hold_dh ? p.dh_parts * a->rows * p.pitch * 4 : 0);
+  p.sum_w = take(p.hold_dw ? p.dw_parts * p.piece * p.pitch * 4 : 0);
   p.bytes = at;
   return p;
 }
@@ -540,7 +556,6 @@ hipError_t run_linear(const mta_linear_loss_args *a, const mta::LinearPlan &p,
   l.z_target = reinterpret_cast<float *>(ws + p.z_target);
   l.partial = reinterpret_cast<float2 *>(ws + p.partial);
   l.h = reinterpret_cast<uint16_t *>(ws + p.h);
-  l.z = reinterpret_cast<uint16_t *>(ws + p.z);
   l.sum_h = reinterpret_cast<float *>(ws + p.sum_h);
   l.sum_w = reinterpret_cast<float *>(ws + p.sum_w);
   l.planes = p.planes;
@@ -549,7 +564,7 @@ hipError_t run_linear(const mta_linear_loss_args *a, const mta::LinearPlan &p,
   l.pitch_z = p.pitch_z;
   l.h_plane = a->rows * p.pitch;
   l.z_plane = p.deep_rows * p.pitch_z;
-  l.tiles = up(a->vocab, p.logits.tile);
+  l.tiles = up(a->vocab, p.tile);
   hipError_t e;
   const auto ok = [&](hipError_t x) { return (e = x) == hipSuccess; };
   if (!ok(mta::launch_linear_rows_in(l, s))) return e;
@@ -567,23 +582,34 @@ hipError_t run_linear(const mta_linear_loss_args *a, const mta::LinearPlan &p,
     }
   }
   if (!backward) {
-    if (a->rows > 0 && !ok(mta::launch_linear_logits(l, p.logits, s))) return e;
+    if (a->rows > 0 && !ok(mta::launch_linear_logits(l, p.tile, s))) return e;
     if (!ok(mta::launch_linear_rows(l, s))) return e;
   }
   if (!a->dh && !a->dw) return e;
   if (a->rows == 0) return a->dw ? mta::launch_linear_none(l, s) : e;
   if (!ok(mta::launch_linear_info(l, s))) return e;
+  const auto piece = [&](int64_t k) {
+    const int64_t first = k * p.piece;
+    return mta::LinearPiece{first, std::min(p.piece, a->vocab - first),
+                            reinterpret_cast<uint16_t *>(ws + p.z[k % 2])};
+  };
+  const mta::LinearBack back{p.dh_parts, p.dw_parts, p.hold_dh, p.hold_dw, 0,
+                             0};
+  mta::LinearPiece here, next = piece(0);
+  if (!ok(mta::launch_linear_back(l, p.back_tile, nullptr, &next, back, s)))
+    return e;
   for (int64_t k = 0; k < p.pieces; ++k) {
-    l.first = k * p.piece;
-    l.count = std::min(p.piece, a->vocab - l.first);
-    if (!ok(mta::launch_linear_grad(l, p.grad, s))) return e;
-    if (a->dh && !ok(mta::launch_linear_dh(l, p.dh, p.hold_dh, s))) return e;
-    if (!a->dw) continue;
-    if (!ok(mta::launch_linear_dw(l, p.dw, p.hold_dw, s))) return e;
-    if (p.hold_dw && !ok(mta::launch_linear_out(l, false, p.dw.parts, s)))
+    here = next;
+    const bool more = k + 1 < p.pieces;
+    if (more) next = piece(k + 1);
+    if (!ok(mta::launch_linear_back(l, p.back_tile, &here,
+                                    more ? &next : nullptr, back, s)))
+      return e;
+    if (p.hold_dw &&
+        !ok(mta::launch_linear_out(l, here, false, p.dw_parts, s)))
       return e;
   }
-  if (p.hold_dh) e = mta::launch_linear_out(l, true, p.dh.parts, s);
+  if (p.hold_dh) e = mta::launch_linear_out(l, here, true, p.dh_parts, s);
   return e;
 }
 

@@ -165,15 +165,6 @@ hipError_t launch_ortho_product(int step, int tile, bool deep,
 
 static_assert(sizeof(mta_linear_row) == 16, "saved row layout");
 
-// One product of a call: its tile and into how many parts of k it is cut, whose
-// sums a second kernel joins.
-struct LinearCut {
-  int tile;
-  bool deep;  // no CU gets a second workgroup of the small tile
-  int parts;
-  double us;  // estimated
-};
-
 // The course of a call.
 struct LinearPlan {
   int planes;
@@ -183,11 +174,13 @@ struct LinearPlan {
   int64_t pieces;
   int64_t pitch_z;      // of dz
   int64_t deep_rows;    // rows of dz, at most: whole steps of 64
-  LinearCut logits, grad, dh, dw;
+  int tile;             // of the forward's product
+  int back_tile;        // of the others
+  int dh_parts, dw_parts;  // of k, whose sums are joined
   bool hold_dh, hold_dw;  // sums held in the workspace before they go out
   // offsets in the workspace
-  int64_t active, scalars, terms, rows, index, info, z_target, partial, h, w, z,
-      sum_h, sum_w, bytes;
+  int64_t active, scalars, terms, rows, index, info, z_target, partial, h, w,
+      z[2], sum_h, sum_w, bytes;
 };
 
 // What dz takes of a row, besides the factor that all rows share.
@@ -212,14 +205,25 @@ struct LinearArgs {
   float2 *partial;        // [tiles][rows]: largest, sum without the target
   uint16_t *h;            // planes
   const uint16_t *w;
-  uint16_t *z;            // planes of a piece of dz
   float *sum_h, *sum_w;   // [parts][rows or piece][pitch]
   int64_t h_plane, w_plane, w_pitch, z_plane;
   int64_t pitch, pitch_z;
-  int64_t first, count;   // the piece
   int64_t tiles;          // of the vocabulary
   int planes;
   int backward;           // rows are the caller's, and say what is left out
+};
+
+// A piece of the vocabulary, and its dz.
+struct LinearPiece {
+  int64_t first, count;
+  uint16_t *z;  // planes
+};
+
+// The parts of dh's and dw's sums, whether they are held in the workspace, and
+// the first workgroups of dw and of dz.
+struct LinearBack {
+  int dh_parts, dw_parts, hold_dh, hold_dw;
+  uint32_t first_dw, first_dz;
 };
 
 hipError_t launch_linear_rows_in(const LinearArgs &l, hipStream_t s);
@@ -227,19 +231,18 @@ hipError_t launch_linear_info(const LinearArgs &l, hipStream_t s);
 hipError_t launch_linear_pack_h(const LinearArgs &l, hipStream_t s);
 hipError_t launch_linear_pack_w(const LinearArgs &l, uint16_t *to,
                                 hipStream_t s);
-hipError_t launch_linear_logits(const LinearArgs &l, const LinearCut &c,
-                                hipStream_t s);
+hipError_t launch_linear_logits(const LinearArgs &l, int tile, hipStream_t s);
 hipError_t launch_linear_rows(const LinearArgs &l, hipStream_t s);
-hipError_t launch_linear_grad(const LinearArgs &l, const LinearCut &c,
+// dh and dw of `piece` and dz of `next`, either of which may be null.  Held dh is
+// added to what is there after the first piece.
+hipError_t launch_linear_back(const LinearArgs &l, int tile,
+                              const LinearPiece *piece,
+                              const LinearPiece *next, LinearBack back,
                               hipStream_t s);
-// hold: into sum_h (added to what is there after the first piece)
-hipError_t launch_linear_dh(const LinearArgs &l, const LinearCut &c, bool hold,
-                            hipStream_t s);
-hipError_t launch_linear_dw(const LinearArgs &l, const LinearCut &c, bool hold,
-                            hipStream_t s);
 // dw of no rows
 hipError_t launch_linear_none(const LinearArgs &l, hipStream_t s);
-hipError_t launch_linear_out(const LinearArgs &l, bool dh, int parts,
-                             hipStream_t s);
+// what is held, out
+hipError_t launch_linear_out(const LinearArgs &l, const LinearPiece &piece,
+                             bool dh, int parts, hipStream_t s);
 
 }  // namespace mta
