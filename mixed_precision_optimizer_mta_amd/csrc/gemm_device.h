@@ -183,7 +183,7 @@ __device__ __forceinline__ void tile_product(
   constexpr int kSlots = kM > kReads ? kM : kReads;
   const int tid = threadIdx.x, lane = tid % 64;
   const int wave = __builtin_amdgcn_readfirstlane(tid / 64);
-  const int wr = wave / C::kWC, wc = wave % C::kWC;
+  const int wr = wave % C::kWR, wc = wave / C::kWR;
 
 #pragma unroll
   for (int i = 0; i < C::kRM; ++i)
@@ -268,6 +268,35 @@ __device__ __forceinline__ void tile_product(
       to_lds(lb, off_b[j < C::kNA ? 0 : j - C::kNA],
              stage + C::kBM * C::kBK * 2 + (j - C::kNA) * C::kThreads * 16);
   };
+
+  // A wave whose outputs lie behind the last row or column only brings its share
+  // of the operands.  (Waves that share a SIMD lie far apart in n, so that a
+  // tile with few columns left uses all SIMDs: 1600 columns are 6.25 tiles.)
+  const int64_t high = a.extent - m0, wide = b.extent - n0;
+  if (wr * C::kTM >= high || wc * C::kTN >= wide) {
+#pragma unroll
+    for (int s = 0; s < C::kST - 1; ++s) {
+      aim();
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) load1(lds0 + s * C::kStage, j);
+    }
+    __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(kPer * (C::kST - 2))
+                     : "memory");
+    __builtin_amdgcn_s_barrier();
+    int cur = 0;
+    for (int s = 0; s < steps; ++s) {
+      const int far = cur == 0 ? C::kST - 1 : cur - 1;
+      aim();
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) load1(lds0 + far * C::kStage, j);
+      __asm__ volatile("s_waitcnt vmcnt(%0)" ::"n"(kPer * (C::kST - 2))
+                       : "memory");
+      __builtin_amdgcn_s_barrier();
+      cur = cur + 1 == C::kST ? 0 : cur + 1;
+    }
+    __asm__ volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    return;
+  }
 
   uint32_t at_a[kR], at_b[kR];
 #pragma unroll
@@ -368,7 +397,7 @@ __device__ __forceinline__ void tile_out(
   static_assert(C::kWR * C::kWC * 16384 <= C::kLds, "the staging fits");
   const int lane = threadIdx.x % 64;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  const int m_at = wave / C::kWC * C::kTM, n_at = wave % C::kWC * C::kTN;
+  const int m_at = wave % C::kWR * C::kTM, n_at = wave / C::kWR * C::kTN;
   // rows of 16 chunks of four, turned by the row so that no two lanes of a
   // write, and none of a read, meet in a bank
   auto *mine = (MTA_LDS float *)(lds + wave * 16384);

@@ -263,7 +263,7 @@ __global__ __launch_bounds__(C::kThreads)
 
   const int lane = threadIdx.x % 64;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  const int wr = wave / C::kWC, wc = wave % C::kWC;
+  const int wr = wave % C::kWR, wc = wave / C::kWR;
   auto *side = (MTA_LDS f32x2 *)lds;  // [WC][BM]
   // columns of this lane: n1 + 32 j + 8 q + e
   const int64_t n1 = n0 + wc * C::kTN + lane / 32 * 4;
