@@ -65,13 +65,16 @@ typedef struct {
  * the others alone; one of zeros comes out zero.
  *
  * A matrix of up to 64 rows or columns is computed in float64.  Otherwise X is
- * kept as a float16 value and a second one for what it leaves (22 bits), A and B
- * as such values and their diagonals in float32; sums are float32.  With
- * `precise` all products are those of 22 bits, three float16 products each.
- * Without, products are of the first values alone, one product each, the
- * diagonals apart: off by 2e-4 to 1.1e-3 of the result's root mean square.
+ * kept as a float16 value and a second one for what it leaves (22 bits), the
+ * symmetric matrices as such values and their diagonals in float32; sums are
+ * float32, and two steps may be taken as one product (Q' Q) X.  With `precise`
+ * all products are those of 22 bits, three float16 products each.  Without,
+ * products are of the first values alone, one product each, the diagonals apart:
+ * off by 2e-4 to 1.1e-3 of the result's root mean square, up to 2.5e-3 where the
+ * singular values span five decades.
  * The coefficients have to keep every singular value in [0, 1] below 7 from
- * step to step (MTA_EINVAL). */
+ * step to step and may not let one grow to 100 times itself in a step
+ * (MTA_EINVAL). */
 typedef struct {
   const mta_ortho_matrix *matrices;
   int64_t count;

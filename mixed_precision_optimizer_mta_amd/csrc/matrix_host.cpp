@@ -24,6 +24,17 @@ long long ll(int64_t x) { return static_cast<long long>(x); }
 
 int64_t up(int64_t n, int64_t d) { return (n + d - 1) / d; }
 
+// Times of workgroups in us, measured here: a step of 64 of k takes the large
+// tile 1.75 and two small ones that share a CU 1.1, a workgroup's start and end 6
+// and 4.
+struct TileTime {
+  double step, ends;
+  int64_t slots;  // workgroups at a time
+};
+TileTime tile_time(int tile, int64_t cus) {
+  return tile == 256 ? TileTime{1.75, 6.0, cus} : TileTime{1.1, 4.0, 2 * cus};
+}
+
 // ---- orthogonalised updates ---------------------------------------------
 
 int check_ortho_sizes(const mta_ortho_args *a) {
@@ -44,23 +55,28 @@ int check_ortho_sizes(const mta_ortho_args *a) {
   return MTA_OK;
 }
 
-// Whether every singular value of [0, 1] stays below 7 over the steps, so that
-// what is kept in float16 stays finite.
-bool bounded(const double *c, int steps) {
+// Whether every singular value of [0, 1] stays below 7 over the steps and grows
+// to less than 100 times itself in one, so that what is kept in float16 stays
+// finite; *pairs: in two of them, too.
+bool bounded(const double *c, int steps, bool *pairs) {
   // (those that are usual, without another look)
   constexpr double kUsual[3] = {3.4445, -4.7750, 2.0315};
   bool usual = true;
   for (int k = 0; k < 3 * steps; ++k) usual = usual && c[k] == kUsual[k % 3];
+  *pairs = true;
   if (usual) return true;
   for (int k = 0; k < 3 * steps; ++k)
     if (!std::isfinite(c[k])) return false;
   constexpr int kPoints = 512;
-  for (int i = 1; i <= kPoints; ++i) {
-    double x = static_cast<double>(i) / kPoints;
+  for (int i = 0; i <= kPoints; ++i) {
+    double x = static_cast<double>(i) / kPoints, before = 1.0;
     for (int s = 0; s < steps; ++s) {
       const double q = x * x;
-      x *= c[3 * s] + q * (c[3 * s + 1] + q * c[3 * s + 2]);
-      if (!(std::fabs(x) < 7.0)) return false;
+      const double f = c[3 * s] + q * (c[3 * s + 1] + q * c[3 * s + 2]);
+      x *= f;
+      if (!(std::fabs(x) < 7.0) || !(std::fabs(f) < 100.0)) return false;
+      if (s % 2 && !(std::fabs(f * before) < 100.0)) *pairs = false;
+      before = f;
     }
   }
   return true;
@@ -74,9 +90,11 @@ int check_ortho(const mta_ortho_args *a) {
   if (a->steps < 1 || a->steps > MTA_ORTHO_STEPS)
     return fail(MTA_EINVAL, "steps must be in [1, %d]", MTA_ORTHO_STEPS);
   if (!a->coefficients) return fail(MTA_EINVAL, "coefficients is NULL");
-  if (!bounded(a->coefficients, a->steps))
+  bool pairs;
+  if (!bounded(a->coefficients, a->steps, &pairs))
     return fail(MTA_EINVAL,
-                "the coefficients let a singular value of [0, 1] grow to 7");
+                "the coefficients let a singular value of [0, 1] grow to 7, or "
+                "to 100 times itself in a step");
   if (!std::isfinite(a->eps) || a->eps < 0.0)
     return fail(MTA_EINVAL, "eps must be finite and >= 0 (got %g)", a->eps);
   if (a->nesterov != 0 && a->nesterov != 1)
@@ -144,7 +162,7 @@ int check_ortho(const mta_ortho_args *a) {
 int64_t ortho_tiles(int step, int64_t rows, int64_t cols, int64_t tile) {
   const int64_t m = up(std::min(rows, cols), tile);
   const int64_t n = up(std::max(rows, cols), tile);
-  return step == mta::kOrthoGram || step == mta::kOrthoSquare ? m * (m + 1) / 2
+  return step == mta::kOrthoGram || step == mta::kOrthoTimes ? m * (m + 1) / 2
                                                               : m * n;
 }
 
@@ -219,6 +237,8 @@ std::vector<OrthoGroup> ortho_groups(const mta_ortho_args *a) {
 hipError_t run_ortho(const mta_ortho_args *a,
                      const std::vector<OrthoGroup> &groups, int cus,
                      hipStream_t s) {
+  bool pairs = false;
+  bounded(a->coefficients, a->steps, &pairs);
   hipError_t e = hipSuccess;
   mta::OrthoCall c{};
   c.d_coef = a->d_coef;
@@ -281,16 +301,35 @@ hipError_t run_ortho(const mta_ortho_args *a,
              up(mta::plane_pitch(std::max(r, n)), mta::kOrthoLoadTile);
     });
     if ((e = mta::launch_ortho_load(l, c, s)) != hipSuccess) return e;
+    // Each kind of product's tile, and its time in us.
+    const int runs = mta::pair_count(c.planes);
+    int tile[4];
+    double us[4];
+    for (int step = 0; step < 4; ++step) {
+      for (int t : {256, 128}) {
+        const TileTime x = tile_time(t, cus);
+        double longest = 0.0, work = 0.0;
+        for (uint32_t k = 0; k < l.count; ++k) {
+          const int64_t rows = l.item[k].rows, cols = l.item[k].cols;
+          const int64_t n = ortho_tiles(step, rows, cols, t);
+          const int64_t deep = step == mta::kOrthoGram ? std::max(rows, cols)
+                                                       : std::min(rows, cols);
+          const int cuts = step == mta::kOrthoGram ? g.cuts : 1;
+          const double one =
+              static_cast<double>(up(up(deep, 64), cuts) * runs) * x.step +
+              x.ends + (cuts > 1 ? 6.0 : 0.0);
+          work += static_cast<double>(n * cuts) * one;
+          longest = std::max(longest, one);
+        }
+        const double all =
+            std::max(work / static_cast<double>(x.slots) + longest / 2, longest);
+        if (t == 128 && all >= us[step]) continue;
+        us[step] = all;
+        tile[step] = t;
+      }
+    }
     const auto product = [&](int step) {
-      // The large tile takes a CU for as long as 1.8 small ones, two of which
-      // share one: whichever needs less.
-      int64_t n[2] = {0, 0};
-      for (uint32_t k = 0; k < l.count; ++k)
-        for (int t = 0; t < 2; ++t)
-          n[t] += ortho_tiles(step, l.item[k].rows, l.item[k].cols,
-                              t ? 256 : 128);
-      const int tile =
-          up(n[1], cus) * 18 <= up(n[0], 2 * cus) * 10 ? 256 : 128;
+      const int t = tile[step];
       if (step == mta::kOrthoGram && g.cuts > 1) {
         deal([&](int64_t r, int64_t m) {
           return ortho_tiles(step, r, m, 128) * g.cuts;
@@ -301,22 +340,47 @@ hipError_t run_ortho(const mta_ortho_args *a,
         deal([&](int64_t r, int64_t m) { return ortho_tiles(step, r, m, 64); });
         return mta::launch_ortho_join(l, c, s);
       }
-      deal([&](int64_t r, int64_t m) { return ortho_tiles(step, r, m, tile); });
+      deal([&](int64_t r, int64_t m) { return ortho_tiles(step, r, m, t); });
       return mta::launch_ortho_product(
-          step, tile, l.first[l.count] <= static_cast<uint32_t>(cus), l, c, s);
+          step, t, l.first[l.count] <= static_cast<uint32_t>(cus), l, c, s);
     };
+    // buffer `out` = e0 P Q + e1 P + e2
+    const auto times = [&](int p, int q, int out, double e0, double e1,
+                           double e2) {
+      c.p = p;
+      c.q = q;
+      c.out = out;
+      c.e0 = static_cast<float>(e0);
+      c.e1 = static_cast<float>(e1);
+      c.e2 = static_cast<float>(e2);
+      return product(mta::kOrthoTimes);
+    };
+    // Two steps at once where that takes less: one product over the columns of
+    // either kind less and three of small matrices more (and a launch).
+    const bool by_two =
+        pairs && us[mta::kOrthoGram] + us[mta::kOrthoNext] >
+                     3.0 * us[mta::kOrthoTimes] + 5.0;
+    const int blocks = by_two ? (a->steps + 1) / 2 : a->steps;
     c.which = 0;
-    for (int k = 0; k < a->steps; ++k) {
-      c.a = static_cast<float>(a->coefficients[3 * k]);
-      c.b = static_cast<float>(a->coefficients[3 * k + 1]);
-      c.c = static_cast<float>(a->coefficients[3 * k + 2]);
-      const bool last = k + 1 == a->steps;
-      c.whole = k + 2 >= a->steps;
+    for (int k = 0, block = 0; k < a->steps; ++block) {
+      const double *co = a->coefficients + 3 * k;
+      const bool two = by_two && k + 1 < a->steps;
       if ((e = product(mta::kOrthoGram)) != hipSuccess) return e;
-      if ((e = product(mta::kOrthoSquare)) != hipSuccess) return e;
-      if ((e = product(last ? mta::kOrthoLast : mta::kOrthoNext)) !=
-          hipSuccess)
-        return e;
+      if ((e = times(0, 0, 1, co[2], co[1], co[0])) != hipSuccess) return e;
+      double rest = co[0];
+      if (two) {
+        if ((e = times(0, 1, 2, 1, 0, 0)) != hipSuccess) return e;
+        if ((e = times(2, 1, 0, 1, 0, 0)) != hipSuccess) return e;
+        if ((e = times(0, 0, 2, co[5], co[4], co[3])) != hipSuccess) return e;
+        if ((e = times(2, 1, 0, 1, 0, 0)) != hipSuccess) return e;
+        rest *= co[3];
+      }
+      k += two ? 2 : 1;
+      c.out = two ? 0 : 1;
+      c.rest = static_cast<float>(rest);
+      c.whole = block + 2 >= blocks;
+      const int step = k < a->steps ? mta::kOrthoNext : mta::kOrthoLast;
+      if ((e = product(step)) != hipSuccess) return e;
       c.which = 1 - c.which;
     }
   }
@@ -341,17 +405,6 @@ constexpr int64_t kPieceBytes = int64_t{160} << 20;
 bool lies_well(const mta_linear_loss_args *a) {
   return a->type != MTA_F32 && a->width % 64 == 0 && a->ldw % 8 == 0 &&
          a->ldw <= kMostPitch && aligned(a->w, 16);
-}
-
-// Times of workgroups in us, measured here: a step of 64 of k takes the large
-// tile 1.75 and two small ones that share a CU 1.1, a workgroup's start and end 6
-// and 4.
-struct TileTime {
-  double step, ends;
-  int64_t slots;  // workgroups at a time
-};
-TileTime tile_time(int tile, int64_t cus) {
-  return tile == 256 ? TileTime{1.75, 6.0, cus} : TileTime{1.1, 4.0, 2 * cus};
 }
 
 // The tile of a product that is a launch of its own.

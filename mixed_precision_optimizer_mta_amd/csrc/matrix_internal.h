@@ -57,12 +57,17 @@ struct OrthoCall {
   double eps;
   float mu;
   float decay;  // of w
-  float a, b, c;  // of the step
+  // a product of two symmetric matrices: e0 P Q + e1 P + e2, of the buffers
+  // number p, q and out
+  float e0, e1, e2;
+  int p, q, out;
+  // X from buffer `out`; what is left of X behind its first plane is multiplied
+  // by its diagonal too (whole), or by `rest`
+  float rest;
   int type, out_type, copy_type, nesterov;
   int planes;   // of a product's operands: 2 with `precise`
   int cuts;     // parts of k that A is summed in
-  int whole;    // the diagonal times all digits of X, not those of the first
-                // plane alone
+  int whole;
   int which;    // the X that is read; the other one is written
 };
 static_assert(sizeof(OrthoList) + sizeof(OrthoCall) +
@@ -98,12 +103,13 @@ __host__ __device__ inline OrthoSmallSpace ortho_small_space(int64_t rows,
   return s;
 }
 
-// A matrix's part of the workspace: two X of `planes` planes each, A and B,
-// their diagonals, the partial sums of squares.
+// A matrix's part of the workspace: two X of two planes each, three symmetric
+// matrices of `planes` planes, their diagonals, the partial sums of squares.
+constexpr int kOrthoSquares = 3;
 struct OrthoSpace {
   int64_t small, large, pitch_x, pitch_a;
   int64_t plane_x, plane_a;          // elements
-  // offsets in bytes, and from the first of two to the second
+  // offsets in bytes, and from the first to the next
   int64_t x, next_x, a, next_a, diag, next_diag, part, bytes;
   int64_t cut;  // partial sums of A: [cuts][small][pitch_a] floats
 };
@@ -121,9 +127,9 @@ __host__ __device__ inline OrthoSpace ortho_space(int64_t rows, int64_t cols,
   s.next_x = round(s.plane_x * 2 * 2);
   s.a = s.x + 2 * s.next_x;
   s.next_a = round(s.plane_a * planes * 2);
-  s.diag = s.a + 2 * s.next_a;
+  s.diag = s.a + kOrthoSquares * s.next_a;
   s.next_diag = round(s.pitch_a * 4);  // zeros behind the last
-  s.part = s.diag + 2 * s.next_diag;
+  s.part = s.diag + kOrthoSquares * s.next_diag;
   s.cut = s.part + kOrthoParts * 8;
   s.bytes = s.cut + (cuts > 1 ? round(cuts * s.plane_a * 4) : 0);
   return s;
@@ -133,7 +139,7 @@ __host__ __device__ inline OrthoSpace ortho_space(int64_t rows, int64_t cols,
 // After a Gram product in parts: 64 x 64 of A, and what mirrors it.
 hipError_t launch_ortho_join(const OrthoList &l, const OrthoCall &c,
                              hipStream_t s);
-enum OrthoStep { kOrthoGram, kOrthoSquare, kOrthoNext, kOrthoLast };
+enum OrthoStep { kOrthoGram, kOrthoTimes, kOrthoNext, kOrthoLast };
 constexpr int kOrthoLoadTile = 64;
 // Workgroups that sum a matrix's squares: 64 elements a lane, as long as they
 // are few enough for one read of their sums by every workgroup that follows.

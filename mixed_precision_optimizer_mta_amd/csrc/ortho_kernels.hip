@@ -1,25 +1,29 @@
 // ortho_kernels.hip -- the orthogonalised update of the Muon rule on the matrix
 // cores of gfx950, for the matrices of a list together.
 //
-//   X = u / (|u| + eps);  steps times  A = X X^T,  B = b A + c A A,  X = a X + B X
+//   X = u / (|u| + eps);  steps times  X = Q X,  Q = a + b R + c R R,  R = X X^T
 //
 // u is the gradient or its momentum, X the one with fewer rows than columns of
-// u and its transpose.  Each step is three products, one launch each over the
-// tiles of all matrices: A and A A are symmetric, so tiles below the diagonal
-// are copies.
+// u and its transpose.  One launch a product, over the tiles of all matrices;
+// those of symmetric matrices are computed on and right of the diagonal and
+// copied.  X of many columns is read and written once for two steps: the second
+// one's R is Q R Q, and (Q' Q) X its result, five products of small matrices in
+// the place of one of each kind over the columns.  (Three steps at once, or all
+// of them, would not do in 16 bits: an eigenvalue of R that rounding has made
+// negative grows by a^2 = 12 a step.)
 //
 // Which digits are kept.  Small singular values grow by a = 3.4 in a step and
 // gradients have many: with X in bfloat16 the result is off by 1.3% of its norm
 // for normal entries and by 32% where four directions stand out a thousandfold,
 // whatever the products' sums.  X is therefore kept in 22 bits, as the sum of
 // two float16 values (scaled by 2^13, so that 1/sqrt(rows cols) and its rest are
-// normal numbers), and the term a X uses them all.  The products take the first
-// values alone.  What hurts then is that B's diagonal, -2.6 of rows that have
-// converged, is rounded with the rest of it: diagonals are kept in float32 apart
-// and enter as e_i X_i, and the error falls from 2.9e-3 to 4.5e-4 (512 x 2048
-// normal entries).  In the first steps e_i multiplies the rounded X that A was
-// made from, so that small directions cancel as they do in A (from 3.3e-3 to
-// 6.8e-4 where eight directions stand out); in the last two the whole X.  With
+// normal numbers).  The products take the first values alone.  What hurts then
+// is that Q's diagonal, 1 of rows that have converged but -2.6 + 3.4, is rounded
+// with the rest: diagonals are kept in float32 apart and enter as d_i X_i, and
+// the error falls from 2.9e-3 to 4.5e-4 (512 x 2048 normal entries).  In the
+// first steps the diagonal's part of R multiplies the rounded X that R was made
+// from, so that small directions cancel as they do in R (from 3.3e-3 to 6.8e-4
+// where eight directions stand out); in the last two products the whole X.  With
 // `precise` every product is of both values: 4e-7.
 #include "gemm_device.h"
 #include "ortho_device.h"
@@ -28,8 +32,8 @@ namespace mta {
 namespace {
 
 // Powers of two that the float16 values are multiplied by: room for singular
-// values of 7 in X, of 49 in A and a multiple of that in B.
-constexpr float kScaleX = 8192.0f, kScaleA = 1024.0f, kScaleB = 512.0f;
+// values of 7 in X and of 100 in the symmetric matrices.
+constexpr float kScaleX = 8192.0f, kScaleA = 512.0f;
 
 // Eight values as float16, and with Two what their roundings leave as a second
 // eight (an infinity leaves a NaN: its matrix is lost anyway).
@@ -129,8 +133,9 @@ __global__ __launch_bounds__(256) void k_ortho_load(const OrthoList l,
   const bool skip = c.amp && c.amp->found_inf != 0.0f;
   const bool tall = it.rows > it.cols;
   if (blockIdx.x == l.first[k])
-    for (int64_t i = sp.small + threadIdx.x; i < sp.pitch_a; i += 256)
-      reinterpret_cast<float *>(it.ws + sp.diag)[i] = 0.0f;
+    for (int n = 0; n < kOrthoSquares; ++n)
+      for (int64_t i = sp.small + threadIdx.x; i < sp.pitch_a; i += 256)
+        reinterpret_cast<float *>(it.ws + sp.diag + n * sp.next_diag)[i] = 0.0f;
   const uint32_t t = blockIdx.x - l.first[k];
   const uint32_t wide = static_cast<uint32_t>(sp.pitch_x) / kT;
   const int64_t m0 = int64_t{t / wide} * kT, n0 = int64_t{t % wide} * kT;
@@ -275,7 +280,7 @@ __global__ __launch_bounds__(C::kThreads)
   const OrthoItem &it = l.item[k];
   const OrthoSpace sp = ortho_space(it.rows, it.cols, Planes, c.cuts);
   const uint32_t t = block - l.first[k];
-  constexpr bool kSym = Step == kOrthoGram || Step == kOrthoSquare;
+  constexpr bool kSym = Step == kOrthoGram || Step == kOrthoTimes;
   constexpr bool kTwo = Planes > 1;
   const uint32_t side = static_cast<uint32_t>(sp.small + C::kBM - 1) / C::kBM;
   const uint32_t part = Step == kOrthoGram ? t % c.cuts : 0;
@@ -293,10 +298,12 @@ __global__ __launch_bounds__(C::kThreads)
   const int64_t m0 = int64_t{tm} * C::kBM, n0 = int64_t{tn} * C::kBN;
   auto *x_old =
       reinterpret_cast<uint16_t *>(it.ws + sp.x + c.which * sp.next_x);
-  auto *pa = reinterpret_cast<uint16_t *>(it.ws + sp.a);
-  auto *pb = reinterpret_cast<uint16_t *>(it.ws + sp.a + sp.next_a);
-  auto *da = reinterpret_cast<float *>(it.ws + sp.diag);
-  auto *db = reinterpret_cast<float *>(it.ws + sp.diag + sp.next_diag);
+  const auto square = [&](int n) {
+    return reinterpret_cast<uint16_t *>(it.ws + sp.a + n * sp.next_a);
+  };
+  const auto diagonal = [&](int n) {
+    return reinterpret_cast<float *>(it.ws + sp.diag + n * sp.next_diag);
+  };
   const Pairs pairs = pairs_of(Planes);
   const int64_t deep_x = (sp.large + 63) / 64 * 64;
   const int64_t deep_a = (sp.small + 63) / 64 * 64;
@@ -312,8 +319,9 @@ __global__ __launch_bounds__(C::kThreads)
       tile_product<C, true, kAlong, kAlong>(x, x, pairs, m0, n0, k0,
                                             min(deep_x, k0 + each), lds, acc);
     } else {
-      const Operand a{pa, sp.plane_a, sp.pitch_a, sp.small, sp.small};
-      tile_product<C, true, kAlong, kAlong>(a, a, pairs, m0, n0, 0, deep_a, lds,
+      const Operand p{square(c.p), sp.plane_a, sp.pitch_a, sp.small, sp.small};
+      const Operand q{square(c.q), sp.plane_a, sp.pitch_a, sp.small, sp.small};
+      tile_product<C, true, kAlong, kAlong>(p, q, pairs, m0, n0, 0, deep_a, lds,
                                             acc);
     }
     float *cut = Step == kOrthoGram && c.cuts > 1
@@ -323,36 +331,38 @@ __global__ __launch_bounds__(C::kThreads)
     // from the tile's corner, and from its mirror image's, in 32 bits a lane
     const uint32_t pitch = static_cast<uint32_t>(sp.pitch_a);
     const int cols = static_cast<int>(min(sp.pitch_a - n0, int64_t{C::kBN}));
-    uint16_t *to = Step == kOrthoGram ? pa : pb;
-    float *diag = Step == kOrthoGram ? da : db;
-    uint16_t *here = to + m0 * sp.pitch_a + n0;
-    uint16_t *there = to + n0 * sp.pitch_a + m0;
-    const uint16_t *seen = pa + m0 * sp.pitch_a + n0;
+    const int out = Step == kOrthoGram ? 0 : c.out;
+    uint16_t *to = square(out);
+    float *diag = diagonal(out);
+    const int64_t corner = m0 * sp.pitch_a + n0;
+    uint16_t *here = to + corner, *there = to + n0 * sp.pitch_a + m0;
+    const uint16_t *at_p = square(c.p) + corner, *at_q = square(c.q) + corner;
+    const float *diag_p = diagonal(c.p), *diag_q = diagonal(c.q);
     // the tile holds a part of the diagonal, or a last column
     const bool edge = tm == tn || tn + 1 == side;
     struct Seen {
-      Raw8<MTA_F16> hi, lo;
+      Raw8<MTA_F16> p, q, p_lo, q_lo;
       float row;
       Raw8<MTA_F32> col;
     };
-    // B, in units of kScaleB, of A = D + O with D its diagonal:
-    // A A = O O + D O + O D + D D
-    const float to_o = c.b * (kScaleB / kScaleA);
-    const float to_do = c.c * (kScaleB / kScaleA);
-    const float to_oo = c.c * (kScaleB / (kScaleA * kScaleA));
+    // With P = D + O, Q = E + N and D, E their diagonals:
+    // P Q = O N + D N + O E + D E, in units of kScaleA
     tile_out<C, true>(
         lds, acc, true, tm != tn && !cut,
         [&](int m, int n) {
           Seen x;
-          if constexpr (Step == kOrthoSquare) {
+          if constexpr (Step == kOrthoTimes) {
             m = min(m, rows - 1);
             n = min(n, cols - 8);
             const uint32_t at = static_cast<uint32_t>(m) * pitch + n;
-            x.hi = load8<MTA_F16, false>(seen + at, 0);
-            if constexpr (kTwo)
-              x.lo = load8<MTA_F16, false>(seen + at + sp.plane_a, 0);
-            x.row = da[m0 + m];
-            x.col = load8<MTA_F32, false>(da + n0, n);
+            x.p = load8<MTA_F16, false>(at_p + at, 0);
+            x.q = load8<MTA_F16, false>(at_q + at, 0);
+            if constexpr (kTwo) {
+              x.p_lo = load8<MTA_F16, false>(at_p + at + sp.plane_a, 0);
+              x.q_lo = load8<MTA_F16, false>(at_q + at + sp.plane_a, 0);
+            }
+            x.row = diag_p[m0 + m];
+            x.col = load8<MTA_F32, false>(diag_q + n0, n);
           }
           return x;
         },
@@ -372,22 +382,26 @@ __global__ __launch_bounds__(C::kThreads)
             for (int e = 0; e < 8; ++e)
               v[e] *= kScaleA / (kScaleX * kScaleX);
           } else {
-            const float of_row = __builtin_fmaf(to_do, x.row, to_o);
+            const float of_q = c.e0 * x.row;
             const int64_t own = m0 + m - (n0 + n);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              float o = x.hi[e];
-              if constexpr (kTwo) o += x.lo[e];
-              const float f = __builtin_fmaf(to_do, x.col[e], of_row);
-              float y = __builtin_fmaf(f, o, v[e] * to_oo);
-              // (O is 0 there, and the diagonal's own)
+              float o = x.p[e], r = x.q[e];
+              if constexpr (kTwo) {
+                o += x.p_lo[e];
+                r += x.q_lo[e];
+              }
+              const float of_p = __builtin_fmaf(c.e0, x.col[e], c.e1);
+              float y = __builtin_fmaf(
+                  of_p, o,
+                  __builtin_fmaf(of_q, r, v[e] * (c.e0 / kScaleA)));
+              // (O and N are 0 there)
               if (edge && e == own)
-                y += kScaleB * (x.row * (c.b + c.c * x.row));
+                y += kScaleA * __builtin_fmaf(of_p, x.row, c.e2);
               v[e] = y;
             }
           }
           if (edge) {
-            constexpr float kTo = Step == kOrthoGram ? kScaleA : kScaleB;
             const int64_t own = m0 + m - (n0 + n);
             const int64_t left = sp.small - (n0 + n);
             float d = 0.0f;
@@ -396,7 +410,7 @@ __global__ __launch_bounds__(C::kThreads)
               d = e == own ? v[e] : d;
               v[e] = e == own || e >= left ? 0.0f : v[e];
             }
-            if (own >= 0 && own < 8) diag[m0 + m] = d * (1.0f / kTo);
+            if (own >= 0 && own < 8) diag[m0 + m] = d * (1.0f / kScaleA);
           }
           store_planes<kTwo>(here + at, sp.plane_a, v);
         },
@@ -408,7 +422,8 @@ __global__ __launch_bounds__(C::kThreads)
           store_planes<kTwo>(there + at, sp.plane_a, v);
         });
   } else {
-    const Operand b{pb, sp.plane_a, sp.pitch_a, sp.small, sp.small};
+    const Operand b{square(c.out), sp.plane_a, sp.pitch_a, sp.small, sp.small};
+    const float *diag = diagonal(c.out);
     tile_product<C, true, kAlong, kAcross>(
         b, Operand{x_old, sp.plane_x, sp.pitch_x, sp.pitch_x, sp.small}, pairs,
         m0, n0, 0, deep_a, lds, acc);
@@ -434,18 +449,17 @@ __global__ __launch_bounds__(C::kThreads)
           const uint32_t at = static_cast<uint32_t>(m) * pitch + n;
           return Seen{load8<MTA_F16, false>(from + at, 0),
                       load8<MTA_F16, false>(from + at + sp.plane_x, 0),
-                      db[m0 + m]};
+                      diag[m0 + m]};
         },
         [&](int m, int n, float (&v)[8], const Seen &x) {
           if (m >= rows || n >= cols) return;
-          // a X + e X, the second one of the first values alone at first
-          const float of_hi = (c.a + x.diag) * kTo;
-          const float of_lo = kTwo || c.whole ? of_hi : c.a * kTo;
+          const float of_hi = x.diag * kTo;
+          const float of_lo = kTwo || c.whole ? of_hi : c.rest * kTo;
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             v[e] = __builtin_fmaf(
                 of_hi, x.hi[e],
-                __builtin_fmaf(of_lo, x.lo[e], v[e] * (kTo / kScaleB)));
+                __builtin_fmaf(of_lo, x.lo[e], v[e] * (kTo / kScaleA)));
           if constexpr (Step == kOrthoNext)
             store_planes<true>(to + static_cast<uint32_t>(m) * pitch + n,
                                sp.plane_x, v);
@@ -470,7 +484,7 @@ hipError_t start(int step, const OrthoList &l, const OrthoCall &c,
   };
   switch (step) {
     case kOrthoGram: return go(std::integral_constant<int, kOrthoGram>{});
-    case kOrthoSquare: return go(std::integral_constant<int, kOrthoSquare>{});
+    case kOrthoTimes: return go(std::integral_constant<int, kOrthoTimes>{});
     case kOrthoNext: return go(std::integral_constant<int, kOrthoNext>{});
     default: return go(std::integral_constant<int, kOrthoLast>{});
   }
