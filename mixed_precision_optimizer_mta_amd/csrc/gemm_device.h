@@ -55,6 +55,7 @@ struct Tile {
   static constexpr int kLds = kStage * ST;
   static_assert(kNA * kThreads * 8 == BM * BK, "whole loads");
   static_assert(kNB * kThreads * 8 == BN * BK, "whole loads");
+  static_assert(BM >= 64 && BN >= 64, "a turn stays in a row of LDS");
 };
 
 // One operand: planes of 16-bit elements, `plane` elements apart, rows of ld.
@@ -126,8 +127,8 @@ struct Slab {
   static __device__ __forceinline__ int turn(int row) {
     if constexpr (L == kAlong)
       return kChunks == 8 ? (row >> 1) & 7 : (row >> 2) & 3;
-    else
-      return (row & 3) << 2;
+    else  // (rows of 64 are half the banks)
+      return kChunks == 8 ? (row & 2) << 1 : (row & 3) << 2;
   }
   // Row and first element of chunk number q of the slab.
   static __device__ __forceinline__ int row_of(int q) { return q / kChunks; }
@@ -379,7 +380,7 @@ __device__ __forceinline__ void tile_product(
   __asm__ volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
 }
 
-// The sums through LDS, 64 rows and 64 columns of a wave at a time, to
+// The sums through LDS, up to 64 rows of a wave's columns at a time, to
 //   emit(m, n, v, x)    eight columns n .. n + 7 of a row, where `direct`
 //   turned(n, m, v, x)  eight rows m .. m + 7 of a column, where `mirror`: with
 //                       Fold what emit has made of them
@@ -392,51 +393,59 @@ template <class C, bool Fold, class Look, class Emit, class Ahead, class Turned>
 __device__ __forceinline__ void tile_out(
     MTA_LDS uint8_t *lds, const f32x16 (&acc)[C::kRM][C::kRN], bool direct,
     bool mirror, Look &&look, Emit &&emit, Ahead &&ahead, Turned &&turned) {
-  constexpr int kBlocks = C::kTM / 64;
-  static_assert(C::kTM % 64 == 0 && C::kTN == 64, "wholes of 64 x 64");
-  static_assert(C::kWR * C::kWC * 16384 <= C::kLds, "the staging fits");
+  constexpr int kH = C::kTM < 64 ? C::kTM : 64, kW = C::kTN;  // at a time
+  constexpr int kBlocks = C::kTM / kH, kChunks = kW / 4;
+  // lanes beside each other in a row (a column), rows (columns) of a turn, turns
+  constexpr int kAlongRow = kW / 8, kRows = 64 / kAlongRow, kTurns = kH / kRows;
+  constexpr int kAlongCol = kH / 8, kCols = 64 / kAlongCol,
+                kTurnsCol = kW / kCols;
+  constexpr int kWave = kH * kW * 4;
+  static_assert(C::kTM % kH == 0 && kTurns % 2 == 0 && kTurnsCol % 2 == 0,
+                "whole turns");
+  static_assert(C::kWR * C::kWC * kWave <= C::kLds, "the staging fits");
   const int lane = threadIdx.x % 64;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const int m_at = wave % C::kWR * C::kTM, n_at = wave / C::kWR * C::kTN;
-  // rows of 16 chunks of four, turned by the row so that no two lanes of a
-  // write, and none of a read, meet in a bank
-  auto *mine = (MTA_LDS float *)(lds + wave * 16384);
+  // rows of chunks of four, turned by the row so that lanes of a write or a
+  // read meet in few banks
+  auto *mine = (MTA_LDS float *)(lds + wave * kWave);
   const auto chunk = [&](int m, int c) {
-    return (MTA_LDS f32x4 *)(mine + m * 64 + ((c ^ (m & 15)) * 4));
+    return (MTA_LDS f32x4 *)(mine + m * kW + ((c ^ (m & (kChunks - 1))) * 4));
   };
   // so many turns' memory is on its way (sums that wait for the second 64 rows
   // leave fewer registers)
   constexpr int kAhead =
-      C::kTM > 64 && sizeof(decltype(look(0, 0))) > 48 ? 2 : 4;
+      kTurns < 4 || (kBlocks > 1 && sizeof(decltype(look(0, 0))) > 48) ? 2 : 4;
+  constexpr int kAheadCol = kTurnsCol < 4 ? 2 : 4;
   decltype(look(0, 0)) seen[kAhead];
+  const int m = lane / kAlongRow, n = lane % kAlongRow * 8;
   if (direct) {
 #pragma unroll
     for (int p = 0; p < kAhead; ++p)
-      seen[p] = look(m_at + p * 8 + lane / 8, n_at + lane % 8 * 8);
+      seen[p] = look(m_at + p * kRows + m, n_at + n);
   }
   __syncthreads();
 #pragma unroll 1
   for (int b = 0; b < kBlocks; ++b) {
-    const int m_b = m_at + b * 64;
+    const int m_b = m_at + b * kH;
 #pragma unroll
     for (int i = 0; i < C::kRM; ++i) {
-      if (i / 2 != b) continue;
+      if (i / (kH / 32) != b) continue;
 #pragma unroll
       for (int j = 0; j < C::kRN; ++j)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          *chunk(i % 2 * 32 + lane % 32, j * 8 + q * 2 + lane / 32) =
+          *chunk(i % (kH / 32) * 32 + lane % 32, j * 8 + q * 2 + lane / 32) =
               f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1],
                     acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]};
     }
     __builtin_amdgcn_wave_barrier();
     if (direct) {
-      const int m = lane / 8, n = lane % 8 * 8;
 #pragma unroll 1
-      for (int h = 0; h < 8; h += kAhead) {
+      for (int h = 0; h < kTurns; h += kAhead) {
 #pragma unroll
         for (int p = 0; p < kAhead; ++p) {
-          const int row = (h + p) * 8 + m;
+          const int row = (h + p) * kRows + m;
           const f32x4 f = *chunk(row, n / 4);
           const f32x4 g = *chunk(row, n / 4 + 1);
           float v[8] = {f[0], f[1], f[2], f[3], g[0], g[1], g[2], g[3]};
@@ -445,30 +454,29 @@ __device__ __forceinline__ void tile_out(
             *chunk(row, n / 4) = f32x4{v[0], v[1], v[2], v[3]};
             *chunk(row, n / 4 + 1) = f32x4{v[4], v[5], v[6], v[7]};
           }
-          // (past the end: the next 64 rows)
-          seen[p] = look(m_b + row + kAhead * 8, n_at + n);
+          // (past the end: the next rows)
+          seen[p] = look(m_b + row + kAhead * kRows, n_at + n);
         }
       }
       __builtin_amdgcn_wave_barrier();
     }
     if (mirror) {
-      // 8 columns, eight runs of eight rows each
-      const int n = lane / 8, m = lane % 8 * 8;
-      decltype(ahead(0, 0)) seen[kAhead];
+      const int across = lane / kAlongCol, down = lane % kAlongCol * 8;
+      decltype(ahead(0, 0)) next[kAheadCol];
 #pragma unroll
-      for (int p = 0; p < kAhead; ++p)
-        seen[p] = ahead(n_at + p * 8 + n, m_b + m);
+      for (int p = 0; p < kAheadCol; ++p)
+        next[p] = ahead(n_at + p * kCols + across, m_b + down);
 #pragma unroll 1
-      for (int h = 0; h < 8; h += kAhead) {
+      for (int h = 0; h < kTurnsCol; h += kAheadCol) {
 #pragma unroll
-        for (int p = 0; p < kAhead; ++p) {
-          const int at = (h + p) * 8 + n;
+        for (int p = 0; p < kAheadCol; ++p) {
+          const int at = (h + p) * kCols + across;
           float v[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            v[e] = ((MTA_LDS float *)chunk(m + e, at / 4))[at % 4];
-          turned(n_at + at, m_b + m, v, seen[p]);
-          seen[p] = ahead(n_at + at + kAhead * 8, m_b + m);
+            v[e] = ((MTA_LDS float *)chunk(down + e, at / 4))[at % 4];
+          turned(n_at + at, m_b + down, v, next[p]);
+          next[p] = ahead(n_at + at + kAheadCol * kCols, m_b + down);
         }
       }
     }
@@ -500,5 +508,7 @@ __device__ __forceinline__ void banded(uint32_t t, uint32_t rows, uint32_t cols,
 using Tile256 = Tile<256, 256, 2, 4, 32, 4, 2>;
 using Tile128 = Tile<128, 128, 2, 2, 64, 2, 2>;
 using TileDeep = Tile<128, 128, 2, 2, 64, 4, 1>;
+// For products that would leave CUs without a tile.
+using Tile64 = Tile<64, 64, 2, 2, 64, 4, 2>;
 
 }  // namespace mta

@@ -697,6 +697,7 @@ template <typename F>
 void with_tile(int tile, uint32_t groups, int type, F &&f) {
   with_type(type, [&](auto t) {
     if (tile == 256) f(Tile256{}, t);
+    else if (tile == 64) f(Tile64{}, t);
     else if (groups <= 256) f(TileDeep{}, t);
     else f(Tile128{}, t);
   });

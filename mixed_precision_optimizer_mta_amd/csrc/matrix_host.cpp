@@ -25,14 +25,24 @@ long long ll(int64_t x) { return static_cast<long long>(x); }
 int64_t up(int64_t n, int64_t d) { return (n + d - 1) / d; }
 
 // Times of workgroups in us, measured here: a step of 64 of k takes the large
-// tile 1.75 and two small ones that share a CU 1.1, a workgroup's start and end 6
-// and 4.
+// tile 1.75, two of 128 that share a CU 1.1 and one alone 0.58, two of 64 0.5 and
+// one alone 0.3; a workgroup's start and end 6, 4 and 3.
+// Tiles of 64 read each operand twice as often: they are taken only where all of
+// them run at once.
+constexpr int kTiles[3] = {256, 128, 64};
+bool too_many(int tile, int64_t groups, int64_t cus) {
+  return tile == 64 && groups > 2 * cus;
+}
 struct TileTime {
   double step, ends;
   int64_t slots;  // workgroups at a time
 };
-TileTime tile_time(int tile, int64_t cus) {
-  return tile == 256 ? TileTime{1.75, 6.0, cus} : TileTime{1.1, 4.0, 2 * cus};
+TileTime tile_time(int tile, int64_t groups, int64_t cus) {
+  const bool shared = groups > cus;
+  if (tile == 256) return TileTime{1.75, 6.0, cus};
+  if (tile == 128)
+    return TileTime{shared ? 1.1 : 0.58, 4.0, shared ? 2 * cus : cus};
+  return TileTime{shared ? 0.5 : 0.3, 3.0, shared ? 2 * cus : cus};
 }
 
 // ---- orthogonalised updates ---------------------------------------------
@@ -306,24 +316,33 @@ hipError_t run_ortho(const mta_ortho_args *a,
     int tile[4];
     double us[4];
     for (int step = 0; step < 4; ++step) {
-      for (int t : {256, 128}) {
-        const TileTime x = tile_time(t, cus);
+      us[step] = 0.0;
+      for (int t : kTiles) {
+        const int cuts = step == mta::kOrthoGram ? g.cuts : 1;
+        if (cuts > 1 && t != 128) continue;
+        int64_t groups = 0;
+        for (uint32_t k = 0; k < l.count; ++k)
+          groups += ortho_tiles(step, l.item[k].rows, l.item[k].cols, t) * cuts;
+        if (too_many(t, groups, cus)) continue;
+        const TileTime x = tile_time(t, groups, cus);
         double longest = 0.0, work = 0.0;
         for (uint32_t k = 0; k < l.count; ++k) {
           const int64_t rows = l.item[k].rows, cols = l.item[k].cols;
-          const int64_t n = ortho_tiles(step, rows, cols, t);
           const int64_t deep = step == mta::kOrthoGram ? std::max(rows, cols)
                                                        : std::min(rows, cols);
-          const int cuts = step == mta::kOrthoGram ? g.cuts : 1;
           const double one =
               static_cast<double>(up(up(deep, 64), cuts) * runs) * x.step +
               x.ends + (cuts > 1 ? 6.0 : 0.0);
-          work += static_cast<double>(n * cuts) * one;
+          work += static_cast<double>(ortho_tiles(step, rows, cols, t) * cuts) *
+                  one;
           longest = std::max(longest, one);
         }
         const double all =
-            std::max(work / static_cast<double>(x.slots) + longest / 2, longest);
-        if (t == 128 && all >= us[step]) continue;
+            groups <= x.slots
+                ? longest
+                : std::max(work / static_cast<double>(x.slots) + longest / 2,
+                           longest);
+        if (us[step] > 0.0 && all >= us[step]) continue;
         us[step] = all;
         tile[step] = t;
       }
@@ -394,7 +413,8 @@ constexpr int64_t kMostVocab = int64_t{1} << 28;
 constexpr int64_t kMostWidth = int64_t{1} << 20;
 constexpr int64_t kMostPitch = int64_t{1} << 22;
 constexpr int64_t kMostRows = int64_t{1} << 30;
-// Workgroups of a launch.
+// Workgroups of a launch, for each of its parts (of 128 x 128 at least: smaller
+// ones are taken where there are few).
 constexpr int64_t kMostGroups = int64_t{1} << 22;
 // A plane of dz of a piece of the vocabulary, at most, unless 256 columns need
 // more; there are two pieces.  (With twice as much 8192 x 1600 x 50257 takes 1.3%
@@ -409,14 +429,19 @@ bool lies_well(const mta_linear_loss_args *a) {
 
 // The tile of a product that is a launch of its own.
 int lone_tile(int64_t m, int64_t n, int64_t k, int runs, int cus) {
-  double us[2];
-  for (int t = 0; t < 2; ++t) {
-    const int tile = t ? 128 : 256;
-    const TileTime x = tile_time(tile, cus);
-    us[t] = static_cast<double>(up(up(m, tile) * up(n, tile), x.slots)) *
-            (x.step * static_cast<double>(up(k, 64) * runs) + x.ends);
+  int best = 0;
+  double best_us = 0.0;
+  for (int tile : kTiles) {
+    const int64_t groups = up(m, tile) * up(n, tile);
+    if (too_many(tile, groups, cus)) continue;
+    const TileTime x = tile_time(tile, groups, cus);
+    const double us = static_cast<double>(up(groups, x.slots)) *
+                      (x.step * static_cast<double>(up(k, 64) * runs) + x.ends);
+    if (best && us >= best_us) continue;
+    best = tile;
+    best_us = us;
   }
-  return us[0] <= us[1] ? 256 : 128;
+  return best;
 }
 
 // Pieces, tile and parts of the gradients' launches.  A launch has dh and dw of a
@@ -433,17 +458,21 @@ void plan_back(const mta_linear_loss_args *a, int runs, int64_t cus,
   for (int64_t n = least; n <= least + (least > 1 ? 2 : 0); ++n) {
     const int64_t piece = n == 1 ? a->vocab : up(up(a->vocab, n), 256) * 256;
     const int64_t pieces = up(a->vocab, piece);
-    for (int tile : {256, 128}) {
-      const TileTime x = tile_time(tile, cus);
+    for (int tile : kTiles) {
       const int64_t rows = up(a->rows, tile), cols = up(a->width, tile);
       const int64_t high = up(piece, tile);
-      const double dz = real(up(a->width, 64) * runs) * x.step + x.ends;
       for (int hp : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
         if (hp > 1 && (!a->dh || hp * 4 > up(piece, 64))) break;
-        const double dh =
-            a->dh ? real(up(up(piece, 64), hp) * runs) * x.step + x.ends : 0.0;
         for (int wp : {1, 2, 4, 8, 16, 32}) {
           if (wp > 1 && (!a->dw || wp * 4 > up(a->rows, 64))) break;
+          const int64_t groups = rows * (a->dh ? cols * hp : 0) + rows * high +
+                                 (a->dw ? high * cols * wp : 0);
+          if (too_many(tile, groups, cus)) break;
+          const TileTime x = tile_time(tile, groups, cus);
+          const double dz = real(up(a->width, 64) * runs) * x.step + x.ends;
+          const double dh =
+              a->dh ? real(up(up(piece, 64), hp) * runs) * x.step + x.ends
+                    : 0.0;
           const double dw =
               a->dw ? real(up(up(a->rows, 64), wp) * runs) * x.step + x.ends
                     : 0.0;
@@ -451,7 +480,10 @@ void plan_back(const mta_linear_loss_args *a, int runs, int64_t cus,
           const double work = real(rows * cols * hp) * dh +
                               real(high * cols * wp) * dw +
                               real(rows * high) * dz;
-          double us = std::max(work / real(x.slots) + longest / 2, longest);
+          double us =
+              groups <= x.slots
+                  ? longest
+                  : std::max(work / real(x.slots) + longest / 2, longest);
           const bool hold_h = a->dh && (pieces > 1 || hp > 1);
           if (hold_h) us += real(hp * a->rows * p->pitch) * 8.0 / 4e6;
           if (wp > 1) us += 5.0 + real(wp * piece * p->pitch) * 8.0 / 4e6;

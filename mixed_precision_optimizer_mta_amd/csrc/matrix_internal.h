@@ -162,7 +162,7 @@ hipError_t launch_ortho_small_factor(const OrthoList &l, const OrthoCall &c,
                                      const OrthoCoefficients &k, hipStream_t s);
 hipError_t launch_ortho_small_apply(const OrthoList &l, const OrthoCall &c,
                                     hipStream_t s);
-// tile: 256 or 128; deep: no CU gets a second workgroup
+// tile: 256, 128 or 64; deep: no CU gets a second workgroup
 hipError_t launch_ortho_product(int step, int tile, bool deep,
                                 const OrthoList &l,
                                 const OrthoCall &c, hipStream_t s);

@@ -522,9 +522,11 @@ hipError_t launch_ortho_join(const OrthoList &l, const OrthoCall &c,
   return hipGetLastError();
 }
 
-hipError_t launch_ortho_product(int step, int tile, bool deep, const OrthoList &l,
-                                const OrthoCall &c, hipStream_t s) {
+hipError_t launch_ortho_product(int step, int tile, bool deep,
+                                const OrthoList &l, const OrthoCall &c,
+                                hipStream_t s) {
   if (tile == 256) return start<Tile256>(step, l, c, s);
+  if (tile == 64) return start<Tile64>(step, l, c, s);
   return deep ? start<TileDeep>(step, l, c, s) : start<Tile128>(step, l, c, s);
 }
 
