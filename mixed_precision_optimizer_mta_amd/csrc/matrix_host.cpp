@@ -223,9 +223,10 @@ std::vector<OrthoGroup> ortho_groups(const mta_ortho_args *a) {
     groups.back().bytes += bytes;
   }
   // Few tiles of A with long sums are cut along k, eight steps of 64 a part at
-  // least, to about two workgroups for each of 256 compute units (the workspace
+  // least, to about one workgroup for each of 256 compute units (the workspace
   // does not depend on the device): 256 x 6400 79 us a product, now 12 and 5
-  // for the joining of its parts.
+  // for the joining of its parts.  Two for each were slower: an update of
+  // matrices with 252 tiles of A takes 601 us so and 575 uncut.
   for (OrthoGroup &g : groups) {
     if (g.small) continue;
     int64_t tiles = 0, steps = 0;
@@ -235,7 +236,7 @@ std::vector<OrthoGroup> ortho_groups(const mta_ortho_args *a) {
       steps = std::max(steps, up(std::max(m.rows, m.cols), 64));
     }
     g.cuts = static_cast<int>(std::clamp<int64_t>(
-        std::min(512 / tiles, steps * (a->precise ? 3 : 1) / 8), 1, 32));
+        std::min(256 / tiles, steps * (a->precise ? 3 : 1) / 8), 1, 32));
     if (g.cuts == 1) continue;
     g.bytes = 0;
     for (int64_t i : g.index)
