@@ -77,9 +77,13 @@ bool bounded(const double *c, int steps, bool *pairs) {
   if (usual) return true;
   for (int k = 0; k < 3 * steps; ++k)
     if (!std::isfinite(c[k])) return false;
-  constexpr int kPoints = 512;
-  for (int i = 0; i <= kPoints; ++i) {
-    double x = static_cast<double>(i) / kPoints, before = 1.0;
+  // evenly, and down to 2^-32, 16 points an octave: the smallest ones come to
+  // any place in later steps
+  constexpr int kEven = 512, kFine = 512;
+  for (int i = 0; i <= kEven + kFine; ++i) {
+    double x = i <= kEven ? static_cast<double>(i) / kEven
+                          : std::exp2((kEven - i) / 16.0);
+    double before = 1.0;
     for (int s = 0; s < steps; ++s) {
       const double q = x * x;
       const double f = c[3 * s] + q * (c[3 * s + 1] + q * c[3 * s + 2]);
@@ -92,7 +96,7 @@ bool bounded(const double *c, int steps, bool *pairs) {
   return true;
 }
 
-int check_ortho(const mta_ortho_args *a) {
+int check_ortho(const mta_ortho_args *a, bool *pairs) {
   int rc = check_ortho_sizes(a);
   if (rc) return rc;
   if (!known_type(a->type) || !known_type(a->out_type))
@@ -100,8 +104,7 @@ int check_ortho(const mta_ortho_args *a) {
   if (a->steps < 1 || a->steps > MTA_ORTHO_STEPS)
     return fail(MTA_EINVAL, "steps must be in [1, %d]", MTA_ORTHO_STEPS);
   if (!a->coefficients) return fail(MTA_EINVAL, "coefficients is NULL");
-  bool pairs;
-  if (!bounded(a->coefficients, a->steps, &pairs))
+  if (!bounded(a->coefficients, a->steps, pairs))
     return fail(MTA_EINVAL,
                 "the coefficients let a singular value of [0, 1] grow to 7, or "
                 "to 100 times itself in a step");
@@ -246,10 +249,8 @@ std::vector<OrthoGroup> ortho_groups(const mta_ortho_args *a) {
 }
 
 hipError_t run_ortho(const mta_ortho_args *a,
-                     const std::vector<OrthoGroup> &groups, int cus,
-                     hipStream_t s) {
-  bool pairs = false;
-  bounded(a->coefficients, a->steps, &pairs);
+                     const std::vector<OrthoGroup> &groups, bool pairs,
+                     int cus, hipStream_t s) {
   hipError_t e = hipSuccess;
   mta::OrthoCall c{};
   c.d_coef = a->d_coef;
@@ -758,13 +759,14 @@ int mta_orthogonalize(const mta_ortho_args *a, void *stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = hipSuccess;
   try {
-    int rc = check_ortho(a);
+    bool pairs = false;
+    int rc = check_ortho(a, &pairs);
     if (rc) return rc;
     const std::vector<OrthoGroup> groups = ortho_groups(a);
     if (groups.empty()) return ok();
     int cus = 0;
     if ((rc = current_cus(&cus))) return rc;
-    e = run_ortho(a, groups, cus, s);
+    e = run_ortho(a, groups, pairs, cus, s);
   } catch (const std::bad_alloc &) {
     return fail(MTA_ENOMEM, "host allocation failed");
   }

@@ -8,6 +8,10 @@ memory: the ``loss_scale`` of a loss-scaled MtaOptimizer, which its step divides
 out again.  ``linear_cross_entropy_forward`` and
 ``linear_cross_entropy_backward`` are the two halves, and
 ``linear_cross_entropy`` is both as an autograd function.
+
+All of them may be captured into a HIP graph; as for the checkpoints' functions,
+a backward pass is captured whole, together with its forward and with no graph
+of an earlier eager forward over the same parameters still alive.
 """
 from collections import namedtuple
 

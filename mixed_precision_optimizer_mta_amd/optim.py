@@ -274,9 +274,10 @@ class MtaOptimizer(torch.optim.Optimizer):
     def _merge_sig(self):
         """The parameter sets the current hyperparameters allow: for each
         group, (index of the first group of its set, its weight decay is
-        0).  A group of kind "muon" is a set of its own.  Groups with equal lr, betas, eps and momentum form one set when
-        at most one nonzero weight decay appears among them; otherwise each
-        of them is a set of its own."""
+        0).  A group of kind "muon" is a set of its own.  Groups with equal
+        lr, betas, eps and momentum form one set when at most one nonzero
+        weight decay appears among them; otherwise each of them is a set of
+        its own."""
         keys, nonzero = [], {}
         for g in self.param_groups:
             key = (float(g["lr"]), tuple(float(b) for b in g["betas"]),

@@ -116,6 +116,23 @@ def test_orthogonalize_refuses(matrix, kw, code):
     assert M.mta_last_error() != ""
 
 
+def test_orthogonalize_refuses_what_only_small_values_reach():
+    """Twelve steps and three more bring whatever begins above 1/512 to 1,
+    where the last polynomial, 60 (x^2 - 1)^2, is 0; smaller ones come to
+    0.447, where it makes 17 of them."""
+    co = [(3.4445, -4.7750, 2.0315)] * 12 + [(1.875, -1.25, 0.375)] * 3 + \
+        [(60.0, -120.0, 60.0)]
+    flat = [v for row in co for v in row]
+    x = [k / 512 for k in range(1, 513)]
+    for a, b, c in co:
+        x = [v * (a + b * v * v + c * v ** 4) for v in x]
+        assert max(map(abs, x)) < 7
+    args = ortho()
+    args.steps, args.coefficients = 16, (ctypes.c_double * 48)(*flat)
+    assert _code(B.mta_orthogonalize, args) == -1
+    assert "coefficients" in M.mta_last_error()
+
+
 def test_orthogonalize_refuses_shared_outputs_of_a_list():
     far = {k: GOOD[k] + (1 << 20) for k in ("g", "m", "out", "w", "w16")}
     assert _code(B.mta_orthogonalize,
