@@ -38,6 +38,16 @@ __device__ __forceinline__ bool left_out(const LinearArgs &l, int64_t r) {
          (l.a.weights && l.a.weights[r] == 0.0f);
 }
 
+// How many rows take part, the weight of a row without weights and the largest.
+__device__ __forceinline__ void put_counts(const LinearArgs &l, int all,
+                                           float most) {
+  const float one =
+      all > 0 ? static_cast<float>(1.0 / static_cast<double>(all)) : 0.0f;
+  l.scalars[0] = one;
+  l.scalars[1] = l.backward || l.a.weights ? most : one;
+  *l.active = all;
+}
+
 // The rows that take part, in order, their number, the weight of a row without
 // weights and the largest magnitude of any: one workgroup, a run of up to 64 rows
 // a lane at a time, whose answers are bits of a word.
@@ -103,11 +113,7 @@ __global__ __launch_bounds__(1024) void k_linear_rows_in(const LinearArgs l) {
   if (threadIdx.x == 0) {
 #pragma unroll
     for (int k = 1; k < 16; ++k) most = fmaxf(most, mosts[k]);
-    const float one =
-        all > 0 ? static_cast<float>(1.0 / static_cast<double>(all)) : 0.0f;
-    l.scalars[0] = one;
-    l.scalars[1] = l.backward || a.weights ? most : one;
-    *l.active = all;
+    put_counts(l, all, most);
   }
 }
 
@@ -176,16 +182,17 @@ __global__ __launch_bounds__(256) void k_linear_pack_w(const LinearArgs l,
   }
 }
 
-// The rows of h that take part into its planes, and zeros where the others'
-// results are.
-template <int D>
-__global__ __launch_bounds__(256) void k_linear_pack_h(const LinearArgs l) {
-  const int64_t runs = l.pitch / 8, active = *l.active;
-  for (int64_t q = int64_t{blockIdx.x} * 256 + threadIdx.x;
-       q < l.a.rows * runs; q += int64_t{gridDim.x} * 256) {
+// The rows of h that take part, of which index[] has the numbers, into its planes,
+// and zeros where the others' results are.
+template <int D, typename Index>
+__device__ __forceinline__ void pack_rows(const LinearArgs &l, int64_t active,
+                                          Index index) {
+  const int64_t runs = l.pitch / 8;
+  for (int64_t q = int64_t{blockIdx.x} * blockDim.x + threadIdx.x;
+       q < l.a.rows * runs; q += int64_t{gridDim.x} * blockDim.x) {
     const int64_t r = q / runs, i = (q - r * runs) * 8;
     if (r < active)
-      pack_run<D>(l, l.a.h, l.index[r] * l.a.ldh, i, l.h + r * l.pitch + i,
+      pack_run<D>(l, l.a.h, index[r] * l.a.ldh, i, l.h + r * l.pitch + i,
                   l.h_plane);
     if (active == l.a.rows || !left_out(l, r)) continue;
     if (i == 0 && !l.backward) {
@@ -203,6 +210,51 @@ __global__ __launch_bounds__(256) void k_linear_pack_h(const LinearArgs l) {
       }
     }
   }
+}
+
+template <int D>
+__global__ __launch_bounds__(256) void k_linear_pack_h(const LinearArgs l) {
+  pack_rows<D>(l, *l.active, l.index);
+}
+
+// Both for up to 1024 rows, whose workgroups find the rows each for itself: 3.5 us
+// at 8 rows where the two launches take 3.3 and 3.1.
+template <int D>
+__global__ __launch_bounds__(1024) void k_linear_few_rows(const LinearArgs l) {
+  const mta_linear_loss_args &a = l.a;
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  __shared__ int counts[16], index[1024];
+  __shared__ float mosts[16];
+  const int64_t r = threadIdx.x;
+  const bool in = r < a.rows && !left_out(l, r);
+  const float w = !in          ? 0.0f
+                  : l.backward ? l.rows[r].weight
+                  : a.weights  ? a.weights[r]
+                               : 0.0f;
+  float most = fabsf(w);
+  const uint64_t bits = __ballot(in);
+#pragma unroll
+  for (int d = 32; d > 0; d /= 2) most = fmaxf(most, __shfl_xor(most, d));
+  if (lane == 0) {
+    counts[wave] = __popcll(bits);
+    mosts[wave] = most;
+  }
+  __syncthreads();
+  int before = __popcll(bits & ((uint64_t{1} << lane) - 1)), all = 0;
+  most = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    if (k < wave) before += counts[k];
+    all += counts[k];
+    most = fmaxf(most, mosts[k]);
+  }
+  if (in) {
+    index[before] = threadIdx.x;
+    if (blockIdx.x == 0) l.index[before] = threadIdx.x;
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) put_counts(l, all, most);
+  __syncthreads();
+  pack_rows<D>(l, all, index);
 }
 
 // e^(z - top) with `shift` = shift_of(top): in one fused step, whose rounding of
@@ -341,15 +393,18 @@ __global__ __launch_bounds__(C::kThreads)
   }
 }
 
-// Rows' tiles joined: 64 rows to a workgroup, 16 waves that take every 16th
-// tile and are joined in order.  A workgroup that has all rows sums the loss
-// too.
+// Rows' tiles joined: `across` rows (up to 64) to a workgroup, one a lane, in 16
+// waves and, with fewer rows, parts of waves that take every so many'th tile and
+// are joined in order (8 rows, 393 tiles: 4.8 us, and 9.0 with a wave for 64 rows
+// at all sizes).  A workgroup that has all rows sums the loss too.
 template <int D>
-__global__ __launch_bounds__(1024) void k_linear_rows(const LinearArgs l) {
+__global__ __launch_bounds__(1024) void k_linear_rows(const LinearArgs l, int across) {
   const mta_linear_loss_args &a = l.a;
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  const int64_t at = int64_t{blockIdx.x} * 64 + lane, active = *l.active;
+  const int64_t at = int64_t{blockIdx.x} * 64 + lane % across;
+  const int64_t active = *l.active;
   if (blockIdx.x * 64 >= active && gridDim.x > 1) return;
+  const int parts = 1024 / across, part = threadIdx.x / across;
   const auto join = [](float &top, float &sum, float t, float s) {
     const float most = fmaxf(top, t), shift = shift_of<D>(most);
     sum = sum * exponential<D>(top, shift) + s * exponential<D>(t, shift);
@@ -358,22 +413,24 @@ __global__ __launch_bounds__(1024) void k_linear_rows(const LinearArgs l) {
   float top = -__builtin_inff(), sum = 0.0f;
   if (at < active) {
     constexpr int kMany = 8;  // on their way at a time
-    for (int64_t t = wave; t < l.tiles; t += 16 * kMany) {
+    for (int64_t t = part; t < l.tiles; t += parts * kMany) {
       float2 v[kMany];
 #pragma unroll
       for (int k = 0; k < kMany; ++k)
-        v[k] = l.partial[min(t + 16 * k, l.tiles - 1) * a.rows + at];
+        v[k] = l.partial[min(t + parts * k, l.tiles - 1) * a.rows + at];
 #pragma unroll
       for (int k = 0; k < kMany; ++k)
-        if (t + 16 * k < l.tiles) join(top, sum, v[k].x, v[k].y);
+        if (t + parts * k < l.tiles) join(top, sum, v[k].x, v[k].y);
     }
   }
+  for (int d = across; d < 64; d *= 2)
+    join(top, sum, __shfl_xor(top, d), __shfl_xor(sum, d));
   __shared__ float2 side[16][64];
   side[wave][lane] = make_float2(top, sum);
   __syncthreads();
   if (wave != 0) return;
   double term = 0.0;
-  if (at < active) {
+  if (at < active && lane < across) {
 #pragma unroll
     for (int k = 1; k < 16; ++k)
       join(top, sum, side[k][lane].x, side[k][lane].y);
@@ -706,15 +763,18 @@ void with_tile(int tile, uint32_t groups, int type, F &&f) {
 }  // namespace
 
 hipError_t launch_linear_rows_in(const LinearArgs &l, hipStream_t s) {
+  const int64_t runs = l.a.rows * (l.pitch / 8);
+  if (l.a.rows <= 1024) {
+    with_type(l.a.type, [&](auto t) {
+      k_linear_few_rows<decltype(t)::value>
+          <<<std::clamp<uint32_t>(up(runs, 1024), 1, 1u << 20), 1024, 0, s>>>(l);
+    });
+    return hipGetLastError();
+  }
   k_linear_rows_in<<<1, 1024, 0, s>>>(l);
-  return hipGetLastError();
-}
-
-hipError_t launch_linear_pack_h(const LinearArgs &l, hipStream_t s) {
-  const uint32_t grid =
-      std::min<uint32_t>(up(l.a.rows * (l.pitch / 8), 256), 1u << 20);
   with_type(l.a.type, [&](auto t) {
-    k_linear_pack_h<decltype(t)::value><<<grid, 256, 0, s>>>(l);
+    k_linear_pack_h<decltype(t)::value>
+        <<<std::min<uint32_t>(up(runs, 256), 1u << 20), 256, 0, s>>>(l);
   });
   return hipGetLastError();
 }
@@ -748,8 +808,10 @@ hipError_t launch_linear_logits(const LinearArgs &l, int tile, hipStream_t s) {
 
 hipError_t launch_linear_rows(const LinearArgs &l, hipStream_t s) {
   const uint32_t grid = std::max(1u, up(l.a.rows, 64));
+  int across = 64;
+  while (across > 1 && across / 2 >= l.a.rows) across /= 2;
   with_type(l.a.type, [&](auto t) {
-    k_linear_rows<decltype(t)::value><<<grid, 1024, 0, s>>>(l);
+    k_linear_rows<decltype(t)::value><<<grid, 1024, 0, s>>>(l, across);
   });
   if (grid > 1) k_linear_sum<<<1, 1024, 0, s>>>(l);
   return hipGetLastError();

@@ -657,7 +657,6 @@ hipError_t run_linear(const mta_linear_loss_args *a, const mta::LinearPlan &p,
   const auto ok = [&](hipError_t x) { return (e = x) == hipSuccess; };
   if (!ok(mta::launch_linear_rows_in(l, s))) return e;
   if (a->rows > 0) {
-    if (!ok(mta::launch_linear_pack_h(l, s))) return e;
     if (p.copy_w) {
       uint16_t *to = reinterpret_cast<uint16_t *>(ws + p.w);
       l.w = to;

@@ -232,9 +232,9 @@ struct LinearBack {
   uint32_t first_dw, first_dz;
 };
 
+// the rows that take part, and h's planes
 hipError_t launch_linear_rows_in(const LinearArgs &l, hipStream_t s);
 hipError_t launch_linear_info(const LinearArgs &l, hipStream_t s);
-hipError_t launch_linear_pack_h(const LinearArgs &l, hipStream_t s);
 hipError_t launch_linear_pack_w(const LinearArgs &l, uint16_t *to,
                                 hipStream_t s);
 hipError_t launch_linear_logits(const LinearArgs &l, int tile, hipStream_t s);

@@ -49,9 +49,6 @@ hipError_t launch_linear_rows_in(const LinearArgs &, hipStream_t) {
 hipError_t launch_linear_info(const LinearArgs &, hipStream_t) {
   reached("launch_linear_info");
 }
-hipError_t launch_linear_pack_h(const LinearArgs &, hipStream_t) {
-  reached("launch_linear_pack_h");
-}
 hipError_t launch_linear_pack_w(const LinearArgs &, uint16_t *, hipStream_t) {
   reached("launch_linear_pack_w");
 }
