@@ -73,8 +73,8 @@ typedef struct {
  * off by 2e-4 to 1.1e-3 of the result's root mean square, up to 2.5e-3 where the
  * singular values span five decades.
  * The coefficients have to keep every singular value in [0, 1] below 7 from
- * step to step and may not let one grow to 100 times itself in a step
- * (MTA_EINVAL). */
+ * step to step and may not let one grow to 100 times itself in a step, or to
+ * more than 2^18 times in all (MTA_EINVAL). */
 typedef struct {
   const mta_ortho_matrix *matrices;
   int64_t count;

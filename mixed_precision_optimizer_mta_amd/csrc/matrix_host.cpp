@@ -67,16 +67,23 @@ int check_ortho_sizes(const mta_ortho_args *a) {
 
 // Whether every singular value of [0, 1] stays below 7 over the steps and grows
 // to less than 100 times itself in one, so that what is kept in float16 stays
-// finite; *pairs: in two of them, too.
+// finite; *pairs: in two of them, too.  And whether the smallest grow to at most
+// 2^18 times themselves in all (ten usual steps): 2^-22 of X is what its two
+// float16 values leave, and 2^-52 what rounding leaves in place of an eigenvalue
+// of 0 beside the matrices of the small, which grows by the square.
 bool bounded(const double *c, int steps, bool *pairs) {
+  double slope = 1.0;
+  for (int k = 0; k < 3 * steps; ++k) {
+    if (!std::isfinite(c[k])) return false;
+    if (k % 3 == 0) slope *= std::max(1.0, std::fabs(c[k]));
+  }
+  if (!(slope <= 262144.0)) return false;
   // (those that are usual, without another look)
   constexpr double kUsual[3] = {3.4445, -4.7750, 2.0315};
   bool usual = true;
   for (int k = 0; k < 3 * steps; ++k) usual = usual && c[k] == kUsual[k % 3];
   *pairs = true;
   if (usual) return true;
-  for (int k = 0; k < 3 * steps; ++k)
-    if (!std::isfinite(c[k])) return false;
   // evenly, and down to 2^-32, 16 points an octave: the smallest ones come to
   // any place in later steps
   constexpr int kEven = 512, kFine = 512;
@@ -106,8 +113,8 @@ int check_ortho(const mta_ortho_args *a, bool *pairs) {
   if (!a->coefficients) return fail(MTA_EINVAL, "coefficients is NULL");
   if (!bounded(a->coefficients, a->steps, pairs))
     return fail(MTA_EINVAL,
-                "the coefficients let a singular value of [0, 1] grow to 7, or "
-                "to 100 times itself in a step");
+                "the coefficients let a singular value of [0, 1] grow to 7, to "
+                "100 times itself in a step, or to 2^18 times in all");
   if (!std::isfinite(a->eps) || a->eps < 0.0)
     return fail(MTA_EINVAL, "eps must be finite and >= 0 (got %g)", a->eps);
   if (a->nesterov != 0 && a->nesterov != 1)

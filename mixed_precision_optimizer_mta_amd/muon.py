@@ -144,10 +144,12 @@ def orthogonalize(x, steps=5, coefficients=COEFFICIENTS, eps=1e-7, scale=None,
     X = a X + (b A + c A A) X, A = X X^T (of the transpose where there are more
     rows than columns), times `scale` (one number, or one a matrix).
 
-    coefficients: one (a, b, c), or one for each step.  The results are new
-    tensors of `dtype` (default: x's), or `out`.  precise: products of 22 bits
-    instead of float16's 11, at three times the work; by default for float32
-    and float16 results, whose digits are more than those of the 11."""
+    coefficients: one (a, b, c), or one for each step; small singular values
+    grow by the product of the a, which is at most 2^18 (ten of the default
+    steps).  The results are new tensors of `dtype` (default: x's), or `out`.
+    precise: products of 22 bits instead of float16's 11, at three times the
+    work; by default for float32 and float16 results, whose digits are more
+    than those of the 11."""
     if isinstance(x, torch.Tensor):
         return _call([x], None, out, dtype, scale, steps, coefficients, eps,
                      0.0, False, precise)[0]

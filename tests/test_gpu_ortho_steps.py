@@ -124,6 +124,25 @@ def test_two_steps_that_grow_too_much_for_one_product(precise):
         3 * (3 * 190) ** 0.5 * 2.0 ** -24 * 25 * 25
 
 
+@pytest.mark.parametrize("precise", [False, True])
+@pytest.mark.parametrize("rows,cols,rank", [(16, 64, 3), (64, 700, 5),
+                                            (33, 2000, 1), (130, 3000, 20),
+                                            (300, 256, 40)])
+def test_most_steps_of_matrices_without_full_rank(rows, cols, rank, precise):
+    """Ten steps raise what rounding leaves of the other directions to any size,
+    but singular values stay where the polynomial has them, below 1.21.  Those
+    of up to 64 rows are right beyond that: 2^-52 of the Gram matrix comes to
+    2^-16, beside 1, of what multiplies directions of up to 2^-26 + 18."""
+    g = torch.Generator().manual_seed(rank)
+    x = torch.randn(rows, rank, generator=g) @ torch.randn(rank, cols,
+                                                           generator=g)
+    y = M.orthogonalize(x.cuda(), steps=10, precise=precise)
+    assert y.isfinite().all()
+    assert torch.linalg.matrix_norm(y.double().cpu(), 2) <= 1.25
+    if rows <= 64:
+        assert R.off(y, R.orthogonal(x, steps=10)) <= 2.0 ** -22 + 2.0 ** -24
+
+
 def test_replays():
     """Captured steps by twos and in parts, replayed on new values with eager
     work between."""

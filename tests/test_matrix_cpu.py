@@ -117,10 +117,10 @@ def test_orthogonalize_refuses(matrix, kw, code):
 
 
 def test_orthogonalize_refuses_what_only_small_values_reach():
-    """Twelve steps and three more bring whatever begins above 1/512 to 1,
+    """Five steps and three more bring whatever begins above 1/512 to 1,
     where the last polynomial, 60 (x^2 - 1)^2, is 0; smaller ones come to
     0.447, where it makes 17 of them."""
-    co = [(3.4445, -4.7750, 2.0315)] * 12 + [(1.875, -1.25, 0.375)] * 3 + \
+    co = [(3.4445, -4.7750, 2.0315)] * 5 + [(1.875, -1.25, 0.375)] * 3 + \
         [(60.0, -120.0, 60.0)]
     flat = [v for row in co for v in row]
     x = [k / 512 for k in range(1, 513)]
@@ -128,9 +128,23 @@ def test_orthogonalize_refuses_what_only_small_values_reach():
         x = [v * (a + b * v * v + c * v ** 4) for v in x]
         assert max(map(abs, x)) < 7
     args = ortho()
-    args.steps, args.coefficients = 16, (ctypes.c_double * 48)(*flat)
+    args.steps, args.coefficients = 9, (ctypes.c_double * 27)(*flat)
     assert _code(B.mta_orthogonalize, args) == -1
     assert "coefficients" in M.mta_last_error()
+
+
+@pytest.mark.parametrize("co,steps", [((3.4445, -4.7750, 2.0315), 11),
+                                      ((5.0, -20.0, 16.0), 8)])
+def test_orthogonalize_refuses_slopes_past_2_18(co, steps):
+    """Ten usual steps, and seven of 16 x^5 - 20 x^3 + 5 x (whose values stay in
+    [-1, 1]), come as far as the workspace, which is missing; one more does
+    not."""
+    for n, word in ((steps - 1, "workspace"), (steps, "coefficients")):
+        args = ortho(workspace=None)
+        args.steps = n
+        args.coefficients = (ctypes.c_double * (3 * n))(*list(co) * n)
+        assert _code(B.mta_orthogonalize, args) == -1
+        assert word in M.mta_last_error()
 
 
 def test_orthogonalize_refuses_shared_outputs_of_a_list():
