@@ -18,6 +18,12 @@
 // GB, whose writing and reading takes as long as the fourth.
 //
 // A float32 call has three bfloat16 planes for each operand and six products.
+//
+// Bound by the matrix pipes at the clock that this card's power allows: 14746
+// rows of 768 against 50257 take 1.15 ms (990 TFLOP/s; the library's large
+// product reaches 1228), 6554 rows of 1600 with gradients 4.3 ms (4.2 TFLOP of
+// four products: 990).  8 rows take 24 us, 16.5 of them the product at 4.7 TB/s
+// of w.
 #include <algorithm>
 
 #include "gemm_device.h"
