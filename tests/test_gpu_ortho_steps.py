@@ -113,7 +113,7 @@ def test_a_list_of_different_lengths(precise):
 def test_two_steps_that_grow_too_much_for_one_product(precise):
     """5 T5(x) and 6 T5(x / 5), T5 = 16 x^5 - 20 x^3 + 5 x: slopes 25 and 6, and
     150 for both."""
-    co = [(25.0, -100.0, 80.0), (6.0, -0.96, 0.03072)]
+    co = [(25.0, -100.0, 80.0), (6.0, -0.96, 1.2 * 16 / 625)]
     x = matrix(130, 3000, "f32", 3)
     y = M.orthogonalize(on_gpu(x), steps=2, coefficients=co, precise=precise)
     want = R.orthogonal(x, co)
