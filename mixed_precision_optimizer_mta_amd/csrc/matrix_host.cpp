@@ -333,7 +333,11 @@ hipError_t run_ortho(const mta_ortho_args *a,
         for (uint32_t k = 0; k < l.count; ++k)
           groups += ortho_tiles(step, l.item[k].rows, l.item[k].cols, t) * cuts;
         if (too_many(t, groups, cus)) continue;
-        const TileTime x = tile_time(t, groups, cus);
+        TileTime x = tile_time(t, groups, cus);
+        // X is read and written at a tile's end, beside the products of the
+        // workgroup that shares the CU with a tile of 128 (768 deep: 69 us, and 75
+        // in tiles of 256; 1600 deep 410 and 350)
+        if (t == 256 && step >= mta::kOrthoNext) x.ends += 4.0;
         double longest = 0.0, work = 0.0;
         for (uint32_t k = 0; k < l.count; ++k) {
           const int64_t rows = l.item[k].rows, cols = l.item[k].cols;
