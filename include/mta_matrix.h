@@ -122,7 +122,8 @@ typedef struct {
  * is not read, its logp is 0 and its dh +0.  Without weights every other row
  * has 1 / their number; a call without such rows has loss 0.  Another target
  * outside [0, vocab) reads nothing out of range and makes the row's logp and
- * dh, the loss and dw NaN.
+ * dh, the loss and dw NaN.  So does a largest logit that is infinite (of either
+ * sign) or, for 16-bit elements, beyond +-2.35e38 (2^128 / log2(e)).
  * Products of 16-bit elements are exact, those of float32 elements are taken as
  * the six largest of nine products of three bfloat16 values; sums are float32.
  * dz is rounded once to the 16-bit type (float32: to three bfloat16 values)

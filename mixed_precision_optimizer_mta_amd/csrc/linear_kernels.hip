@@ -269,8 +269,10 @@ __global__ __launch_bounds__(1024) void k_linear_few_rows(const LinearArgs l) {
 constexpr float kLog2e = 1.44269504f;
 template <int D>
 __device__ __forceinline__ float shift_of(float top) {
-  // (a row of nothing but -infinity)
-  const float t = top == -__builtin_inff() ? 0.0f : top;
+  // (nothing but -infinity, or what times log2(e) would be: exponentials of 0)
+  constexpr float kLeast =
+      D == MTA_F32 ? -3.40282347e38f : -3.40282347e38f / kLog2e;
+  const float t = top < kLeast ? 0.0f : top;
   return D == MTA_F32 ? t : t * -kLog2e;
 }
 template <int D>
@@ -453,8 +455,10 @@ __global__ __launch_bounds__(1024) void k_linear_rows(const LinearArgs l, int ac
       r.total = sum + own;
       r.rest = sum / r.total;
       logp = zt == top ? -log1pf(sum) : (zt - top) - logf(r.total);
-      // (the largest may be infinite)
-      if (!(own == own)) logp = own;
+      // (no exponential of the row's is a number above 0: its largest logit is
+      // infinite or, in 16 bits, beyond 2^128 / log2(e))
+      if (!(r.total > 0.0f && r.total < __builtin_inff()))
+        r.top = r.total = r.rest = logp = __builtin_nanf("");
     }
     l.rows[row] = r;
     if (a.logp) a.logp[row] = logp;

@@ -1,0 +1,71 @@
+"""Rows of the linear cross entropy whose logits or weights leave the range of
+finite numbers: what becomes of them, and that the others do not notice."""
+import pytest
+import torch
+
+import matrix_oracle as R
+import mixed_precision_optimizer_mta_amd as M
+from test_gpu_linear_loss import case
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("dtype,vocab,h,w", [
+    ("f32", 5, 1e30, -1e30), ("bf16", 5, 1e30, -1e30),
+    ("bf16", 700, 1e30, -1e30),
+    # 16-bit elements: logits of -infinity from a weight of it, and logits whose
+    # multiple of log2(e) is none
+    ("f16", 5, 1.0, -float("inf")), ("f16", 700, 1.0, -float("inf")),
+    ("bf16", 5, 1.0, -3e38)])
+def test_no_logit_that_is_a_number(dtype, vocab, h, w):
+    """log softmax of nothing but -infinity is NaN, in loss, logp and
+    gradients."""
+    dt = R.DTYPES[dtype]
+    hidden = torch.zeros(3, 8, dtype=dt, device="cuda")
+    hidden[:, 0] = h
+    weight = torch.zeros(vocab, 8, dtype=dt, device="cuda")
+    weight[:, 0] = w
+    t = torch.tensor([0, vocab - 1, -100], device="cuda")
+    r = M.linear_cross_entropy_grad(hidden, weight, t)
+    assert r.loss.isnan() and r.logp[:2].isnan().all() and r.logp[2] == 0
+    assert r.dhidden[:2].isnan().all() and not r.dhidden[2].any()
+    assert r.dweight.isnan().any()
+    f = M.linear_cross_entropy_forward(hidden, weight, t)
+    assert f.loss.isnan() and f.logp[:2].isnan().all()
+
+
+@pytest.mark.parametrize("vocab", [50, 700])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_row_beside_it(dtype, vocab):
+    """Only one row's logits are all -infinity: sixteen products of the lowest
+    number with 1 or more."""
+    d = case(30, vocab, 16, dtype, 1, masked=0.0)
+    w = d["w"].abs() + 1
+    want = M.linear_cross_entropy_grad(d["h"], w, d["t"])
+    h = d["h"].clone()
+    h[4] = torch.finfo(h.dtype).min
+    r = M.linear_cross_entropy_grad(h, w, d["t"])
+    rest = torch.arange(30) != 4
+    assert r.logp[4].isnan() and r.loss.isnan()
+    assert r.dhidden[4].isnan().all()
+    assert torch.equal(r.logp[rest], want.logp[rest])
+    assert torch.equal(r.dhidden[rest], want.dhidden[rest])
+
+
+def test_logits_far_below_a_row_s_others():
+    """A tile of the vocabulary whose logits are all beyond -2^127 / log2(e)
+    adds nothing to a row whose other logits are ordinary."""
+    for vocab in (257, 513, 700):
+        h = torch.ones(4, 8, dtype=torch.bfloat16, device="cuda")
+        w = torch.zeros(vocab, 8, dtype=torch.bfloat16, device="cuda")
+        w[:5, 0] = torch.arange(5)
+        w[128:, 0] = -3e38
+        t = torch.tensor([0, 3, 4, 1], device="cuda")
+        r = M.linear_cross_entropy_grad(h, w, t)
+        z = torch.zeros(128, dtype=torch.float64)
+        z[:5] = torch.arange(5)
+        lp = torch.log_softmax(z, 0)[t.cpu()]
+        # the sum of 128 exponentials, and the argument's and value's roundings
+        assert torch.allclose(r.logp.cpu().double(), lp, rtol=0, atol=64 *
+                              2.0 ** -24)
+        assert r.dhidden.isfinite().all() and r.dweight.isfinite().all()
