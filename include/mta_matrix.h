@@ -127,7 +127,7 @@ typedef struct {
  * Products of 16-bit elements are exact, those of float32 elements are taken as
  * the six largest of nine products of three bfloat16 values; sums are float32.
  * dz is rounded once to the 16-bit type (float32: to three bfloat16 values)
- * before dh and dw are made of it, scaled so that its largest weight is 1
+ * before dh and dw are made of it, scaled so that its largest finite weight is 1
  * (float16: 2^14): neither S nor small weights cost digits. */
 typedef struct {
   const void *h;              /* [rows, width], rows of ldh elements */

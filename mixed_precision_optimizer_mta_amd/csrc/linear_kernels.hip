@@ -44,9 +44,18 @@ __device__ __forceinline__ bool left_out(const LinearArgs &l, int64_t r) {
          (l.a.weights && l.a.weights[r] == 0.0f);
 }
 
-// How many rows take part, the weight of a row without weights and the largest.
+// A weight's part in the largest: an infinite one's would leave zeros of the
+// other rows' dz, and NaN (a NaN's part is none, too).
+__device__ __forceinline__ float finite_size(float weight) {
+  const float x = fabsf(weight);
+  return x < __builtin_inff() ? x : 0.0f;
+}
+
+// How many rows take part, the weight of a row without weights and the largest
+// finite one.
 __device__ __forceinline__ void put_counts(const LinearArgs &l, int all,
                                            float most) {
+  if (!(most > 0.0f)) most = 1.0f;
   const float one =
       all > 0 ? static_cast<float>(1.0 / static_cast<double>(all)) : 0.0f;
   l.scalars[0] = one;
@@ -55,8 +64,8 @@ __device__ __forceinline__ void put_counts(const LinearArgs &l, int all,
 }
 
 // The rows that take part, in order, their number, the weight of a row without
-// weights and the largest magnitude of any: one workgroup, a run of up to 64 rows
-// a lane at a time, whose answers are bits of a word.
+// weights and the largest finite magnitude of any: one workgroup, a run of up to
+// 64 rows a lane at a time, whose answers are bits of a word.
 __global__ __launch_bounds__(1024) void k_linear_rows_in(const LinearArgs l) {
   const mta_linear_loss_args &a = l.a;
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
@@ -79,14 +88,14 @@ __global__ __launch_bounds__(1024) void k_linear_rows_in(const LinearArgs l) {
     if (l.backward)
       mark([&](int64_t r) {
         const float w = l.rows[r].weight;
-        most = fmaxf(most, fabsf(w));
+        most = fmaxf(most, finite_size(w));
         return w != 0.0f;
       });
     else if (a.weights)
       mark([&](int64_t r) {
         const float w = a.weights[r];
         const bool is = a.targets[r] != a.ignore_index && w != 0.0f;
-        most = is ? fmaxf(most, fabsf(w)) : most;
+        most = is ? fmaxf(most, finite_size(w)) : most;
         return is;
       });
     else
@@ -237,7 +246,7 @@ __global__ __launch_bounds__(1024) void k_linear_few_rows(const LinearArgs l) {
                   : l.backward ? l.rows[r].weight
                   : a.weights  ? a.weights[r]
                                : 0.0f;
-  float most = fabsf(w);
+  float most = finite_size(w);
   const uint64_t bits = __ballot(in);
 #pragma unroll
   for (int d = 32; d > 0; d /= 2) most = fmaxf(most, __shfl_xor(most, d));

@@ -206,6 +206,7 @@ struct LinearArgs {
   int *index;             // [rows]
   LinearInfo *info;       // [deep_rows]
   float *scalars;         // [0] weight of a row without weights, [1] largest
+                          // finite one
   double *terms;          // [rows] of the loss
   float *z_target;        // [rows]
   float2 *partial;        // [tiles][rows]: largest, sum without the target

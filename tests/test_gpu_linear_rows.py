@@ -69,3 +69,35 @@ def test_logits_far_below_a_row_s_others():
         assert torch.allclose(r.logp.cpu().double(), lp, rtol=0, atol=64 *
                               2.0 ** -24)
         assert r.dhidden.isfinite().all() and r.dweight.isfinite().all()
+
+
+@pytest.mark.parametrize("rows", [30, 1500])
+@pytest.mark.parametrize("dtype", list(R.DTYPES))
+def test_an_infinite_weight(dtype, rows):
+    """The row's own gradient is no number; the others' are what they are."""
+    d = case(rows, 300, 64, dtype, 2)
+    on = (d["t"] != -100).nonzero()[:, 0]
+    wt = torch.rand(rows, generator=torch.Generator().manual_seed(1)).cuda()
+    wt[on[0]] = 0.75                       # the largest stays the largest
+    wt.clamp_max_(0.75)
+    want = M.linear_cross_entropy_grad(d["h"], d["w"], d["t"], weights=wt)
+    rest = torch.ones(rows, dtype=torch.bool, device="cuda")
+    for bad in (float("inf"), -float("inf"), float("nan")):
+        w2 = wt.clone()
+        w2[on[3]] = bad
+        rest[on[3]] = False
+        r = M.linear_cross_entropy_grad(d["h"], d["w"], d["t"], weights=w2)
+        assert not r.dhidden[on[3]].isfinite().any()
+        assert not r.dweight.isfinite().any()
+        assert torch.equal(r.logp, want.logp)
+        assert torch.equal(r.dhidden[rest], want.dhidden[rest])
+        f = M.linear_cross_entropy_forward(d["h"], d["w"], d["t"], weights=w2)
+        dh, _ = M.linear_cross_entropy_backward(d["h"], d["w"], d["t"],
+                                                f.saved, need_weight=False)
+        assert torch.equal(dh[rest], want.dhidden[rest])
+    # no finite weight at all: no NaN where the product with it has none
+    w2 = torch.full_like(wt, float("inf"))
+    r = M.linear_cross_entropy_grad(d["h"], d["w"], d["t"], weights=w2)
+    assert r.loss == float("inf")
+    assert not r.dhidden[on].isfinite().any()
+    assert not r.dhidden[d["t"] == -100].any()
