@@ -65,7 +65,8 @@ typedef struct {
  * the others alone; one of zeros comes out zero.
  *
  * A matrix of up to 64 rows or columns is computed in float64.  Otherwise X is
- * kept as a float16 value and a second one for what it leaves (22 bits), the
+ * kept as a float16 value and a second one for what it leaves (22 bits), times a
+ * power of two as long as it is far below 1 (|u| far below eps); the
  * symmetric matrices as such values and their diagonals in float32; sums are
  * float32, and two steps may be taken as one product (Q' Q) X.  With `precise`
  * all products are those of 22 bits, three float16 products each.  Without,

@@ -85,6 +85,9 @@ __host__ __device__ constexpr Pairs pairs_of(int planes) {
 __device__ __forceinline__ uint32_t scalar(uint32_t x) {
   return __builtin_amdgcn_readfirstlane(x);
 }
+__device__ __forceinline__ float scalar(float x) {
+  return __uint_as_float(scalar(__float_as_uint(x)));
+}
 __device__ __forceinline__ const MTA_GLOBAL uint8_t *scalar(
     const MTA_GLOBAL uint8_t *p) {
   const uint64_t x = (uint64_t)p;

@@ -70,8 +70,9 @@ int check_ortho_sizes(const mta_ortho_args *a) {
 // finite; *pairs: in two of them, too.  And whether the smallest grow to at most
 // 2^18 times themselves in all (ten usual steps): 2^-22 of X is what its two
 // float16 values leave, and 2^-52 what rounding leaves in place of an eigenvalue
-// of 0 beside the matrices of the small, which grows by the square.
-bool bounded(const double *c, int steps, bool *pairs) {
+// of 0 beside the matrices of the small, which grows by the square.  grown[k]: what
+// one of them is after any of the first k steps over what it was, at most.
+bool bounded(const double *c, int steps, bool *pairs, double *grown) {
   double slope = 1.0;
   for (int k = 0; k < 3 * steps; ++k) {
     if (!std::isfinite(c[k])) return false;
@@ -83,27 +84,42 @@ bool bounded(const double *c, int steps, bool *pairs) {
   bool usual = true;
   for (int k = 0; k < 3 * steps; ++k) usual = usual && c[k] == kUsual[k % 3];
   *pairs = true;
-  if (usual) return true;
+  grown[0] = 1.0;
+  if (usual) {
+    // (the slope at 0)
+    for (int s = 0; s < steps; ++s) grown[s + 1] = grown[s] * kUsual[0];
+    return true;
+  }
+  std::fill(grown + 1, grown + steps + 1, 1.0);
   // evenly, and down to 2^-32, 16 points an octave: the smallest ones come to
   // any place in later steps
   constexpr int kEven = 512, kFine = 512;
   for (int i = 0; i <= kEven + kFine; ++i) {
     double x = i <= kEven ? static_cast<double>(i) / kEven
                           : std::exp2((kEven - i) / 16.0);
-    double before = 1.0;
+    double before = 1.0, all = 1.0;
     for (int s = 0; s < steps; ++s) {
       const double q = x * x;
       const double f = c[3 * s] + q * (c[3 * s + 1] + q * c[3 * s + 2]);
       x *= f;
+      all *= f;
+      grown[s + 1] = std::max(grown[s + 1], std::fabs(all));
       if (!(std::fabs(x) < 7.0) || !(std::fabs(f) < 100.0)) return false;
       if (s % 2 && !(std::fabs(f * before) < 100.0)) *pairs = false;
       before = f;
     }
   }
+  for (int s = 0; s < steps; ++s) grown[s + 1] = std::max(grown[s + 1], grown[s]);
   return true;
 }
 
-int check_ortho(const mta_ortho_args *a, bool *pairs) {
+// What check_ortho finds out about the coefficients.
+struct OrthoCourse {
+  bool pairs;
+  double grown[MTA_ORTHO_STEPS + 1];
+};
+
+int check_ortho(const mta_ortho_args *a, OrthoCourse *course) {
   int rc = check_ortho_sizes(a);
   if (rc) return rc;
   if (!known_type(a->type) || !known_type(a->out_type))
@@ -111,7 +127,7 @@ int check_ortho(const mta_ortho_args *a, bool *pairs) {
   if (a->steps < 1 || a->steps > MTA_ORTHO_STEPS)
     return fail(MTA_EINVAL, "steps must be in [1, %d]", MTA_ORTHO_STEPS);
   if (!a->coefficients) return fail(MTA_EINVAL, "coefficients is NULL");
-  if (!bounded(a->coefficients, a->steps, pairs))
+  if (!bounded(a->coefficients, a->steps, &course->pairs, course->grown))
     return fail(MTA_EINVAL,
                 "the coefficients let a singular value of [0, 1] grow to 7, to "
                 "100 times itself in a step, or to 2^18 times in all");
@@ -256,8 +272,8 @@ std::vector<OrthoGroup> ortho_groups(const mta_ortho_args *a) {
 }
 
 hipError_t run_ortho(const mta_ortho_args *a,
-                     const std::vector<OrthoGroup> &groups, bool pairs,
-                     int cus, hipStream_t s) {
+                     const std::vector<OrthoGroup> &groups,
+                     const OrthoCourse &course, int cus, hipStream_t s) {
   hipError_t e = hipSuccess;
   mta::OrthoCall c{};
   c.d_coef = a->d_coef;
@@ -313,13 +329,6 @@ hipError_t run_ortho(const mta_ortho_args *a,
       if ((e = mta::launch_ortho_small_apply(l, c, s)) != hipSuccess) return e;
       continue;
     }
-    deal([](int64_t r, int64_t n) { return mta::ortho_parts(r, n); });
-    if ((e = mta::launch_ortho_norm(l, c, s)) != hipSuccess) return e;
-    deal([](int64_t r, int64_t n) {
-      return up(std::min(r, n), mta::kOrthoLoadTile) *
-             up(mta::plane_pitch(std::max(r, n)), mta::kOrthoLoadTile);
-    });
-    if ((e = mta::launch_ortho_load(l, c, s)) != hipSuccess) return e;
     // Each kind of product's tile, and its time in us.
     const int runs = mta::pair_count(c.planes);
     int tile[4];
@@ -376,38 +385,56 @@ hipError_t run_ortho(const mta_ortho_args *a,
       return mta::launch_ortho_product(
           step, t, l.first[l.count] <= static_cast<uint32_t>(cus), l, c, s);
     };
-    // buffer `out` = e0 P Q + e1 P + e2
-    const auto times = [&](int p, int q, int out, double e0, double e1,
-                           double e2) {
+    // buffer `out` = P Q, or a + b P + c P P with a step's coefficients
+    const auto times = [&](int p, int q, int out, const double *of) {
       c.p = p;
       c.q = q;
       c.out = out;
-      c.e0 = static_cast<float>(e0);
-      c.e1 = static_cast<float>(e1);
-      c.e2 = static_cast<float>(e2);
+      c.steps_of = of != nullptr;
+      c.e0 = of ? static_cast<float>(of[2]) : 1.0f;
+      c.e1 = of ? static_cast<float>(of[1]) : 0.0f;
+      c.e2 = of ? static_cast<float>(of[0]) : 0.0f;
       return product(mta::kOrthoTimes);
     };
     // Two steps at once where that takes less: one product over the columns of
     // either kind less and three of small matrices more (and a launch).
     const bool by_two =
-        pairs && us[mta::kOrthoGram] + us[mta::kOrthoNext] >
-                     3.0 * us[mta::kOrthoTimes] + 5.0;
+        course.pairs && us[mta::kOrthoGram] + us[mta::kOrthoNext] >
+                            3.0 * us[mta::kOrthoTimes] + 5.0;
     const int blocks = by_two ? (a->steps + 1) / 2 : a->steps;
+    // the step behind those that are taken together with step k, and what
+    // singular values have grown by there (0: there is no step k)
+    const auto behind = [&](int k) {
+      return by_two ? std::min(k + 2, a->steps) : k + 1;
+    };
+    const auto grown = [&](int k) {
+      return k < a->steps ? static_cast<float>(course.grown[behind(k)]) : 0.0f;
+    };
+    c.grown = grown(0);
+    deal([](int64_t r, int64_t n) { return mta::ortho_parts(r, n); });
+    if ((e = mta::launch_ortho_norm(l, c, s)) != hipSuccess) return e;
+    deal([](int64_t r, int64_t n) {
+      return up(std::min(r, n), mta::kOrthoLoadTile) *
+             up(mta::plane_pitch(std::max(r, n)), mta::kOrthoLoadTile);
+    });
+    if ((e = mta::launch_ortho_load(l, c, s)) != hipSuccess) return e;
     c.which = 0;
     for (int k = 0, block = 0; k < a->steps; ++block) {
       const double *co = a->coefficients + 3 * k;
-      const bool two = by_two && k + 1 < a->steps;
+      const bool two = behind(k) == k + 2;
+      c.grown = grown(k);
+      c.grows = grown(behind(k));
       if ((e = product(mta::kOrthoGram)) != hipSuccess) return e;
-      if ((e = times(0, 0, 1, co[2], co[1], co[0])) != hipSuccess) return e;
+      if ((e = times(0, 0, 1, co)) != hipSuccess) return e;
       double rest = co[0];
       if (two) {
-        if ((e = times(0, 1, 2, 1, 0, 0)) != hipSuccess) return e;
-        if ((e = times(2, 1, 0, 1, 0, 0)) != hipSuccess) return e;
-        if ((e = times(0, 0, 2, co[5], co[4], co[3])) != hipSuccess) return e;
-        if ((e = times(2, 1, 0, 1, 0, 0)) != hipSuccess) return e;
+        if ((e = times(0, 1, 2, nullptr)) != hipSuccess) return e;
+        if ((e = times(2, 1, 0, nullptr)) != hipSuccess) return e;
+        if ((e = times(0, 0, 2, co + 3)) != hipSuccess) return e;
+        if ((e = times(2, 1, 0, nullptr)) != hipSuccess) return e;
         rest *= co[3];
       }
-      k += two ? 2 : 1;
+      k = behind(k);
       c.out = two ? 0 : 1;
       c.rest = static_cast<float>(rest);
       c.whole = block + 2 >= blocks;
@@ -769,14 +796,14 @@ int mta_orthogonalize(const mta_ortho_args *a, void *stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = hipSuccess;
   try {
-    bool pairs = false;
-    int rc = check_ortho(a, &pairs);
+    OrthoCourse course;
+    int rc = check_ortho(a, &course);
     if (rc) return rc;
     const std::vector<OrthoGroup> groups = ortho_groups(a);
     if (groups.empty()) return ok();
     int cus = 0;
     if ((rc = current_cus(&cus))) return rc;
-    e = run_ortho(a, groups, pairs, cus, s);
+    e = run_ortho(a, groups, course, cus, s);
   } catch (const std::bad_alloc &) {
     return fail(MTA_ENOMEM, "host allocation failed");
   }

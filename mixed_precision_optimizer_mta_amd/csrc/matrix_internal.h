@@ -69,6 +69,10 @@ struct OrthoCall {
   int cuts;     // parts of k that A is summed in
   int whole;
   int which;    // the X that is read; the other one is written
+  int steps_of;  // e0 and e1 are those of a polynomial of A
+  // What singular values grow by, at most, to the end of this product's steps
+  // and to the end of the next ones' (0: X is handed out)
+  float grown, grows;
 };
 static_assert(sizeof(OrthoList) + sizeof(OrthoCall) +
                       sizeof(double) * 3 * MTA_ORTHO_STEPS + 8 <=
@@ -104,13 +108,14 @@ __host__ __device__ inline OrthoSmallSpace ortho_small_space(int64_t rows,
 }
 
 // A matrix's part of the workspace: two X of two planes each, three symmetric
-// matrices of `planes` planes, their diagonals, the partial sums of squares.
+// matrices of `planes` planes, their diagonals, the partial sums of squares and
+// the first X's norm, a float.
 constexpr int kOrthoSquares = 3;
 struct OrthoSpace {
   int64_t small, large, pitch_x, pitch_a;
   int64_t plane_x, plane_a;          // elements
   // offsets in bytes, and from the first to the next
-  int64_t x, next_x, a, next_a, diag, next_diag, part, bytes;
+  int64_t x, next_x, a, next_a, diag, next_diag, part, norm, bytes;
   int64_t cut;  // partial sums of A: [cuts][small][pitch_a] floats
 };
 __host__ __device__ inline OrthoSpace ortho_space(int64_t rows, int64_t cols,
@@ -130,7 +135,8 @@ __host__ __device__ inline OrthoSpace ortho_space(int64_t rows, int64_t cols,
   s.diag = s.a + kOrthoSquares * s.next_a;
   s.next_diag = round(s.pitch_a * 4);  // zeros behind the last
   s.part = s.diag + kOrthoSquares * s.next_diag;
-  s.cut = s.part + kOrthoParts * 8;
+  s.norm = s.part + kOrthoParts * 8;
+  s.cut = s.norm + 256;
   s.bytes = s.cut + (cuts > 1 ? round(cuts * s.plane_a * 4) : 0);
   return s;
 }

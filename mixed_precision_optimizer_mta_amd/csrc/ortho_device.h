@@ -47,6 +47,18 @@ __device__ __forceinline__ Look look_of(const OrthoCall &c) {
   return Look{unscale_of(c), c.d_coef ? *c.d_coef : 1.0f, c.mu, c.nesterov};
 }
 
+// X of a matrix whose norm is far below eps begins far below 1, where float16
+// values have few digits: it is kept times 2^n, with n the most that leaves
+// singular values below 1 until they have grown by `grown`.  0 for any other
+// matrix (and for NaN).
+__device__ __forceinline__ int lift_of(float norm, float grown) {
+  const float x = norm * grown;
+  if (!(x > 0.0f && x < 1.0f)) return 0;
+  int e;
+  frexpf(x, &e);
+  return min(-e, 100);
+}
+
 // Eight results of a row: out, and the weights' step.
 __device__ __forceinline__ void put_result(const OrthoItem &it,
                                            const OrthoCall &c, int64_t row,

@@ -17,7 +17,8 @@
 // for normal entries and by 32% where four directions stand out a thousandfold,
 // whatever the products' sums.  X is therefore kept in 22 bits, as the sum of
 // two float16 values (scaled by 2^13, so that 1/sqrt(rows cols) and its rest are
-// normal numbers).  The products take the first values alone.  What hurts then
+// normal numbers; by more for a matrix whose norm is far below eps, until it has
+// grown).  The products take the first values alone.  What hurts then
 // is that Q's diagonal, 1 of rows that have converged but -2.6 + 3.4, is rounded
 // with the rest: diagonals are kept in float32 apart and enter as d_i X_i, and
 // the error falls from 2.9e-3 to 4.5e-4 (512 x 2048 normal entries).  In the
@@ -134,15 +135,20 @@ __global__ __launch_bounds__(256) void k_ortho_load(const OrthoList l,
       threadIdx.x < parts
           ? reinterpret_cast<const double *>(it.ws + sp.part)[threadIdx.x]
           : 0.0;
-  const double norm = sqrt(sum256(mine, four)) + c.eps;
-  const double factor = norm == 0.0 ? 0.0 : kScaleX / norm;
+  const double size = sqrt(sum256(mine, four)), norm = size + c.eps;
+  const float begin = norm == 0.0 ? 0.0f : static_cast<float>(size / norm);
+  const double factor =
+      norm == 0.0 ? 0.0
+                  : ldexp(kScaleX / norm, lift_of(begin, c.grown));
   const Look look = look_of(c);
   const bool skip = c.amp && c.amp->found_inf != 0.0f;
   const bool tall = it.rows > it.cols;
-  if (blockIdx.x == l.first[k])
+  if (blockIdx.x == l.first[k]) {
     for (int n = 0; n < kOrthoSquares; ++n)
       for (int64_t i = sp.small + threadIdx.x; i < sp.pitch_a; i += 256)
         reinterpret_cast<float *>(it.ws + sp.diag + n * sp.next_diag)[i] = 0.0f;
+    if (threadIdx.x == 0) *reinterpret_cast<float *>(it.ws + sp.norm) = begin;
+  }
   const uint32_t t = blockIdx.x - l.first[k];
   const uint32_t wide = static_cast<uint32_t>(sp.pitch_x) / kT;
   const int64_t m0 = int64_t{t / wide} * kT, n0 = int64_t{t % wide} * kT;
@@ -316,6 +322,8 @@ __global__ __launch_bounds__(C::kThreads)
   const int64_t deep_a = (sp.small + 63) / 64 * 64;
   // rows that are there, from the tile's first
   const int rows = static_cast<int>(min(sp.small - m0, int64_t{C::kBM}));
+  // (on its way until the sums are there)
+  const float begin = *reinterpret_cast<const float *>(it.ws + sp.norm);
   f32x16 acc[C::kRM][C::kRN];
 
   if constexpr (kSym) {
@@ -345,6 +353,10 @@ __global__ __launch_bounds__(C::kThreads)
     uint16_t *here = to + corner, *there = to + n0 * sp.pitch_a + m0;
     const uint16_t *at_p = square(c.p) + corner, *at_q = square(c.q) + corner;
     const float *diag_p = diagonal(c.p), *diag_q = diagonal(c.q);
+    // A is that of the lifted X
+    const int lift = lift_of(begin, c.grown);
+    const float e1 = scalar(c.steps_of ? ldexpf(c.e1, -2 * lift) : c.e1);
+    const float e0 = scalar(c.steps_of ? ldexpf(c.e0, -4 * lift) : c.e0);
     // the tile holds a part of the diagonal, or a last column
     const bool edge = tm == tn || tn + 1 == side;
     struct Seen {
@@ -389,7 +401,7 @@ __global__ __launch_bounds__(C::kThreads)
             for (int e = 0; e < 8; ++e)
               v[e] *= kScaleA / (kScaleX * kScaleX);
           } else {
-            const float of_q = c.e0 * x.row;
+            const float of_q = e0 * x.row;
             const int64_t own = m0 + m - (n0 + n);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -398,10 +410,10 @@ __global__ __launch_bounds__(C::kThreads)
                 o += x.p_lo[e];
                 r += x.q_lo[e];
               }
-              const float of_p = __builtin_fmaf(c.e0, x.col[e], c.e1);
+              const float of_p = __builtin_fmaf(e0, x.col[e], e1);
               float y = __builtin_fmaf(
                   of_p, o,
-                  __builtin_fmaf(of_q, r, v[e] * (c.e0 / kScaleA)));
+                  __builtin_fmaf(of_q, r, v[e] * (e0 / kScaleA)));
               // (O and N are 0 there)
               if (edge && e == own)
                 y += kScaleA * __builtin_fmaf(of_p, x.row, c.e2);
@@ -442,8 +454,11 @@ __global__ __launch_bounds__(C::kThreads)
     uint16_t *to = reinterpret_cast<uint16_t *>(
                        it.ws + sp.x + (1 - c.which) * sp.next_x) +
                    m0 * sp.pitch_x + n0;
-    // kept: times kScaleX; handed out: as it is
-    constexpr float kTo = Step == kOrthoLast ? 1.0f / kScaleX : 1.0f;
+    // kept: times kScaleX and what the next steps leave of the lift; handed out:
+    // as it is
+    const float to_next =
+        scalar(ldexpf(Step == kOrthoLast ? 1.0f / kScaleX : 1.0f,
+                      lift_of(begin, c.grows) - lift_of(begin, c.grown)));
     struct Seen {
       Raw8<MTA_F16> hi, lo;
       float diag;
@@ -460,13 +475,13 @@ __global__ __launch_bounds__(C::kThreads)
         },
         [&](int m, int n, float (&v)[8], const Seen &x) {
           if (m >= rows || n >= cols) return;
-          const float of_hi = x.diag * kTo;
-          const float of_lo = kTwo || c.whole ? of_hi : c.rest * kTo;
+          const float of_hi = x.diag * to_next;
+          const float of_lo = kTwo || c.whole ? of_hi : c.rest * to_next;
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             v[e] = __builtin_fmaf(
                 of_hi, x.hi[e],
-                __builtin_fmaf(of_lo, x.lo[e], v[e] * (kTo / kScaleA)));
+                __builtin_fmaf(of_lo, x.lo[e], v[e] * (to_next / kScaleA)));
           if constexpr (Step == kOrthoNext)
             store_planes<true>(to + static_cast<uint32_t>(m) * pitch + n,
                                sp.plane_x, v);
