@@ -97,15 +97,19 @@ __device__ __forceinline__ const MTA_GLOBAL uint8_t *scalar(
 }
 
 // Sixteen bytes a lane from base + off to lds + 16 * lane (base and lds the
-// same in a wave).
+// same in a wave).  m0 is a register that the compiler keeps for itself, of which
+// it warns; it is told all the same that this writes it.
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
 __device__ __forceinline__ void to_lds(const MTA_GLOBAL uint8_t *base,
                                        uint32_t off, uint32_t lds) {
   __asm__ volatile(
       "s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
       :
       : "v"(off), "s"(base), "s"(lds)
-      : "memory");
+      : "m0", "memory");
 }
+#pragma clang diagnostic pop
 
 template <bool F16>
 __device__ __forceinline__ f32x16 mfma(s16x8 a, s16x8 b, f32x16 c) {
