@@ -195,7 +195,11 @@ def linear_cross_entropy(hidden, weight, targets, weights=None,
     weight; the gradients of a scaled loss are scaled before they are rounded.
     Tensors of any strides are taken; a weight of another dtype (a float32
     master under 16-bit hidden states) is cast to hidden's, and its gradient
-    back."""
+    back.  There is no gradient for weights: those that require one are
+    refused."""
+    if weights is not None and weights.requires_grad and \
+            torch.is_grad_enabled():
+        raise ValueError("there is no gradient for weights: detach them")
     _check_type(hidden, "hidden")
     _check_type(weight, "weight")
 
