@@ -104,6 +104,8 @@ class MtaOptimizer(torch.optim.Optimizer):
     "momentum" (SGD with momentum, no dampening, not Nesterov), "muon"
     (orthogonalised momentum, for matrices; also the "kind" of single groups).
 
+    momentum is 0.95 by default for muon, and 0 for the other kinds.
+
     For muon: momentum is the group's, nesterov looks one momentum ahead,
     ns_steps, ns_coefficients and ns_eps are those of ``orthogonalize``, and
     ns_precise its `precise` (by default for float32 gradients).  update_scale
@@ -112,7 +114,7 @@ class MtaOptimizer(torch.optim.Optimizer):
     the size of AdamW's), or a number."""
 
     def __init__(self, params, kind="adamw", lr=1e-3, betas=(0.9, 0.999),
-                 eps=1e-8, weight_decay=0.0, momentum=0.0, max_norm=None,
+                 eps=1e-8, weight_decay=0.0, momentum=None, max_norm=None,
                  packed_moments=False, zero_grad=False, loss_scale=None,
                  growth_factor=2.0, backoff_factor=0.5,
                  growth_interval=2000, capturable=False,
@@ -127,6 +129,9 @@ class MtaOptimizer(torch.optim.Optimizer):
             raise ValueError('update_scale is "spectral", "rms" or a number')
         if packed_moments and kind not in ("adamw", "adam"):
             raise ValueError("packed moments are for the Adam family")
+        self._muon_momentum = 0.95 if momentum is None else momentum
+        if momentum is None:
+            momentum = self._muon_momentum if kind == "muon" else 0.0
         defaults = dict(lr=lr, betas=tuple(betas), eps=eps,
                         weight_decay=weight_decay, momentum=momentum)
         self.kind = kind
@@ -175,6 +180,8 @@ class MtaOptimizer(torch.optim.Optimizer):
         if kind != self.kind and kind != "muon":
             raise ValueError('a group\'s own kind is "muon", not '
                              f"{kind!r}")
+        if kind == "muon":
+            param_group.setdefault("momentum", self._muon_momentum)
         super().add_param_group(param_group)
         if kind == "muon" and any(
                 p.dim() < 2 for p in self.param_groups[-1]["params"]):

@@ -1,0 +1,36 @@
+"""Options and checkpoints of MtaOptimizer's groups of kind "muon", without a
+GPU."""
+import pytest
+import torch
+
+import mixed_precision_optimizer_mta_amd as M
+
+
+def p(*shape):
+    return torch.nn.Parameter(torch.zeros(*shape))
+
+
+def momenta(opt):
+    return [g["momentum"] for g in opt.param_groups]
+
+
+def test_momentum_by_default():
+    """That of muon_update, unless the optimizer or the group has one."""
+    groups = [{"params": [p(3, 3)], "kind": "muon"}, {"params": [p(3)]},
+              {"params": [p(2, 2)], "kind": "muon", "momentum": 0.5}]
+
+    def new(**kw):
+        return M.MtaOptimizer([dict(g) for g in groups], **kw)
+
+    assert momenta(M.MtaOptimizer([p(3, 3)], kind="muon")) == [0.95]
+    assert momenta(M.MtaOptimizer([p(3, 3)], kind="muon", momentum=0.0)) == \
+        [0.0]
+    assert momenta(new()) == [0.95, 0.0, 0.5]
+    assert momenta(new(momentum=0.0)) == [0.0, 0.0, 0.5]
+    assert momenta(new(kind="momentum", momentum=0.9)) == [0.9, 0.9, 0.5]
+    opt = new()
+    opt.add_param_group({"params": [p(4, 3)], "kind": "muon"})
+    opt.add_param_group({"params": [p(4)]})
+    assert momenta(opt) == [0.95, 0.0, 0.5, 0.95, 0.0]
+    for kind in ("adamw", "adam", "sgd", "momentum"):
+        assert momenta(M.MtaOptimizer([p(3)], kind=kind)) == [0.0]
