@@ -176,6 +176,8 @@ class MtaOptimizer(torch.optim.Optimizer):
     def add_param_group(self, param_group):
         """As torch.optim.Optimizer.add_param_group; a group may have the
         "kind" "muon" of its own, which takes matrices alone."""
+        if not isinstance(param_group, dict):
+            raise TypeError("a parameter group is a dict")
         kind = param_group.get("kind", self.kind)
         if kind != self.kind and kind != "muon":
             raise ValueError('a group\'s own kind is "muon", not '

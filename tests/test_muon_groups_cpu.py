@@ -34,3 +34,9 @@ def test_momentum_by_default():
     assert momenta(opt) == [0.95, 0.0, 0.5, 0.95, 0.0]
     for kind in ("adamw", "adam", "sgd", "momentum"):
         assert momenta(M.MtaOptimizer([p(3)], kind=kind)) == [0.0]
+
+
+def test_a_group_is_a_dict():
+    opt = M.MtaOptimizer([p(3, 3)], kind="muon")
+    with pytest.raises(TypeError):
+        opt.add_param_group([p(2, 2)])
