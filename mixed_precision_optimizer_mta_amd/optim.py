@@ -183,6 +183,9 @@ class MtaOptimizer(torch.optim.Optimizer):
             raise ValueError('a group\'s own kind is "muon", not '
                              f"{kind!r}")
         if kind == "muon":
+            # (written down, so that a checkpoint's groups keep it wherever it
+            # is loaded)
+            param_group.setdefault("kind", kind)
             param_group.setdefault("momentum", self._muon_momentum)
         super().add_param_group(param_group)
         if kind == "muon" and any(

@@ -36,6 +36,22 @@ def test_momentum_by_default():
         assert momenta(M.MtaOptimizer([p(3)], kind=kind)) == [0.0]
 
 
+def test_a_checkpoint_keeps_the_kind():
+    """Groups of an optimizer of kind "muon" loaded into one of another kind,
+    whose groups have it as their own: the rule they were saved under."""
+    a = M.MtaOptimizer([p(3, 3)], kind="muon", lr=0.02)
+    a.add_param_group({"params": [p(2, 2)]})
+    sd = a.state_dict()
+    assert [g["kind"] for g in sd["param_groups"]] == ["muon", "muon"]
+    b = M.MtaOptimizer([{"params": [p(3, 3)], "kind": "muon"},
+                        {"params": [p(2, 2)], "kind": "muon"}], kind="adamw")
+    b.load_state_dict(sd)
+    assert [b._kind(g) for g in b.param_groups] == ["muon", "muon"]
+    assert b.param_groups[0]["lr"] == 0.02
+    # other kinds' groups are as they were
+    assert "kind" not in M.MtaOptimizer([p(3)], kind="adamw").param_groups[0]
+
+
 def test_a_group_is_a_dict():
     opt = M.MtaOptimizer([p(3, 3)], kind="muon")
     with pytest.raises(TypeError):
