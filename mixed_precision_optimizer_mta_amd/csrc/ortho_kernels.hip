@@ -136,9 +136,10 @@ __global__ __launch_bounds__(256) void k_ortho_load(const OrthoList l,
           ? reinterpret_cast<const double *>(it.ws + sp.part)[threadIdx.x]
           : 0.0;
   const double size = sqrt(sum256(mine, four)), norm = size + c.eps;
-  const float begin = norm == 0.0 ? 0.0f : static_cast<float>(size / norm);
+  // (zeros stay zeros, however small eps is)
+  const float begin = size == 0.0 ? 0.0f : static_cast<float>(size / norm);
   const double factor =
-      norm == 0.0 ? 0.0
+      size == 0.0 ? 0.0
                   : ldexp(kScaleX / norm, lift_of(begin, c.grown));
   const Look look = look_of(c);
   const bool skip = c.amp && c.amp->found_inf != 0.0f;

@@ -171,8 +171,8 @@ __global__ __launch_bounds__(1024) void k_ortho_small_factor(
   __syncthreads();
   double trace = 0.0;
   for (int i = 0; i < side; ++i) trace += at[0][i][i];
-  const double norm = sqrt(trace) + c.eps;
-  const double f = norm == 0.0 ? 0.0 : 1.0 / norm;
+  // (zeros stay zeros, however small eps is)
+  const double f = trace == 0.0 ? 0.0 : 1.0 / (sqrt(trace) + c.eps);
   __syncthreads();
   for (int q = threadIdx.x; q < side * side; q += 1024)
     at[0][q / side][q % side] *= f * f;

@@ -78,3 +78,20 @@ def test_a_list_of_loud_and_faint():
     for x, y in zip(xs, M.orthogonalize(xs)):
         assert y.isfinite().all()
         assert torch.equal(M.orthogonalize(x), y)
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-160, 2.3e-308, 5e-324])
+def test_zeros(eps):
+    """However small eps is."""
+    g = torch.ones(300, 200, device="cuda")
+    for shape in ((20, 30), (1, 1), (130, 257), (257, 130)):
+        z = torch.zeros(*shape, device="cuda")
+        one, other = M.orthogonalize([z, g], eps=eps)
+        assert torch.equal(one, z) and other.isfinite().all()
+        faint = torch.zeros(*shape, device="cuda")
+        faint[0, 0] = 1e-45            # the smallest there is
+        y = M.orthogonalize(faint, eps=eps)
+        want = R.orthogonal(torch.ones(1, 1), eps=0.0)
+        assert abs(y[0, 0].item() - want.item()) <= 1e-5
+        y[0, 0] = 0.0
+        assert not y.any()
