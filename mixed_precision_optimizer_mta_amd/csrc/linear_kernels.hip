@@ -520,11 +520,12 @@ __global__ __launch_bounds__(256) void k_linear_info(const LinearArgs l) {
   l.info[q] = x;
 }
 
-// The factor that all of dz shares.
+// The factor that all of dz shares (its own factors' product is exact in 64 bits,
+// where small weights under a large scale do not leave the range of numbers).
 template <int D>
 __device__ __forceinline__ float shared_factor(const LinearArgs &l) {
-  const float s = l.a.d_grad_scale ? *l.a.d_grad_scale : 1.0f;
-  return s * (l.scalars[1] / kRoom<D>);
+  const double s = l.a.d_grad_scale ? *l.a.d_grad_scale : 1.0f;
+  return static_cast<float>(s * l.scalars[1] * (1.0 / kRoom<D>));
 }
 
 // Eight sums of a gradient's row, out.

@@ -101,3 +101,27 @@ def test_an_infinite_weight(dtype, rows):
     assert r.loss == float("inf")
     assert not r.dhidden[on].isfinite().any()
     assert not r.dhidden[d["t"] == -100].any()
+
+
+@pytest.mark.parametrize("dtype", list(R.DTYPES))
+def test_small_weights_under_a_large_scale(dtype):
+    """Weights that are no normal numbers times 2^-14, and a factor that makes
+    up for them: dw as of ordinary ones, to the bit but for the weights' own
+    digits (2^-126 times 0.7 keeps 23 of 24, a rounding of 2^-24 of each)."""
+    d = case(90, 300, 64, dtype, 3)
+    wt = 0.5 + torch.rand(90, generator=torch.Generator().manual_seed(2))
+    wt = wt.cuda()
+    to = torch.empty(300, 64, device="cuda")
+
+    def dw(weights, scale):
+        return M.linear_cross_entropy_grad(
+            d["h"], d["w"], d["t"], weights=weights, grad_scale=torch.tensor(
+                [scale], device="cuda"), out_weight=to).dweight.double()
+
+    want = dw(wt, 1.0)
+    got = dw(wt * 2.0 ** -126, 2.0 ** 126)
+    # dz's own rounding may turn out the other way: half a step of either
+    assert (got - want).norm() <= 4 * (R.half_step(R.DTYPES[dtype]) +
+                                       2.0 ** -23) * want.norm()
+    for tiny, large in ((2.0 ** -120, 2.0 ** 120), (2.0 ** 100, 2.0 ** -100)):
+        assert torch.equal(dw(wt * tiny, large), want)
