@@ -64,6 +64,9 @@ typedef struct {
  * unspecified.  A matrix with a NaN or infinity comes out all NaN and leaves
  * the others alone; one of zeros comes out zero.
  *
+ * Matrices are taken up to forty at a time, those of up to 64 rows or columns
+ * apart, and by 4 GiB of workspace; one such group follows the other.
+ *
  * A matrix of up to 64 rows or columns is computed in float64.  Otherwise X is
  * kept as a float16 value and a second one for what it leaves (22 bits), times a
  * power of two as long as it is far below 1 (|u| far below eps); the
@@ -129,7 +132,10 @@ typedef struct {
  * the six largest of nine products of three bfloat16 values; sums are float32.
  * dz is rounded once to the 16-bit type (float32: to three bfloat16 values)
  * before dh and dw are made of it, scaled so that its largest finite weight is 1
- * (float16: 2^14): neither S nor small weights cost digits. */
+ * (float16: 2^14): neither S nor weights that are all small cost digits.  Float16
+ * has 11 bits down to 2^-28 of the largest weight and none below 2^-39: a row
+ * whose own weight is 1e-6 of the largest has its target's digits, and those of
+ * probabilities of 1 / 50257 to 9%. */
 typedef struct {
   const void *h;              /* [rows, width], rows of ldh elements */
   const void *w;              /* [vocab, width], rows of ldw elements */

@@ -14,8 +14,9 @@
 // gradients take the vocabulary in pieces: the product again, its tiles written
 // as dz in 16 bits, then dh += dz w and the piece of dw = dz^T h, which read dz,
 // w and h as they lie, with k along or across.  Four products instead of the
-// three that kept logits would need: logits in 32 bits for 8192 x 50257 are 1.6
-// GB, whose writing and reading takes as long as the fourth.
+// three that kept logits would need: memory is the reason.  Logits in 32 bits for
+// 8192 x 50257 are 1.6 GB; writing and reading them would take 0.7 ms, the fourth
+// product of 1600 columns 1.3.
 //
 // A float32 call has three bfloat16 planes for each operand and six products.
 //

@@ -31,8 +31,9 @@
 // allows: four of 6400 x 1600 and four of 1600 x 6400 take 2.22 ms for the 1.54
 // TFLOP of a (2, 2, 1) course, and a library product of that size would take 1.25.
 // Small ones are bound by launches of which each waits for the one before: twelve
-// of 768 x 768 take 0.30 ms, 22 launches of 10 to 20 us whose 12 steps along k
-// take 7, what comes before the first and after the last the rest.
+// of 768 x 768 take 0.30 to 0.35 ms in 17 launches, of whose products' 17 to 23 us
+// (under a tracer) 12 steps along k are 7, what comes before the first and after
+// the last the rest.
 #include "gemm_device.h"
 #include "ortho_device.h"
 

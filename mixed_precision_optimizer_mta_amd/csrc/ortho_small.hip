@@ -148,7 +148,7 @@ __global__ __launch_bounds__(256) void k_ortho_small_gram(const OrthoList l,
 // its blocks on and above the diagonal are computed, one or two a wave, and what is
 // above the diagonal is copied below it in blocks on it too: rows are multiplied by
 // rows, as p q^T, and what a rounding has made unlike on the two sides would grow
-// by up to (a + |b|)^2 = 38 a step instead of staying as small as it is.
+// by up to (a + |b|)^2 = 68 a step instead of staying as small as it is.
 __global__ __launch_bounds__(1024) void k_ortho_small_factor(
     const OrthoList l, const OrthoCall c, const OrthoCoefficients co) {
   // R, Q, R Q and F

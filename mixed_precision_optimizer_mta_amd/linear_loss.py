@@ -131,7 +131,9 @@ def linear_cross_entropy_grad(hidden, weight, targets, weights=None,
     times *grad_scale.
 
     A row whose target is ignore_index or whose weight is 0 is not read; its
-    logp is 0 and its gradient 0.  dhidden is a new tensor or `out`; dweight a
+    logp is 0 and its gradient 0.  With float16, rows of unequal weights have the
+    digits that are left beside the largest: what is below 2^-28 of it has fewer.
+    dhidden is a new tensor or `out`; dweight a
     new one or `out_weight` (of any of the three dtypes), overwritten or, with
     accumulate, added to."""
     return _loss(hidden, weight, targets, weights, ignore_index, True, False,
@@ -195,7 +197,7 @@ def linear_cross_entropy(hidden, weight, targets, weights=None,
     weight; the gradients of a scaled loss are scaled before they are rounded.
     Tensors of any strides are taken; a weight of another dtype (a float32
     master under 16-bit hidden states) is cast to hidden's, and its gradient
-    back.  There is no gradient for weights: those that require one are
+    back (linear_cross_entropy_grad writes one of float32).  There is no gradient for weights: those that require one are
     refused."""
     if weights is not None and weights.requires_grad and \
             torch.is_grad_enabled():

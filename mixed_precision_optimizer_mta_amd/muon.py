@@ -2,7 +2,7 @@
 include/mta_matrix.h.
 
 ``orthogonalize`` brings the singular values of a matrix, or of the matrices of
-a list together, near 1 by Newton-Schulz steps; ``muon_update`` is that of
+a list together (up to forty a launch), near 1 by Newton-Schulz steps; ``muon_update`` is that of
 momenta that take their gradients in first (the update of the Muon rule).  An
 MtaOptimizer applies it to the weights of its groups of kind "muon".
 
